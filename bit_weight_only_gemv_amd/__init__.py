@@ -4,7 +4,7 @@ FP16 outlier columns, behind the C ABI of ``include/wq.h``.
 
 ``_lib`` is the ctypes binding of ``libwq.so`` (same names as the C ABI);
 ``layer`` packs a float32 weight matrix with the library's host encoder and
-moves the packed arrays to the GPU.  Nothing here computes on the CPU except
+moves the packed arrays to the GPU; ``kv4`` is the paged 4-bit key/value cache.  Nothing here computes on the CPU except
 the library's own host encoder, and nothing falls back to another
 implementation: calls fail if ``libwq.so`` has not been built.
 """
@@ -18,5 +18,7 @@ from ._lib import (  # noqa: F401
     wq_outlier_add, wq_embed_gather, wq_topk_count, wq_topk_chunks, wq_refine_add,
     wq_refine_topk,
     wq_tiled_bytes, wq_tile_host, wq_gemv_tiled, wq_gemm_tiled, wq_gemv_tiled_refine,
+    WQ_KV4_PAGE, WQ_KV4_MAX_SEQS, WQ_DT_F16, WQ_DT_BF16, wq_kv4_max_runs, wq_kv4_plan,
     wq_read_probe, wq_read_probe_sink_words, wq_read_probe_geom, wq_copy_probe,
 )
+from .kv4 import KV4Cache  # noqa: F401

@@ -32,6 +32,10 @@ WQ_FUSE_OUTLIERS = 1
 WQ_GROUP = 32
 WQ_MAX_K = 65536
 WQ_GEMM_MAX_M = 16
+WQ_KV4_PAGE = 64
+WQ_KV4_MAX_SEQS = 8192
+WQ_DT_F16 = 0
+WQ_DT_BF16 = 1
 
 # Every symbol include/wq.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
@@ -77,6 +81,14 @@ SIGNATURES = {
     "wq_refine_topk_v": (_INT, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     "wq_gemv_tiled_refine_v": (_INT, [_INT, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64,
                                       _I64, _P, _P, _P]),
+    "wq_kv4_max_runs": (_I64, [_I64, _I64]),
+    "wq_kv4_plan": (_INT, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P]),
+    "wq_kv4_append": (_INT, [_P, _INT, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    "wq_kv4_select_workspace": (_I64, [_I64, _I64, _I64]),
+    "wq_kv4_select": (_INT, [_P, _P, _I64, _P, _P, _I64, _P]),
+    "wq_kv4_attention_workspace": (_I64, [_P, _P, _I64, _I64, _I64]),
+    "wq_kv4_attention": (_INT, [_P, _P, _I64, _I64, ctypes.c_float, _I64, _P, _I64, _P, _P, _P,
+                                _I64, _P]),
     "wq_read_probe": (_INT, [_P, _I64, _P, _P]),
     "wq_read_probe_sink_words": (_I64, [_I64]),
     "wq_read_probe_geom": (_INT, [_P, _I64, _P, _INT, _INT, _INT, _P]),
@@ -109,6 +121,19 @@ def variant(**fields) -> Variant:
 
 def _vptr(v):
     return ctypes.addressof(v) if v is not None else None
+
+
+class Kv4Cache(ctypes.Structure):
+    """wq_kv4_cache."""
+    _fields_ = [("data", _P), ("summary", _P), ("n_pages", _I64), ("n_kv_heads", _I64),
+                ("head_dim", _I64)]
+
+
+class Kv4Rows(ctypes.Structure):
+    """wq_kv4_rows."""
+    _fields_ = [("block_table", _P), ("lens", _P), ("cu_rows", _P), ("table_width", _I64),
+                ("n_seqs", _I64), ("n_rows", _I64), ("n_heads", _I64), ("dtype", ctypes.c_int32),
+                ("q", _P), ("q_row_stride", _I64), ("q_head_stride", _I64)]
 
 
 class WQError(RuntimeError):
@@ -409,6 +434,32 @@ def wq_refine_topk(rcodes, rscales, rzeros, N, K, chunk, k, x, y, sel_out=None, 
 def wq_outlier_add(idx, out_w, n_out, N, X, M, K, Y, stream=None):
     _check(load().wq_outlier_add(_dptr(idx) if n_out else None, _dptr(out_w) if n_out else None,
                                  n_out, N, _dptr(X), M, K, _dptr(Y), _stream(stream)))
+
+
+def wq_kv4_max_runs(n_seqs: int, n_rows: int) -> int:
+    n = int(load().wq_kv4_max_runs(n_seqs, n_rows))
+    if n < 0:
+        _check(n)
+    return n
+
+
+def _i32(t, shape, what):
+    """Pointer of a contiguous int32 GPU tensor of the given shape."""
+    if "int32" not in str(t.dtype) or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return _dptr(t)
+
+
+def wq_kv4_plan(lens, cu_rows, block_table, free_pages, new_lens, slots, runs, taken, stream=None):
+    """Sizes from the tensors: lens [B], cu_rows [B + 1], block_table [B, width],
+    free_pages [n_free], new_lens [B], slots [rows], runs [n_runs, 2], taken [1]."""
+    B, width = block_table.shape
+    T, F, n_runs = slots.numel(), free_pages.numel(), runs.shape[0]
+    _check(load().wq_kv4_plan(
+        _i32(lens, (B,), "lens"), _i32(cu_rows, (B + 1,), "cu_rows"), B, T,
+        _i32(block_table, (B, width), "block_table"), width, _i32(free_pages, (F,), "free_pages"),
+        F, _i32(new_lens, (B,), "new_lens"), _i32(slots, (T,), "slots"),
+        _i32(runs, (n_runs, 2), "runs"), n_runs, _i32(taken, (1,), "taken"), _stream(stream)))
 
 
 def wq_read_probe_sink_words(nbytes: int) -> int:

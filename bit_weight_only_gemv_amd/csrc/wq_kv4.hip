@@ -1,0 +1,495 @@
+// The paged 4-bit key/value cache (wq.h, "4-bit key/value cache"): where new
+// tokens go, writing them, and the choice of pages for sparse attention.
+// Attention itself is in wq_kv4_attn.hip.
+
+#include "wq_common.cuh"
+#include "wq_device.h"
+#include "wq_kv4.cuh"
+
+namespace wqd {
+
+// ------------------------------------------------------------------- plan
+// Block table, slots and runs from request lengths.  Every workgroup scans the
+// sequences for itself (page needs and run counts, exclusive sums in LDS), so
+// one launch without any exchange between workgroups does it all: a scan of
+// 1000 sequences is 4 loads a thread, less than a second launch.  Table
+// entries, slots and runs are then found by binary search in those sums.
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxLen = 1 << 30;
+constexpr int kMaxPage = (1 << 25) - 1;   // slots stay below 2^31
+
+__device__ __forceinline__ int upper_index(const int* sums, int n, int x) {
+  // the last b in [0, n) with sums[b] <= x, for rising sums and sums[0] <= x
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (sums[m] <= x) lo = m; else hi = m;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ cu, int B, int T,
+            int32_t* __restrict__ table, int64_t width, const int32_t* __restrict__ free_pages,
+            int n_free, int32_t* __restrict__ new_lens, int32_t* __restrict__ slots,
+            int32_t* __restrict__ runs, int n_runs, int32_t* __restrict__ taken) {
+  extern __shared__ int s_plan[];
+  int* s_len = s_plan;                 // [B]
+  int* s_cu = s_len + B;               // [B + 1]
+  int* s_need = s_cu + B + 1;          // [B + 1] exclusive sums of pages needed
+  int* s_runs = s_need + B + 1;        // [B + 1] exclusive sums of runs
+  __shared__ int s_wave[2][kPlanThreads / kWave];
+  const int tid = threadIdx.x;
+  const int per = (B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  int need = 0, nruns = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = min(max(lens[b], 0), kMaxLen);
+    const int c = cu[b], n = min(max(cu[b + 1] - c, 0), T);
+    s_len[b] = len;
+    s_cu[b] = c;
+    if (b == B - 1) s_cu[B] = cu[B];
+    s_need[b] = need;
+    s_runs[b] = nruns;
+    need += (len + n + 63) / 64 - (len + 63) / 64;
+    nruns += n > 0 ? (len + n - 1) / 64 - len / 64 + 1 : 0;
+  }
+  int ni = need, ri = nruns;           // inclusive sums over the wave's lanes
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int a = __shfl_up(ni, d), b = __shfl_up(ri, d);
+    if ((tid & 63) >= d) { ni += a; ri += b; }
+  }
+  if ((tid & 63) == 63) { s_wave[0][tid >> 6] = ni; s_wave[1][tid >> 6] = ri; }
+  __syncthreads();
+  int nbase = ni - need, rbase = ri - nruns;
+  for (int w = 0; w < tid >> 6; ++w) { nbase += s_wave[0][w]; rbase += s_wave[1][w]; }
+  for (int b = b0; b < b1; ++b) { s_need[b] += nbase; s_runs[b] += rbase; }
+  if (tid == kPlanThreads - 1) { s_need[B] = nbase + need; s_runs[B] = rbase + nruns; }
+  __syncthreads();
+  const int total = s_need[B], total_runs = s_runs[B];
+  const int g0 = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+
+  if (g0 == 0) taken[0] = total;
+  for (int b = g0; b < B; b += step) new_lens[b] = s_len[b] + max(s_cu[b + 1] - s_cu[b], 0);
+  for (int i = g0; i < total; i += step) {
+    const int b = upper_index(s_need, B, i);
+    const int p = (s_len[b] + 63) / 64 + i - s_need[b];
+    if (p < width) table[b * width + p] = i < n_free ? free_pages[i] : -1;
+  }
+  for (int row = g0; row < T; row += step) {
+    int slot = -1;
+    const int b = upper_index(s_cu, B, row);
+    const int off = row - s_cu[b];
+    if (off >= 0 && off < s_cu[b + 1] - s_cu[b]) {
+      const int pos = s_len[b] + off, p = pos / 64;
+      const int fresh = p - (s_len[b] + 63) / 64;   // pages this call adds start at 0
+      int page = -1;
+      if (p < width) {
+        if (fresh < 0) page = table[b * width + p];
+        else if (s_need[b] + fresh < n_free) page = free_pages[s_need[b] + fresh];
+      }
+      if (page >= 0 && page <= kMaxPage) slot = page * 64 + (pos & 63);
+    }
+    slots[row] = slot;
+  }
+  for (int j = g0; j < n_runs; j += step) {
+    int first = -1, count = 0;
+    if (j < total_runs) {
+      const int b = upper_index(s_runs, B, j);
+      const int len = s_len[b], end = len + s_cu[b + 1] - s_cu[b];
+      const int page = len / 64 + j - s_runs[b];
+      const int lo = max(page * 64, len), hi = min(page * 64 + 64, end);
+      first = s_cu[b] + lo - len;
+      count = hi - lo;
+    }
+    reinterpret_cast<int2*>(runs)[j] = make_int2(first, count);
+  }
+}
+
+// ----------------------------------------------------------------- append
+// One workgroup per (run, head, keys or values).  A thread takes 8 channels of
+// a token, 4 neighbouring lanes one group of 32.
+constexpr int kAppendThreads = 256;
+
+template <int DT>
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const u4v v = *reinterpret_cast<const u4v*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint16_t b = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    x[i] = to_float<DT>(b);
+    x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -65504.f), 65504.f);
+  }
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
+              const uint16_t* __restrict__ v, int64_t v_row, int64_t v_head, int T,
+              const int32_t* __restrict__ slots, const int2* __restrict__ runs,
+              uint8_t* __restrict__ data, uint16_t* __restrict__ summary, int64_t n_pages,
+              int heads) {
+  constexpr int G = D / 32, W = G < 4 ? G : 4, O = D / 8, TS = kAppendThreads / O;
+  const bool values = blockIdx.x & 1;
+  const int head = (int)((blockIdx.x >> 1) % (unsigned)heads);
+  const int run = (int)((blockIdx.x >> 1) / (unsigned)heads);
+  const int2 rc = runs[run];
+  if (rc.x < 0 || rc.y <= 0 || rc.y > 64 || rc.x > T - rc.y) return;
+  const int slot = slots[rc.x];
+  const int o = slot & 63;
+  if (slot < 0 || (slot >> 6) >= n_pages || o + rc.y > 64) return;
+  if (slots[rc.x + rc.y - 1] != slot + rc.y - 1) return;
+  const int64_t ph = (int64_t)(slot >> 6) * heads + head;
+  uint8_t* const page = data + ph * (80 * D);
+  const uint16_t* const src =
+      values ? v + rc.x * v_row + head * v_head : k + rc.x * k_row + head * k_head;
+  const int64_t row = values ? v_row : k_row;
+
+  __shared__ uint8_t s_code[64 * D];          // values: codes by token and channel
+  __shared__ float s_min[TS][D], s_max[TS][D];
+  const int oc = threadIdx.x % O, g = oc >> 2, r8 = oc & 3;
+  float lo8[8], hi8[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) { lo8[i] = INFINITY; hi8[i] = -INFINITY; }
+  for (int n = threadIdx.x / O; n < rc.y; n += TS) {
+    const int t = o + n, tt = t & 31, u = tt >> 4, r = (tt >> 2) & 3, e = 4 * u + (tt & 3);
+    float x[8];
+    load8<DT>(src + n * row + oc * 8, x);
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      lo8[i] = fminf(lo8[i], x[i]);
+      hi8[i] = fmaxf(hi8[i], x[i]);
+    }
+    lo = fminf(lo, __shfl_xor(lo, 1)); lo = fminf(lo, __shfl_xor(lo, 2));
+    hi = fmaxf(hi, __shfl_xor(hi, 1)); hi = fmaxf(hi, __shfl_xor(hi, 2));
+    const uint16_t zb = f2h(h2f(f2h(lo)) + 0.0f), sb = f2h((hi - lo) / 15.0f);
+    const float z = h2f(zb), s = h2f(sb);
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i] = s > 0.f ? (int)fminf(fmaxf(rintf((x[i] - z) / s), 0.f), 15.f) : 0;
+    uint8_t* const tile = page + (t >> 5) * (40 * D);
+    if (!values) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= (uint32_t)q[i] << (4 * ((i >> 1) + 4 * (i & 1)));
+      *reinterpret_cast<uint32_t*>(tile + u * (8 * D) + (g / W) * (256 * W) +
+                                   ((r8 * 16 + (tt & 15)) * W + g % W) * 4) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_code[t * D + oc * 8 + i] = (uint8_t)q[i];
+    }
+    uint16_t* const meta = reinterpret_cast<uint16_t*>(tile + (values ? 36 : 32) * D);
+    if (r8 == 0) meta[r * 8 * G + g * 8 + e] = sb;
+    if (r8 == 1) meta[D + (values ? r * 8 * G + g * 8 + e : tt * G + g)] = zb;
+  }
+  if (!values) {
+    if (summary == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s_min[threadIdx.x / O][oc * 8 + i] = lo8[i];
+      s_max[threadIdx.x / O][oc * 8 + i] = hi8[i];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * D; c += kAppendThreads) {
+      const bool mx = c >= D;
+      const int d = c % D;
+      uint16_t* const at = summary + ph * (2 * D) + c;
+      float m = o > 0 ? h2f(*at) : (mx ? -INFINITY : INFINITY);
+      for (int j = 0; j < TS; ++j) m = mx ? fmaxf(m, s_max[j][d]) : fminf(m, s_min[j][d]);
+      *at = f2h(m);
+    }
+    return;
+  }
+  __syncthreads();
+  // words of 8 tokens: tile, r and channel; bits of other tokens stay
+  for (int c = threadIdx.x; c < 8 * D; c += kAppendThreads) {
+    const int d = c % D, r = (c / D) & 3, tile = c / (4 * D);
+    uint32_t w = 0, mask = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = tile * 32 + (e >> 2) * 16 + r * 4 + (e & 3);
+      if (t >= o && t < o + rc.y) {
+        const int bit = 4 * ((e >> 1) + 4 * (e & 1));
+        w |= (uint32_t)s_code[t * D + d] << bit;
+        mask |= 15u << bit;
+      }
+    }
+    if (mask == 0) continue;
+    uint32_t* const at = reinterpret_cast<uint32_t*>(page + tile * (40 * D) + 16 * D +
+                                                     (d >> 6) * 1024 +
+                                                     (r * 16 + (d & 15)) * 16 + ((d >> 4) & 3) * 4);
+    *at = mask == 0xFFFFFFFFu ? w : (*at & ~mask) | w;
+  }
+}
+
+// ----------------------------------------------------------------- select
+// Scores (float32 in the workspace, [row][head][page]), then the n_sel highest.
+constexpr int kScoreThreads = 64;
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kScoreThreads)
+score_kernel(KvRows a, const uint16_t* __restrict__ summary, int64_t n_pages, int kv_heads,
+             float* __restrict__ scores) {
+  __shared__ double s_q[D];
+  const int row = blockIdx.y, head = blockIdx.z;
+  const SeqRow sr = find_row(a, row);
+  const int pages = sr.pos >= 0 ? (int)min((int64_t)(sr.pos / 64 + 1), a.width) : 0;
+  const int p = blockIdx.x * kScoreThreads + threadIdx.x;
+  if ((int)(blockIdx.x * kScoreThreads) >= pages) return;
+  const int R = a.heads / kv_heads;
+  const int page = p < pages ? a.table[sr.b * a.width + p] : -1;
+  const bool ok = page >= 0 && page < n_pages;
+  const uint16_t* sm = summary + ((int64_t)(ok ? page : 0) * kv_heads + head) * (2 * D);
+  double best = -INFINITY;
+  for (int h = 0; h < R; ++h) {
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += kScoreThreads)
+      s_q[d] = (double)to_float<DT>(a.q[row * a.q_row + (head * R + h) * a.q_head + d]);
+    __syncthreads();
+    double s = 0;
+    for (int d = 0; d < D; ++d)
+      s += s_q[d] * (double)h2f(s_q[d] > 0 ? sm[D + d] : sm[d]);
+    best = s > best ? s : best;
+  }
+  if (p < pages)
+    scores[((int64_t)row * kv_heads + head) * a.width + p] =
+        p == 0 || p == pages - 1 ? INFINITY : (ok ? (float)best : -INFINITY);
+}
+
+// Order of a float32 score as an unsigned key (NaN lowest).
+__device__ __forceinline__ uint32_t score_key(float f) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, f);
+  if (f != f) return 0;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+constexpr int kPickThreads = 256;
+
+__global__ void __launch_bounds__(kPickThreads)
+pick_kernel(KvRows a, int kv_heads, const float* __restrict__ scores, int n_sel,
+            int32_t* __restrict__ sel) {
+  __shared__ uint32_t s_hist[256];
+  __shared__ uint32_t s_prefix, s_rank;
+  __shared__ int s_count[2][kPickThreads];
+  const int row = blockIdx.x / kv_heads;
+  const SeqRow sr = find_row(a, row);
+  const int pages = sr.pos >= 0 ? (int)min((int64_t)(sr.pos / 64 + 1), a.width) : 0;
+  const float* sc = scores + (int64_t)blockIdx.x * a.width;
+  int32_t* out = sel + (int64_t)blockIdx.x * n_sel;
+  const int n = min(n_sel, pages);
+  for (int j = n + threadIdx.x; j < n_sel; j += kPickThreads) out[j] = -1;
+  if (n == pages) {
+    for (int j = threadIdx.x; j < n; j += kPickThreads) out[j] = j;
+    return;
+  }
+  // the n-th highest key, 8 bits at a time
+  if (threadIdx.x == 0) { s_prefix = 0; s_rank = n; }
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    s_hist[threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t prefix = s_prefix;
+    for (int p = threadIdx.x; p < pages; p += kPickThreads) {
+      const uint32_t key = score_key(sc[p]);
+      if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&s_hist[(key >> shift) & 255], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t above = 0;
+      int bin = 255;
+      while (above + s_hist[bin] < s_rank) above += s_hist[bin--];
+      s_rank -= above;
+      s_prefix = (prefix << 8) | (uint32_t)bin;
+    }
+    __syncthreads();
+  }
+  const uint32_t cut = s_prefix;
+  const int ties = (int)s_rank;        // of the keys equal to the cut, the first ones
+  // each thread a stretch of pages: counts, sums over threads, then the picks in order
+  const int per = (pages + kPickThreads - 1) / kPickThreads;
+  const int p0 = min((int)threadIdx.x * per, pages), p1 = min(p0 + per, pages);
+  int above = 0, equal = 0;
+  for (int p = p0; p < p1; ++p) {
+    const uint32_t key = score_key(sc[p]);
+    above += key > cut;
+    equal += key == cut;
+  }
+  s_count[0][threadIdx.x] = above;
+  s_count[1][threadIdx.x] = equal;
+  __syncthreads();
+  int at = 0, eq = 0;
+  for (int j = 0; j < (int)threadIdx.x; ++j) { at += s_count[0][j]; eq += s_count[1][j]; }
+  at += min(eq, ties);
+  for (int p = p0; p < p1; ++p) {
+    const uint32_t key = score_key(sc[p]);
+    if (key > cut) out[at++] = p;
+    else if (key == cut && eq++ < ties) out[at++] = p;
+  }
+}
+
+// -------------------------------------------------------------- host side
+
+int kv4_check_cache(const wq_kv4_cache* c, const char* who) {
+  if (c == nullptr || c->data == nullptr) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL cache", who);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: head_dim must be 64, 128 or 256, got %lld", who,
+                    (long long)c->head_dim);
+  if (c->n_pages < 1 || c->n_pages > kMaxPage + 1 || c->n_kv_heads < 1 || c->n_kv_heads > 65535)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad cache shape (%lld pages, %lld heads)", who,
+                    (long long)c->n_pages, (long long)c->n_kv_heads);
+  if (!aligned16(c->data) || !aligned16(c->summary))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: cache pointers must be 16-byte aligned", who);
+  return WQ_OK;
+}
+
+int kv4_check_rows(const wq_kv4_cache* c, const wq_kv4_rows* a, const char* who) {
+  if (a == nullptr) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL rows", who);
+  if (a->dtype != WQ_DT_F16 && a->dtype != WQ_DT_BF16)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: dtype must be WQ_DT_F16 or WQ_DT_BF16", who);
+  if (a->n_seqs < 0 || a->n_rows < 0 || a->n_rows > (1 << 24) || a->n_seqs > (1 << 24) ||
+      a->n_heads < 1 || a->n_heads > 65535 || a->table_width < 1 || a->table_width > (1 << 24))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
+  if (a->n_heads % c->n_kv_heads)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: %lld heads do not divide into %lld key/value heads",
+                    who, (long long)a->n_heads, (long long)c->n_kv_heads);
+  if (a->n_rows == 0 || a->n_seqs == 0) return WQ_OK;
+  if (!a->block_table || !a->lens || !a->cu_rows || !a->q)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned4(a->block_table) || !aligned4(a->lens) || !aligned4(a->cu_rows) ||
+      !aligned16(a->q))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
+  if (a->q_row_stride % 8 || a->q_head_stride % 8 || a->q_row_stride < 0 || a->q_head_stride < 0)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: q strides must be multiples of 8 elements", who);
+  return WQ_OK;
+}
+
+KvRows kv4_rows(const wq_kv4_rows* a) {
+  return KvRows{a->block_table, a->lens,          a->cu_rows,       a->table_width,
+                (int)a->n_seqs, (int)a->n_rows,   (int)a->n_heads,  a->q,
+                a->q_row_stride, a->q_head_stride};
+}
+
+}  // namespace wqd
+
+using namespace wqd;
+
+extern "C" int64_t wq_kv4_max_runs(int64_t n_seqs, int64_t n_rows) {
+  if (n_seqs < 0 || n_rows < 0 || n_rows > (1 << 24) || n_seqs > WQ_KV4_MAX_SEQS)
+    return wq::fail(WQ_ERR_INVALID_ARG, "wq_kv4_max_runs: bad sizes");
+  wq::ok();
+  const int64_t n = n_rows / WQ_KV4_PAGE + 2 * n_seqs;
+  return n < n_rows ? n : n_rows;
+}
+
+extern "C" int wq_kv4_plan(const int32_t* lens, const int32_t* cu_rows, int64_t n_seqs,
+                           int64_t n_rows, int32_t* block_table, int64_t table_width,
+                           const int32_t* free_pages, int64_t n_free, int32_t* new_lens,
+                           int32_t* slots, int32_t* runs, int64_t n_runs, int32_t* taken,
+                           void* stream) {
+  const char* who = "wq_kv4_plan";
+  if (n_seqs > WQ_KV4_MAX_SEQS)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: at most %d sequences", who, WQ_KV4_MAX_SEQS);
+  if (n_seqs < 0 || n_rows < 0 || n_rows > (1 << 24) || table_width < 1 ||
+      table_width > (1 << 24) || n_free < 0 || n_free > kMaxPage + 1)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
+  if (n_seqs == 0) return wq::ok();
+  const int64_t want = wq_kv4_max_runs(n_seqs, n_rows);
+  if (n_runs < want)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: runs holds %lld, %lld needed", who, (long long)n_runs,
+                    (long long)want);
+  if (n_runs > (1 << 25)) return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
+  if (!lens || !cu_rows || !block_table || !new_lens || !taken || (n_rows && !slots) ||
+      (n_runs && !runs) || (n_free && !free_pages))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned4(lens) || !aligned4(cu_rows) || !aligned4(block_table) || !aligned4(new_lens) ||
+      !aligned4(taken) || !aligned4(slots) || ((uintptr_t)runs & 7u) || !aligned4(free_pages))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
+  const size_t lds = (size_t)(4 * n_seqs + 3) * 4;
+  if (!allow_lds((const void*)plan_kernel, lds))
+    return wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
+  int64_t most = n_rows > n_runs ? n_rows : n_runs;
+  if (n_seqs > most) most = n_seqs;
+  int64_t wgs = (most + kPlanThreads - 1) / kPlanThreads;
+  if (wgs > 256) wgs = 256;
+  plan_kernel<<<dim3((unsigned)wgs), kPlanThreads, lds, (hipStream_t)stream>>>(
+      lens, cu_rows, (int)n_seqs, (int)n_rows, block_table, table_width, free_pages, (int)n_free,
+      new_lens, slots, runs, (int)n_runs, taken);
+  return check_launch(who);
+}
+
+extern "C" int wq_kv4_append(const wq_kv4_cache* cache, int dtype, const uint16_t* k,
+                             int64_t k_row_stride, int64_t k_head_stride, const uint16_t* v,
+                             int64_t v_row_stride, int64_t v_head_stride, int64_t n_rows,
+                             const int32_t* slots, const int32_t* runs, int64_t n_runs,
+                             void* stream) {
+  const char* who = "wq_kv4_append";
+  if (int e = kv4_check_cache(cache, who)) return e;
+  if (dtype != WQ_DT_F16 && dtype != WQ_DT_BF16)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: dtype must be WQ_DT_F16 or WQ_DT_BF16", who);
+  if (n_rows < 0 || n_rows > (1 << 24) || n_runs < 0 ||
+      n_runs * cache->n_kv_heads * 2 > 0x7FFFFFFFll)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
+  if (n_rows == 0 || n_runs == 0) return wq::ok();
+  if (!k || !v || !slots || !runs) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(k) || !aligned16(v) || !aligned4(slots) || ((uintptr_t)runs & 7u))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
+  if (k_row_stride % 8 || k_head_stride % 8 || v_row_stride % 8 || v_head_stride % 8 ||
+      k_row_stride < 0 || k_head_stride < 0 || v_row_stride < 0 || v_head_stride < 0)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements", who);
+  const dim3 grid((unsigned)(n_runs * cache->n_kv_heads * 2));
+  kv4_dispatch(dtype, cache->head_dim, [&](auto dt, auto d) {
+    append_kernel<decltype(dt)::value, decltype(d)::value>
+        <<<grid, kAppendThreads, 0, (hipStream_t)stream>>>(
+            k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, (int)n_rows, slots,
+            reinterpret_cast<const int2*>(runs), cache->data, cache->summary, cache->n_pages,
+            (int)cache->n_kv_heads);
+  });
+  return check_launch(who);
+}
+
+extern "C" int64_t wq_kv4_select_workspace(int64_t n_rows, int64_t n_kv_heads,
+                                           int64_t table_width) {
+  if (n_rows < 0 || n_rows > (1 << 24) || n_kv_heads < 1 || n_kv_heads > 65535 ||
+      table_width < 1 || table_width > (1 << 24))
+    return wq::fail(WQ_ERR_INVALID_ARG, "wq_kv4_select_workspace: bad sizes");
+  wq::ok();
+  return (n_rows * n_kv_heads * table_width * 4 + 15) / 16 * 16;
+}
+
+extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t n_sel,
+                             int32_t* sel, void* workspace, int64_t workspace_bytes,
+                             void* stream) {
+  const char* who = "wq_kv4_select";
+  if (int e = kv4_check_cache(cache, who)) return e;
+  if (int e = kv4_check_rows(cache, rows, who)) return e;
+  if (cache->summary == nullptr)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: the cache has no summary", who);
+  if (n_sel < 2 || n_sel > (1 << 20))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: n_sel must be at least 2 (the first and last page)", who);
+  if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
+  const int64_t need = wq_kv4_select_workspace(rows->n_rows, cache->n_kv_heads, rows->table_width);
+  if (!sel || !workspace) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (workspace_bytes < need)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                    (long long)workspace_bytes, (long long)need);
+  if (!aligned4(sel) || !aligned16(workspace))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
+  if (rows->n_rows > 65535 || rows->n_rows * cache->n_kv_heads > 0x7FFFFFFFll)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: at most 65535 rows", who);
+  const KvRows a = kv4_rows(rows);
+  float* scores = static_cast<float*>(workspace);
+  const dim3 grid((unsigned)((rows->table_width + kScoreThreads - 1) / kScoreThreads),
+                  (unsigned)rows->n_rows, (unsigned)cache->n_kv_heads);
+  kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
+    score_kernel<decltype(dt)::value, decltype(d)::value>
+        <<<grid, kScoreThreads, 0, (hipStream_t)stream>>>(a, cache->summary, cache->n_pages,
+                                                          (int)cache->n_kv_heads, scores);
+  });
+  pick_kernel<<<dim3((unsigned)(rows->n_rows * cache->n_kv_heads)), kPickThreads, 0,
+                (hipStream_t)stream>>>(a, (int)cache->n_kv_heads, scores, (int)n_sel, sel);
+  return check_launch(who);
+}

@@ -364,6 +364,134 @@ int wq_gemv_tiled_refine(int fmt, const uint8_t* tiled, int64_t N, int64_t K,
                          const uint8_t* rcodes, const uint16_t* rscales, const uint16_t* rzeros,
                          int64_t chunk, int64_t k, int32_t* sel_out, void* stream);
 
+/* ------------------------------------------------- 4-bit key/value cache
+ * Keys and values of past tokens in 4 bits, in groups of 32 channels (SPECTRA
+ * section 4.5 names a 4-bit group-32 cache; the layout is this library's own),
+ * kept in pages that block tables name, and attention over it: over all cached
+ * tokens, or over the pages that a cheap bound selects for each query row.
+ *
+ * Format: a value w of a group of 32 consecutive channels of one token and head
+ * stands as S q + Z with FP16 S and Z and q in 0..15 (5 bits per value), made in
+ * float32 with round-half-to-even from inputs clamped to +-65504 (NaN as 0):
+ *   Z = FP16(min), S = FP16((max - min) / 15), q = clamp(rint((w - Z) / S), 0, 15)
+ * (S == 0: q = 0).  So a cache that was written always holds finite values.
+ *
+ * Layout: data [n_pages][n_kv_heads][80 D] bytes, D = head_dim = 64, 128 or 256,
+ * G = D / 32.  A page holds WQ_KV4_PAGE = 64 tokens: two tiles of 32 tokens, 40 D
+ * bytes each, with the sections
+ *   key codes 16 D | value codes 16 D | key S 2 D | key Z 2 D | value S 2 D | value Z 2 D
+ * Token t of a tile is t = 16 u + 4 r + i (u < 2, r < 4, i < 4), w = min(4, G),
+ * and slot e (0..7) of a 32-bit word is its nibble (e >> 1) + 4 (e & 1):
+ *   key codes    word [u][g / w][rc][t % 16][g % w], slot e = channel 32 g + 8 rc + e
+ *   value codes  word [d / 64][r][d % 16][(d / 16) % 4], slot e = 4 u + i, channel d
+ *   key S, value S, value Z   FP16 [r][g][e], e = 4 u + i;   key Z   FP16 [t][g]
+ * A word's slots are then the 8 consecutive k of a matrix-core operand after one
+ * mask each (FP16 subnormals), and a wave's load of a section is contiguous.
+ *
+ * summary: FP16 [n_pages][n_kv_heads][2][D], the minimum (0) and maximum (1) of
+ * every key channel over the page's tokens (before quantization, rounded to
+ * FP16); NULL where page selection is not used.
+ *
+ * Page numbers and slots are device data and are not checked on the host: a
+ * page outside [0, n_pages) holds no tokens (attention skips them, append does
+ * not write).  dtype is the type of q, k, v and out.  The int32 and float32
+ * arrays of these calls need the alignment of their elements only (runs: of a
+ * pair), so that they may be parts of longer ones. */
+
+#define WQ_KV4_PAGE 64
+#define WQ_KV4_MAX_SEQS 8192 /* sequences of one wq_kv4_plan call */
+
+#define WQ_DT_F16 0
+#define WQ_DT_BF16 1
+
+typedef struct wq_kv4_cache {
+  uint8_t* data;
+  uint16_t* summary;
+  int64_t n_pages, n_kv_heads, head_dim;
+} wq_kv4_cache;
+
+/* Query rows and the cached sequences they belong to.  Rows cu_rows[b] ..
+ * cu_rows[b + 1] - 1 are the last ones of sequence b (cu_rows int32 [n_seqs + 1],
+ * rising from 0 to n_rows): row i of its n_b rows has position
+ * lens[b] - n_b + i, and sees the cached tokens 0 .. its position (lens int32,
+ * cached tokens with these rows' own).  block_table int32 [n_seqs][table_width]:
+ * page p of sequence b holds its tokens 64 p .. 64 p + 63.
+ * q: n_rows x n_heads x D, strides in elements (channels are consecutive;
+ * strides are multiples of 8).  n_heads is a multiple of n_kv_heads; head h reads
+ * key/value head h / (n_heads / n_kv_heads). */
+typedef struct wq_kv4_rows {
+  const int32_t* block_table;
+  const int32_t* lens;
+  const int32_t* cu_rows;
+  int64_t table_width, n_seqs, n_rows, n_heads;
+  int32_t dtype;
+  const uint16_t* q;
+  int64_t q_row_stride, q_head_stride;
+} wq_kv4_rows;
+
+/* Runs that wq_kv4_plan can make of n_rows new tokens of n_seqs sequences:
+ * min(n_rows, n_rows / 64 + 2 n_seqs).  Negative WQ_ERR_* on bad sizes. */
+int64_t wq_kv4_max_runs(int64_t n_seqs, int64_t n_rows);
+
+/* Where new tokens go.  Sequence b holds lens[b] tokens and gets
+ * n_b = cu_rows[b + 1] - cu_rows[b] more:
+ *   block_table  its pages ceil(lens / 64) .. ceil((lens + n_b) / 64) - 1 get the
+ *                next entries of free_pages, sequences in order (-1 where
+ *                free_pages has no more; entries past table_width are not written)
+ *   new_lens[b]  lens[b] + n_b
+ *   slots[row]   page * 64 + offset of each new token (-1 where it has no page)
+ *   runs[j]      {first row, count}: the rows that share a page, in row order,
+ *                n_runs = wq_kv4_max_runs(...) of them; unused ones are {-1, 0}
+ *   taken[0]     pages needed; more than n_free means that some were missing
+ * lens is only read, so a call may be repeated. */
+int wq_kv4_plan(const int32_t* lens, const int32_t* cu_rows, int64_t n_seqs, int64_t n_rows,
+                int32_t* block_table, int64_t table_width, const int32_t* free_pages,
+                int64_t n_free, int32_t* new_lens, int32_t* slots, int32_t* runs, int64_t n_runs,
+                int32_t* taken, void* stream);
+
+/* Quantizes new keys and values (n_rows x n_kv_heads x D, strides in elements,
+ * multiples of 8) into their slots, and keeps the summary (where there is one): a run
+ * that starts at its page's first token begins the page's summary, others extend
+ * it.  Only these tokens' bits are written.  The rows of a run have consecutive
+ * slots inside one page, and no two runs share a page.  A run whose first and
+ * last slot are not so, or are outside the cache, is skipped.
+ * Two calls that write the same page must not run at the same time. */
+int wq_kv4_append(const wq_kv4_cache* cache, int dtype, const uint16_t* k, int64_t k_row_stride,
+                  int64_t k_head_stride, const uint16_t* v, int64_t v_row_stride,
+                  int64_t v_head_stride, int64_t n_rows, const int32_t* slots,
+                  const int32_t* runs, int64_t n_runs, void* stream);
+
+/* Pages for sparse attention.  For each row and key/value head, of the pages
+ * that hold tokens up to the row's position, the n_sel of highest
+ *   max over the group's heads h of  sum_d max(q[h][d] min[d], q[h][d] max[d])
+ * (an upper bound of the page's logits), the first and the last page always.
+ * Sums are made in 64 bits and rounded once to float32; ties go to the lower
+ * page, NaN counts as lowest.  sel int32 [n_rows][n_kv_heads][n_sel]: page
+ * positions in the block table, rising, -1 where there are fewer.
+ * workspace: wq_kv4_select_workspace bytes, 16-byte aligned. */
+int64_t wq_kv4_select_workspace(int64_t n_rows, int64_t n_kv_heads, int64_t table_width);
+int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t n_sel, int32_t* sel,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Attention of the rows over the cache:
+ *   out[row][h] = sum_t p_t v_t,  p = softmax over t of scale * (q . k_t),
+ * over the tokens t that the row sees: up to its position, with window > 0 only
+ * the last `window` of them, with sel != NULL (as wq_kv4_select makes it) only those
+ * in the row's pages.  A row that sees none gives zeros.  out is n_rows x
+ * n_heads x D, contiguous; lse float32 [n_rows][n_heads] (NULL if not wanted)
+ * receives log(sum_t exp(logit)), -inf where a row sees none.  Logits, softmax and
+ * sums are held in float32; out is rounded once.
+ * max_rows and max_len are the largest n_b and lens the caller expects: they
+ * choose how the work is split, and results hold for others as well.
+ * workspace: wq_kv4_attention_workspace bytes for the same arguments, 16-byte
+ * aligned (NULL where that is 0).  out must not overlap q. */
+int64_t wq_kv4_attention_workspace(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
+                                   int64_t max_rows, int64_t max_len, int64_t n_sel);
+int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t max_rows,
+                     int64_t max_len, float scale, int64_t window, const int32_t* sel,
+                     int64_t n_sel, uint16_t* out, float* lse, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------ kernel-variant selection
  * Not part of the method: for tests and measurements that run a call on each
  * of the kernels the library could choose for it.  Each *_v entry point is

@@ -2,7 +2,8 @@
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` leg of
 ``bench.py`` may import this package.  It shares no code with the HIP library
-and the library never imports it.  See :mod:`oracle.wq_oracle` for the
+and the library never imports it.  See :mod:`oracle.wq_oracle`
+(and :mod:`oracle.kv4_oracle` for the 4-bit key/value cache) for the
 definitions, their sources on the pages, and the readings taken where the
 pages are silent.
 

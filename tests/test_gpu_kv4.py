@@ -1,0 +1,511 @@
+"""4-bit key/value cache on the GPU against the oracle (64 bits)."""
+
+import sys
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import bit_weight_only_gemv_amd as B  # noqa: E402
+from oracle import kv4_oracle as K4  # noqa: E402
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def say(*a):
+    print(*a, flush=True, file=sys.stderr)
+
+
+def ints(v):
+    return torch.tensor(np.ascontiguousarray(v), dtype=torch.int32, device="cuda")
+
+
+def host(t):
+    """GPU tensor as numpy (float64 for floating types)."""
+    return t.detach().cpu().double().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def f32(t):
+    return t.detach().cpu().float().numpy()
+
+
+class Made:
+    """Sequences in a cache: pages shuffled, everything past a sequence's end and
+    every page in no table filled with 0xFF bytes (NaN scales and offsets)."""
+
+    def __init__(self, lens, H, D, seed=0, spread=1.0, extra=3, width=None, v_scale=0.7):
+        rng = np.random.default_rng(seed)
+        self.lens = np.asarray(lens)
+        need = -(-self.lens // 64)
+        width = width or max(1, int(need.max()))
+        self.n_pages = int(need.sum()) + extra
+        order = rng.permutation(self.n_pages)
+        self.table = np.full((len(lens), width), -1, np.int64)
+        self.data = np.full((self.n_pages, H, 80 * D), 0xFF, np.uint8)
+        self.summary = np.full((self.n_pages, H, 2, D), np.nan, np.float16)
+        at = 0
+        for b, n in enumerate(self.lens):
+            self.table[b, :need[b]] = order[at:at + need[b]]
+            at += need[b]
+            if n:
+                k = spread * (rng.standard_normal((n, H, D)) + 2 * rng.standard_normal((1, H, D)))
+                v = v_scale * rng.standard_normal((n, H, D))
+                slots = self.table[b, np.arange(n) // 64] * 64 + np.arange(n) % 64
+                self._append(k.astype(np.float16), v.astype(np.float16), slots)
+
+    def _append(self, k, v, slots):
+        K4.append(self.data, self.summary, k, v, slots)
+
+    def gpu(self):
+        self.d, self.s = torch.from_numpy(self.data).cuda(), torch.from_numpy(self.summary).cuda()
+        return B.KV4Cache(self.d, self.s)
+
+
+def check_attention(out, lse, made, q, cu, scale, window=0, sel=None, label=""):
+    """|out - ref| <= half a step of the type, and what float32 logits and sums and
+    the FP16 probabilities can lose.  A logit sums D products whose absolute sum
+    is `top`, in float32 with fewer than 64 roundings: 64 2^-24 top.  A
+    probability is off by that, once in itself and once in the sum, by the
+    exponential's and the sums' roundings (fewer than 64: 2^-17), and for BF16
+    outputs by one FP16 rounding (2^-11)."""
+    ref, lse_ref, size, top = K4.attention(made.data, f32(q), made.table, made.lens, cu, scale, window, sel)
+    bf = q.dtype == torch.bfloat16
+    e_logit = 64 * 2.0 ** -24 * top[..., None] + 2.0 ** -18
+    e_p = 2 * e_logit + 2.0 ** -17 + (2.0 ** -11 if bf else 0)
+    tol = torch.finfo(q.dtype).eps / 2 * np.abs(ref) + e_p * (size + np.abs(ref)) + 2.0 ** -25
+    got = host(out)
+    assert np.isfinite(got).all(), label
+    worst = float((np.abs(got - ref) / tol).max()) if ref.size else 0.0
+    say(f"  {label}: worst |err|/bound = {worst:.4f}")
+    assert worst <= 1, label
+    if lse is not None:
+        none = np.isinf(lse_ref)
+        g = host(lse)
+        assert np.array_equal(none, g == -np.inf), label
+        lim = e_logit[..., 0] + 2.0 ** -17 + 2.0 ** -22 * np.abs(np.where(none, 0, lse_ref))
+        assert (np.abs(np.where(none, 0, g) - np.where(none, 0, lse_ref)) <= lim).all(), label
+
+
+def attend(made, cache, rows, heads, dtype, seed=1, scale=None, window=0, sel=None, label="", q_scale=1.0,
+           max_rows=None, max_len=None):
+    D = cache.head_dim
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    g = torch.Generator().manual_seed(seed)
+    q = (q_scale * torch.randn(int(cu[-1]), heads, D, generator=g)).to(dtype).cuda()
+    scale = D ** -0.5 if scale is None else scale
+    lse = torch.full((int(cu[-1]), heads), 7.0, device="cuda")
+    out = torch.full((int(cu[-1]), heads, D), float("nan"), dtype=dtype, device="cuda")
+    cache.attention(q, ints(made.table), ints(made.lens), ints(cu),
+                    max_rows if max_rows is not None else int(max(rows)),
+                    max_len if max_len is not None else int(made.lens.max()), scale=scale, window=window,
+                    sel=None if sel is None else ints(sel), out=out, lse=lse)
+    torch.cuda.synchronize()
+    check_attention(out, lse, made, q, cu, scale, window, sel, label)
+    return q, out
+
+
+# ------------------------------------------------------------------ plan
+
+
+@pytest.mark.parametrize("n_seqs,most_len,most_new,short", [
+    (1, 1, 2, 0), (1, 500, 300, 0), (5, 200, 130, 0), (64, 300, 2, 0), (70, 200, 3, 9), (1025, 400, 40, 0),
+    (2500, 300, 5, 100), (8192, 100, 3, 0)])
+def test_plan(n_seqs, most_len, most_new, short):
+    say("plan", n_seqs, most_len, most_new, short)
+    rng = np.random.default_rng(n_seqs + most_len)
+    lens = rng.integers(0, most_len, n_seqs)
+    new = rng.integers(0, most_new, n_seqs)
+    if n_seqs == 1:
+        new[0] = most_new
+    cu = np.concatenate([[0], np.cumsum(new)])
+    width = int((-(-(lens + new) // 64)).max()) + 1
+    held = -(-lens // 64)
+    order = rng.permutation(int(held.sum()) + int((-(-(lens + new) // 64) - held).sum()) + 4)
+    table = np.full((n_seqs, width), -1)
+    at = 0
+    for b in range(n_seqs):
+        table[b, :held[b]] = order[at:at + held[b]]
+        at += held[b]
+    free = order[at:][: len(order) - at - short - 4] if short else order[at:]
+    want = K4.plan(lens, cu, table, free)
+    T, n_runs = int(cu[-1]), len(want[3])
+    t, slots, runs = ints(table), ints(np.full(T, 9)), ints(np.full((n_runs, 2), 9))
+    after, taken = ints(np.zeros(n_seqs)), ints([0])
+    for _ in range(2):                          # a second call gives the same
+        B.wq_kv4_plan(ints(lens), ints(cu), t, ints(free), after, slots, runs, taken)
+        torch.cuda.synchronize()
+        for got, ref in zip((t, after, slots, runs, taken), want):
+            assert np.array_equal(host(got), np.asarray(ref).reshape(host(got).shape))
+
+
+def test_plan_narrow_table():
+    lens, cu = np.array([100, 0]), np.array([0, 100, 130])
+    table = np.array([[5, 6], [-1, -1]])
+    want = K4.plan(lens, cu, table, np.array([9, 8, 7]))
+    t, slots, runs = ints(table), ints(np.zeros(130)), ints(np.zeros((len(want[3]), 2)))
+    after, taken = ints([0, 0]), ints([0])
+    B.wq_kv4_plan(ints(lens), ints(cu), t, ints([9, 8, 7]), after, slots, runs, taken)
+    for got, ref in zip((t, after, slots, runs, taken), want):
+        assert np.array_equal(host(got), np.asarray(ref).reshape(host(got).shape))
+    assert (host(slots)[28:100] == -1).all()
+
+
+# ---------------------------------------------------------------- append
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,new", [([0], [1]), ([63], [1]), ([64], [64]), ([5, 0, 31], [1, 130, 40]),
+                                      ([100, 7, 0], [0, 57, 64]), ([33], [31])])
+def test_append(D, dtype, lens, new):
+    say("append", D, dtype, lens, new)
+    H, t = 3, TYPES[dtype]
+    lens, new = np.array(lens), np.array(new)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    made = Made(lens, H, D, seed=D + int(cu[-1]), extra=8, width=8)
+    rng = np.random.default_rng(2)
+    free = np.setdiff1d(np.arange(made.n_pages), made.table)
+    table, after, slots, runs, _ = K4.plan(lens, cu, made.table, free)
+    T = int(cu[-1])
+    # keys and values are parts of one wider buffer
+    qkv = torch.from_numpy(rng.standard_normal((T, 4, H, D)) * np.exp(rng.standard_normal((T, 1, H, 1)))).to(t)
+    cache = made.gpu()
+    dev = qkv.cuda()
+    cache.append(dev[:, 1], dev[:, 3], ints(slots), ints(runs))
+    torch.cuda.synchronize()
+    K4.append(made.data, made.summary, f32(qkv[:, 1]), f32(qkv[:, 3]), slots)
+    assert np.array_equal(made.d.cpu().numpy(), made.data)
+    assert np.array_equal(made.s.cpu().numpy(), made.summary, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_append_edge_values(dtype):
+    """Constant groups, huge and tiny ranges, signed zeros, infinities and NaN:
+    the cache stays finite and equal to the oracle's."""
+    D, H, T = 64, 1, 64
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((T, H, D))
+    x[0], x[1], x[2], x[3, :, ::2] = 0.0, -0.0, 3.25, -0.0
+    x[4, 0, 5], x[5, 0, 6], x[6, 0, 7] = np.nan, np.inf, -np.inf
+    x[7] *= 1e4
+    x[8] = np.where(x[8] > 0, 6e4, -6e4)
+    x[9] *= 1e-7
+    x[10] = 1000 + x[10] * 1e-2
+    x[11:20] = np.round(x[11:20] * 2) / 4           # many ties
+    x[20] = np.nan
+    v = torch.from_numpy(x).to(TYPES[dtype])
+    made = Made([64], H, D, seed=9)
+    cache = made.gpu()
+    slots = np.arange(T) + 64 * made.table[0, 0]
+    cache.append(v.cuda(), v.cuda().flip(0), ints(slots), ints([[0, 64]]))
+    torch.cuda.synchronize()
+    K4.append(made.data, made.summary, f32(v), f32(v.flip(0)), slots)
+    assert np.array_equal(made.d.cpu().numpy(), made.data)
+    assert np.array_equal(made.s.cpu().numpy().astype(np.float32), made.summary.astype(np.float32), equal_nan=True)
+    k, w, _ = K4.read_page(made.data[made.table[0, 0], 0], D)
+    assert np.isfinite(k).all() and np.isfinite(w).all()
+
+
+def test_append_skips_bad_runs_and_pages():
+    D, H = 64, 2
+    made = Made([64, 64], H, D)
+    cache = made.gpu()
+    x = torch.randn(70, H, D, generator=torch.Generator().manual_seed(0)).half().cuda()
+    slots = np.concatenate([np.arange(60), np.arange(10)])
+    bad = [[-1, 0], [0, 65], [69, 2], [0, 0], [5, -3], [55, 10], [1 << 30, 4], [70, 1]]
+    cache.append(x, x, ints(slots), ints(bad))
+    cache.append(x, x, ints(np.full(70, -1)), ints([[0, 1], [3, 2]]))
+    cache.append(x, x, ints(np.arange(70) + made.n_pages * 64), ints([[0, 1], [3, 2]]))
+    cache.append(x, x, ints(np.arange(70) + 60), ints([[0, 8]]))          # crosses a page's end
+    torch.cuda.synchronize()
+    assert np.array_equal(made.d.cpu().numpy(), made.data)
+
+
+# ------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [[1], [31, 32, 33], [64, 65, 0, 500], [1500, 3]])
+def test_attention_one_row(D, dtype, lens):
+    say("attention", D, dtype, lens)
+    made = Made(lens, 2, D, seed=len(lens))
+    attend(made, made.gpu(), [1] * len(lens), 8, TYPES[dtype], label=f"{D} {dtype} {lens}")
+
+
+@pytest.mark.parametrize("H,heads", [(1, 1), (1, 16), (2, 2), (2, 10), (1, 17), (3, 21), (2, 64), (1, 40)])
+def test_attention_head_groups(H, heads):
+    made = Made([200, 77], H, 128, seed=heads)
+    attend(made, made.gpu(), [1, 3], heads, torch.float16, label=f"{heads} heads over {H}")
+
+
+@pytest.mark.parametrize("D,heads", [(64, 6), (128, 8), (256, 2)])
+@pytest.mark.parametrize("lens,rows", [([40], [40]), ([130, 64, 300], [7, 64, 33]), ([700, 9], [100, 1]),
+                                       ([50, 20], [0, 20]), ([5, 70], [9, 70])])
+def test_attention_rows(D, heads, lens, rows):
+    """Prompts and pieces of prompts; in the last, rows before the first token."""
+    made = Made(lens, 2, D, seed=D)
+    for dtype in TYPES.values():
+        attend(made, made.gpu(), rows, heads, dtype, label=f"{D} {lens} {rows}")
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 64, 65, 200, 5000, 1 << 40])
+def test_attention_window(window):
+    made = Made([333, 64, 1], 2, 128, seed=3)
+    attend(made, made.gpu(), [20, 1, 1], 4, torch.float16, window=window, label=f"window {window}")
+
+
+def test_attention_hints_do_not_change_what_is_seen():
+    made = Made([900, 130], 2, 64, seed=6)
+    cache = made.gpu()
+    for max_rows, max_len in ((1, 1), (0, 0), (500, 1 << 20), (1, 900), (40, 64)):
+        attend(made, cache, [1, 40], 4, torch.float16, max_rows=max_rows, max_len=max_len,
+               label=f"hints {max_rows} {max_len}")
+
+
+def test_attention_extreme_logits_and_values():
+    for q_scale, v_scale, spread in ((30.0, 1.0, 3.0), (1e-4, 1e-3, 1.0), (1.0, 8000.0, 1.0), (1000.0, 0.01, 30.0),
+                                     (1.0, 3.0, 1.0)):
+        made = Made([300, 2000], 1, 128, seed=8, spread=spread, v_scale=v_scale)
+        for dtype in TYPES.values():
+            attend(made, made.gpu(), [1, 2], 4, dtype, q_scale=q_scale, label=f"q {q_scale} v {v_scale} k {spread}")
+
+
+def test_attention_mixed_value_scales():
+    """Small values first, then a page of very large ones, and a flat long tail
+    beside one strong token: nothing overflows and the tail keeps its weight."""
+    made = Made([3000], 1, 64, seed=5, v_scale=0.01)
+    k, v = np.zeros((64, 1, 64), np.float16), np.full((64, 1, 64), 1.0, np.float16)
+    v[:, 0, ::2] = 60000.0
+    slots = np.arange(64) + 64 * made.table[0, 20]
+    K4.append(made.data, made.summary, k, v, slots)
+    attend(made, made.gpu(), [1], 2, torch.float16, label="large page")
+    tail = Made([20000], 1, 64, seed=7, spread=0.01, v_scale=0.02)
+    k = np.full((1, 1, 64), 2.0, np.float16)
+    K4.append(tail.data, tail.summary, k, np.zeros((1, 1, 64), np.float16), [64 * tail.table[0, 3] + 7])
+    cache = tail.gpu()
+    q = torch.full((1, 2, 64), 0.9, dtype=torch.float16, device="cuda")
+    lse = torch.empty(1, 2, device="cuda")
+    out = cache.attention(q, ints(tail.table), ints(tail.lens), ints([0, 1]), 1, 20000, scale=0.1, lse=lse)
+    check_attention(out, lse, tail, q, np.array([0, 1]), 0.1, label="flat tail")
+
+
+def test_attention_bf16_queries_of_any_size():
+    made = Made([100], 1, 64, seed=2)
+    for big in (1e30, 1e-30):
+        attend(made, made.gpu(), [1], 2, torch.bfloat16, q_scale=big, scale=0.125 / big, label=f"q {big}")
+
+
+def test_attention_skips_bad_pages():
+    made = Made([300, 300], 2, 64, seed=1)
+    made.table[0, 1], made.table[1, 0], made.table[1, 4] = -1, made.n_pages, 1 << 30
+    attend(made, made.gpu(), [1, 2], 4, torch.float16, label="bad pages")
+    made.table[:] = -5
+    attend(made, made.gpu(), [1, 2], 4, torch.float16, label="no pages")
+
+
+def test_attention_strided_queries():
+    made = Made([90, 10], 2, 128, seed=1)
+    cache = made.gpu()
+    wide = torch.randn(2, 3, 12, 128, generator=torch.Generator().manual_seed(3)).half().cuda()
+    cu = np.array([0, 1, 2])
+    for q in (wide[:, 1, 4:12], wide[:, 2, ::3], wide[:, 0].transpose(0, 1)[:8:4].transpose(0, 1)):
+        lse = torch.empty(2, q.shape[1], device="cuda")
+        out = cache.attention(q, ints(made.table), ints(made.lens), ints(cu), 1, 90, lse=lse)
+        check_attention(out, lse, made, q, cu, 128 ** -0.5, label=f"strides {q.stride()}")
+
+
+def test_attention_is_reproducible():
+    made = Made([3000, 100], 2, 128, seed=12)
+    cache = made.gpu()
+    a = [attend(made, cache, [1, 5], 8, torch.float16)[1] for _ in range(3)]
+    assert torch.equal(a[0], a[1]) and torch.equal(a[0], a[2])
+
+
+def test_attention_nan_query_stays_in_its_row():
+    made = Made([100, 100], 1, 64, seed=12)
+    cache = made.gpu()
+    q = torch.randn(5, 4, 64, generator=torch.Generator().manual_seed(3)).half().cuda()
+    args = (ints(made.table), ints(made.lens), ints([0, 3, 5]), 3, 100)
+    clean = cache.attention(q, *args)
+    bad = q.clone()
+    bad[1, 2, 7] = float("nan")
+    out = cache.attention(bad, *args)
+    assert out[1, 2].isnan().all()
+    keep = torch.ones(5, 4, dtype=torch.bool, device="cuda")
+    keep[1, 2] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+# ---------------------------------------------------------------- select
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,rows,heads,n_sel", [([1], [1], 2, 2), ([64, 65, 0], [1, 1, 1], 2, 4),
+                                                   ([3000, 900], [1, 3], 8, 7), ([9000], [2], 10, 40),
+                                                   ([500, 20000], [1, 1], 4, 100)])
+def test_select_and_sparse_attention(D, dtype, lens, rows, heads, n_sel):
+    say("select", D, dtype, lens, rows, heads, n_sel)
+    if D == 256 and max(lens) > 10000:
+        lens = [500, 8000]
+    made = Made(lens, 2, D, seed=n_sel)
+    cache = made.gpu()
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(int(cu[-1]), heads, D, generator=g).to(TYPES[dtype]).cuda()
+    args = (ints(made.table), ints(made.lens), ints(cu))
+    sel = cache.select(q, *args, n_sel)
+    want = K4.select(made.summary, f32(q), made.table, made.lens, cu, n_sel)
+    assert np.array_equal(host(sel), want)
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = cache.attention(q, *args, max(rows), max(lens), sel=sel, lse=lse)
+    check_attention(out, lse, made, q, cu, D ** -0.5, 0, want, f"sparse {D} {dtype} {lens}")
+
+
+def test_select_ties_go_to_the_lower_page():
+    made = Made([64 * 300], 1, 64, seed=1)
+    for p in range(300):
+        made.summary[made.table[0, p]] = made.summary[made.table[0, p % 3]]
+    cache = made.gpu()
+    q = torch.randn(1, 3, 64, generator=torch.Generator().manual_seed(5)).half().cuda()
+    for n in (2, 3, 50, 101, 102, 299, 300, 400):
+        sel = cache.select(q, ints(made.table), ints(made.lens), ints([0, 1]), n)
+        assert np.array_equal(host(sel), K4.select(made.summary, f32(q), made.table, made.lens, [0, 1], n)), n
+
+
+def test_select_is_exact_where_float32_is_not():
+    """Bounds that differ in the last bits of their 64-bit sums' float32 rounding."""
+    made = Made([64 * 200], 1, 128, seed=2)
+    rng = np.random.default_rng(0)
+    base = rng.standard_normal(128).astype(np.float16)
+    for p in range(200):
+        s = base.copy()
+        j = rng.integers(0, 128, 2)
+        s[j] = np.nextafter(s[j], np.float16(9), dtype=np.float16)
+        made.summary[made.table[0, p], 0] = s
+    cache = made.gpu()
+    q = torch.randn(1, 4, 128, generator=torch.Generator().manual_seed(5)).half().cuda()
+    for n in (5, 20, 100):
+        sel = cache.select(q, ints(made.table), ints(made.lens), ints([0, 1]), n)
+        assert np.array_equal(host(sel), K4.select(made.summary, f32(q), made.table, made.lens, [0, 1], n)), n
+
+
+def test_sparse_attention_takes_any_list():
+    """A caller's own list: unused entries anywhere, pages past the row's position."""
+    made = Made([700, 130], 2, 64, seed=4)
+    sel = np.full((3, 2, 6), -1)
+    sel[0, 0] = [-1, 3, -1, 5, 10, -1]
+    sel[0, 1] = [0, 1, 2, 9, 10, 11]
+    sel[1, 0] = [10, 2, 1 << 30, 7, -1, 0]
+    sel[2, 0] = [0, 1, 2, 3, 4, 5]
+    attend(made, made.gpu(), [2, 1], 4, torch.float16, sel=sel, label="own list")
+
+
+# ------------------------------------------------- streams, graphs, steps
+
+
+def step(cache, free, k, v, q, state):
+    table, lens, cu, after, slots, runs, taken, sel, out, out2 = state
+    B.wq_kv4_plan(lens, cu, table, free, after, slots, runs, taken)
+    cache.append(k, v, slots, runs)
+    cache.attention(q, table, after, cu, 1, 400, out=out)
+    cache.select(q, table, after, cu, 3, sel=sel)
+    cache.attention(q, table, after, cu, 1, 400, sel=sel, out=out2)
+
+
+@pytest.mark.parametrize("how", ["stream", "graph"])
+def test_steps_on_a_side_stream_and_in_a_graph(how):
+    """Decode steps in which sequences grow over page ends; each step's cache and
+    outputs against the oracle."""
+    H, D, heads, n = 2, 64, 4, 3
+    made = Made([62, 0, 191], H, D, seed=3, extra=40, width=6)
+    cache = made.gpu()
+    free_np = np.setdiff1d(np.arange(made.n_pages), made.table)
+    cu = np.arange(n + 1)
+    g = torch.Generator().manual_seed(0)
+    k, v, q = (torch.zeros(n, c, D, dtype=torch.float16, device="cuda") for c in (H, H, heads))
+    free = ints(free_np)
+    state = [ints(made.table), ints(made.lens), ints(cu), ints(np.zeros(n)), ints(np.zeros(n)), ints(np.zeros((n, 2))),
+             ints([0]), ints(np.zeros((n, H, 3))), torch.empty_like(q), torch.empty_like(q)]
+    side = torch.cuda.Stream()
+    graph = None
+    if how == "graph":
+        saved = [made.d.clone(), made.s.clone(), state[0].clone()]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(cache, free, k, v, q, state)          # loads the kernels
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(cache, free, k, v, q, state)
+        made.d.copy_(saved[0]), made.s.copy_(saved[1]), state[0].copy_(saved[2])
+    for i in range(5):
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=g).half())
+        state[1].copy_(ints(made.lens))
+        free.copy_(ints(free_np))
+        torch.cuda.synchronize()
+        if graph is None:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                step(cache, free, k, v, q, state)
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        made.table, made.lens, slots, runs, taken = K4.plan(made.lens, cu, made.table, free_np)
+        free_np = np.roll(free_np, -taken)
+        K4.append(made.data, made.summary, f32(k), f32(v), slots)
+        assert np.array_equal(made.d.cpu().numpy(), made.data), i
+        assert np.array_equal(host(state[0]), made.table), i
+        check_attention(state[8], None, made, q, cu, D ** -0.5, label=f"step {i}")
+        sel = K4.select(made.summary, f32(q), made.table, made.lens, cu, 3)
+        assert np.array_equal(host(state[7]), sel), i
+        check_attention(state[9], None, made, q, cu, D ** -0.5, 0, sel, f"step {i} sparse")
+
+
+def test_explicit_stream():
+    made = Made([500, 3], 2, 64, seed=3)
+    cache = made.gpu()
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(0)).half().cuda()
+    args = (ints(made.table), ints(made.lens), ints([0, 1, 2]), 1, 500)
+    want = cache.attention(q, *args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        out = cache.attention(q, *args, stream=s)
+        side.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_long_cache_addresses_past_32_bits():
+    """Pages whose bytes lie past 4 GiB of the cache, append and both attentions."""
+    D, H, n_pages = 256, 8, 30000                   # 4.9 GB
+    data = torch.zeros(n_pages, H, 80 * D, dtype=torch.uint8, device="cuda")
+    summary = torch.zeros(n_pages, H, 2, D, dtype=torch.float16, device="cuda")
+    cache = B.KV4Cache(data, summary)
+    pages = np.array([29999, 27000, 29998])
+    rng = np.random.default_rng(1)
+    k, v = (torch.from_numpy(rng.standard_normal((150, H, D))).half() for _ in range(2))
+    slots = pages[np.arange(150) // 64] * 64 + np.arange(150) % 64
+    cache.append(k.cuda(), v.cuda(), ints(slots), ints([[0, 64], [64, 64], [128, 22]]))
+    torch.cuda.synchronize()
+    made = Made([0], H, D, extra=3)
+    made.table, made.lens = np.array([[0, 1, 2]]), np.array([150])
+    made.data[:], made.summary[:] = 0, 0
+    K4.append(made.data, made.summary, f32(k), f32(v), np.arange(150))
+    assert np.array_equal(data[torch.from_numpy(pages).cuda()].cpu().numpy(), made.data)
+    q = torch.randn(2, 16, D, generator=torch.Generator().manual_seed(0)).half().cuda()
+    args = (ints(pages[None]), ints([150]), ints([0, 2]))
+    sel = cache.select(q, *args, 2)
+    want = K4.select(made.summary, f32(q), made.table, made.lens, [0, 2], 2)
+    assert np.array_equal(host(sel), want)
+    for s, w in ((None, None), (sel, want)):
+        out = cache.attention(q, *args, 2, 150, sel=s)
+        check_attention(out, None, made, q, np.array([0, 2]), D ** -0.5, 0, w, "far pages")
