@@ -1,97 +1,587 @@
 // Attention over the paged 4-bit key/value cache (wq.h, "4-bit key/value
-// cache").
+// cache"), on the matrix cores.
+//
+// A wave takes pages of 64 tokens and CT column tiles of 16 (row, head) pairs
+// of one key/value head.  With key code c, scale S and offset Z of a token and
+// group g, and the group's part of the query Q_g,
+//   logit = scale (sum_g S_g (c_g . Q_g) + sum_g Z_g sum(Q_g)),
+// and with the softmax weights p,
+//   out_d = sum_t (p_t S_{t,g(d)}) c_{t,d} + sum_t p_t Z_{t,g(d)}.
+// Both sums over codes are 16x16x32 products whose A operand is the codes: one
+// mask per two codes makes FP16 subnormals c 2^-24 (or 16 c 2^-24; B carries the
+// 1/16).  Tokens are the rows of the first product, so a lane ends with 4 tokens
+// of one column per 16, and two such tiles are just its 8 k of the second
+// product's B operand: the weights never leave their registers.
+//
+// Precision.  Queries are scaled by a power of two to [2^14, 2^15) and so are
+// exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  The weights
+// times their scales enter as an FP16 head and, for FP16 outputs, an FP16
+// remainder (22 bits); for BF16 outputs the head alone (2^-12, against the
+// output's 2^-9).  They carry 2^8, and value scales of 2 and more lower that by a
+// running power of two, so that neither end of FP16's range is met: a weight
+// 2^-30 of the largest still counts.  The running maximum is only raised when a
+// logit passes it by 2^6, which spares most pages the cross-lane maximum and
+// the rescale of the sums.
 
 #include "wq_common.cuh"
 #include "wq_device.h"
 #include "wq_kv4.cuh"
 
+#include <utility>
+
 namespace wqd {
 
-constexpr int kAttnThreads = 256;
+constexpr int kAttnWaves = 4;
+constexpr int kFoldPages = 2;
+constexpr float kWeightExp = 8.f;    // weights carry 2^8 ...
+constexpr float kRaise = 6.f;        // ... and grow by up to 2^6 before the maximum is raised
 
-// One workgroup per (row, head): 256 tokens at a time, a thread's logit each,
-// then a thread's channel each over those tokens.
-template <int DT, int D>
-__global__ void __launch_bounds__(kAttnThreads)
-attn_kernel(KvRows a, const uint8_t* __restrict__ data, int64_t n_pages, int kv_heads, float scale,
-            int window, const int32_t* __restrict__ sel, int n_sel, uint16_t* __restrict__ out,
-            float* __restrict__ lse) {
-  constexpr int G = D / 32, W = G < 4 ? G : 4;
-  __shared__ float s_q[D], s_p[kAttnThreads], s_red[kAttnThreads];
-  __shared__ int64_t s_page[kAttnThreads / 64];
-  const int row = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
-  const int kvh = h / (a.heads / kv_heads), tid = threadIdx.x;
-  const SeqRow sr = find_row(a, row);
-  if (row >= a.cu[sr.b + 1]) return;
-  for (int d = tid; d < D; d += kAttnThreads)
-    s_q[d] = to_float<DT>(a.q[row * a.q_row + h * a.q_head + d]);
-  const int first = window > 0 ? max(sr.pos - window + 1, 0) : 0;
-  const int pages = (int)min((int64_t)((sr.pos + 64) / 64), a.width);
-  const int n = sel != nullptr ? n_sel : pages;
-  const int32_t* pick =
-      sel != nullptr ? sel + ((int64_t)row * kv_heads + kvh) * n_sel : nullptr;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j0 = 0; j0 < n; j0 += 4) {
-    __syncthreads();
-    const int j = j0 + tid / 64;
-    const int p = j < n ? (pick != nullptr ? pick[j] : j) : -1;
-    const int page = p >= 0 && p < pages ? a.table[sr.b * a.width + p] : -1;
-    const bool ok = page >= 0 && page < n_pages;
-    const int t = p * 64 + (tid & 63);
-    if ((tid & 63) == 0) s_page[tid / 64] = ok ? page : -1;
-    float x = -INFINITY;
-    if (ok && t <= sr.pos && t >= first) {
-      const int tt = t & 31, u = tt >> 4, r = (tt >> 2) & 3, e = 4 * u + (tt & 3);
-      const uint8_t* tile = data + ((int64_t)page * kv_heads + kvh) * (80 * D) + ((t >> 5) & 1) * (40 * D);
-      const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + 32 * D);
-      x = 0.f;
-      for (int g = 0; g < G; ++g) {
-        float dot = 0.f, sum = 0.f;
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(
-              tile + u * (8 * D) + (g / W) * (256 * W) + ((c * 16 + (tt & 15)) * W + g % W) * 4);
-          for (int i = 0; i < 8; ++i) {
-            const float q = s_q[g * 32 + c * 8 + i];
-            dot += q * (float)((w >> (4 * ((i >> 1) + 4 * (i & 1)))) & 15u);
-            sum += q;
-          }
-        }
-        x += h2f(meta[r * 8 * G + g * 8 + e]) * dot + h2f(meta[D + tt * G + g]) * sum;
-      }
-      x *= scale;
+// f(0), ..., f(N - 1) with the index as a compile-time constant.
+template <typename F, int... I>
+__device__ __forceinline__ void unroll_over(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unroll(F f) {
+  unroll_over(f, std::make_integer_sequence<int, N>{});
+}
+
+// Lane N of every row of 16 lanes, in all of the row's lanes.
+template <int N>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + N, 0xF, 0xF, false);
+}
+
+// 8 codes of a word as a matrix-core operand: slots 0, 1, 4, 5 hold c 2^-24,
+// slots 2, 3, 6, 7 hold 16 c 2^-24.
+__device__ __forceinline__ h8 code_operand(uint32_t w) {
+  uint32_t lo0, hi0, lo1, hi1;
+  w4_word_sub(w, lo0, hi0, lo1, hi1);
+  return __builtin_bit_cast(h8, u4v{lo0, hi0, lo1, hi1});
+}
+
+// The same with the codes as normal numbers: c and 16 c.  A sum on the matrix
+// cores drops what lies below its largest operand's exponent, which subnormals
+// make 2^10 too large: here that would be a bias of 2^-19, and it matters where
+// many values average out.
+__device__ __forceinline__ h8 normal_operand(uint32_t w) {
+  uint32_t v[4];
+  w4_word_magic(w, v[0], v[1], v[2], v[3]);
+  h8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const h2 x = as_h2(v[i]) - h2{(_Float16)1024.f, (_Float16)1024.f};
+    o[2 * i] = x[0];
+    o[2 * i + 1] = x[1];
+  }
+  return o;
+}
+
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// One tile of 32 tokens of one head in registers: lane (row r = lane / 16,
+// l = lane % 16).
+template <int D>
+struct Tile {
+  static constexpr int G = D / 32, W = G < 4 ? G : 4, J = D / 16, M = G == 8 ? 2 : 1, ZN = G / 2;
+  uint32_t kc[2][G];      // 16-token part, group: 8 codes of token l
+  uint32_t vc[J];         // 16 channels: 8 codes of channel l
+  uint32_t ks[M], vs[M];  // row r's scales, M dwords a lane (2 slots each)
+  uint32_t kz[2][ZN];     // token l's offsets, all groups
+  u4v vz;                 // group l's offsets of 8 tokens
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int lane) {
+    const int r = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < G / W; ++c)
+        __builtin_memcpy(&kc[u][c * W], q + u * (8 * D) + c * (256 * W) + lane * (4 * W), 4 * W);
+    const int at = G == 2 ? (l & 7) * 4 : l * (4 * M);
+    __builtin_memcpy(&ks[0], q + 32 * D + r * (16 * G) + at, 4 * M);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      __builtin_memcpy(&kz[u][0], q + 34 * D + (16 * u + l) * (2 * G), 2 * G);
+#pragma unroll
+    for (int c = 0; c < J / 4; ++c)
+      __builtin_memcpy(&vc[c * 4], q + 16 * D + c * 1024 + lane * 16, 16);
+    __builtin_memcpy(&vs[0], q + 36 * D + r * (16 * G) + at, 4 * M);
+    __builtin_memcpy(&vz, q + 38 * D + r * (16 * G) + (l < G ? l : 0) * 16, 16);
+  }
+  // Clears the value scales and offsets of tokens n and later (they were never
+  // written and may be anything).
+  __device__ __forceinline__ void cut(int n, int lane) {
+    const int r = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int x = 0; x < M; ++x) {
+      const int j = (M == 1 ? l : 2 * l + x) & 3;
+      const int tok = 16 * (j >> 1) + 4 * r + 2 * (j & 1);
+      vs[x] = tok >= n ? 0 : tok + 1 >= n ? vs[x] & 0xFFFFu : vs[x];
     }
-    s_red[tid] = x != x ? INFINITY : x;   // a NaN logit makes its row NaN
-    __syncthreads();
-    for (int w = kAttnThreads / 2; w > 0; w >>= 1) {
-      if (tid < w) s_red[tid] = fmaxf(s_red[tid], s_red[tid + w]);
-      __syncthreads();
-    }
-    const float m_new = fmaxf(m, s_red[0]);
-    if (m_new == -INFINITY) continue;   // the same for every thread
-    s_p[tid] = __expf(x - m_new);
-    __syncthreads();
-    const float f = __expf(m - m_new);
-    m = m_new;
-    l *= f;
-    o *= f;
-    for (int i = 0; i < kAttnThreads; ++i) {
-      const float pv = s_p[i];
-      if (pv == 0.f) continue;
-      l += pv;
-      if (tid < D) {
-        const int tt = i & 31, u = tt >> 4, r = (tt >> 2) & 3, e = 4 * u + (tt & 3), d = tid;
-        const uint8_t* tile = data + (s_page[i / 64] * kv_heads + kvh) * (80 * D) + ((i >> 5) & 1) * (40 * D);
-        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + 36 * D);
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-            tile + 16 * D + (d >> 6) * 1024 + (r * 16 + (d & 15)) * 16 + ((d >> 4) & 3) * 4);
-        const int at = r * 8 * G + (d / 32) * 8 + e;
-        o += pv * (h2f(meta[at]) * (float)((w >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) + h2f(meta[D + at]));
-      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tok = 16 * (j >> 1) + 4 * r + 2 * (j & 1);
+      vz[j] = tok >= n ? 0 : tok + 1 >= n ? vz[j] & 0xFFFFu : vz[j];
     }
   }
-  if (tid < D) out[((int64_t)row * a.heads + h) * D + tid] = from_float<DT>(l == 0.f ? 0.f : o / l);
-  if (tid == 0 && lse != nullptr)
-    lse[(int64_t)row * a.heads + h] = l == 0.f ? -INFINITY : m + __logf(l);
+  // Dword j (slots 2j, 2j + 1) of group g of row r's scales (GJ = 4 g + j), in all lanes.
+  template <int GJ>
+  static __device__ __forceinline__ h2 scale2(const uint32_t (&s)[M]) {
+    if constexpr (M == 1) return as_h2(row_lane<GJ>(s[0]));
+    else return as_h2(row_lane<GJ / 2>(s[GJ & 1]));
+  }
+};
+
+struct AttnArgs {
+  KvRows a;
+  const uint8_t* data;
+  int64_t n_pages;
+  int kv_heads, window, n_sel, tiles, splits, split_pages;
+  float scale;
+  const int32_t* sel;
+  uint16_t* out;
+  float* lse;
+  float* part;            // [row][head][split][D], then [row][head][split][2]
+};
+
+template <int DT, int D, int CT, bool SEL>
+__global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p) {
+  using Tl = Tile<D>;
+  constexpr int G = Tl::G, J = Tl::J;
+  constexpr int NT = CT == 1 && D <= 128 ? 2 : 1;     // tiles taken together
+  constexpr int kPart = (4 * J + 2) * 64;    // floats a wave keeps for a column tile
+  extern __shared__ __attribute__((aligned(16))) float s_merge[];
+  const KvRows& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane >> 4, l = lane & 15;
+  const int R = a.heads / p.kv_heads;
+
+  // pairs (sequence or row, key/value head) vary fastest: workgroups that read
+  // the same pages are a multiple of the pairs apart and so, for 8 pairs and
+  // their multiples, on the same XCD; the last column tiles, which see the most
+  // tokens, come first
+  const unsigned pairs = (SEL ? a.rows : a.seqs) * (unsigned)p.kv_heads;
+  const int pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
+  const int kvh = pair % p.kv_heads, split = rest % p.splits;
+  const int tile0 = p.tiles - 1 - rest / p.splits;
+  int b, row0, n, len;
+  if constexpr (SEL) {
+    row0 = pair / p.kv_heads;
+    const SeqRow sr = find_row(a, row0);
+    b = sr.b;
+    n = 1;
+    len = sr.pos + 1;
+    if (row0 >= a.cu[b + 1]) return;
+  } else {
+    b = pair / p.kv_heads;
+    row0 = max(a.cu[b], 0);
+    n = min(a.cu[b + 1], a.rows) - row0;
+    len = a.lens[b];
+  }
+  const int cols = n * R;
+  const int written = SEL ? a.lens[b] : len;      // tokens that the cache holds
+  for (int tile = tile0; tile * (16 * CT) < cols; tile += p.tiles) {
+    // this lane's columns, and the scaled queries
+    int pos[CT], row[CT], head[CT];
+    h8 Q[CT][G], SQ[CT];
+    float c1[CT], c2[CT];
+    int pos_lo = 0x7FFFFFFF, pos_hi = -1;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int c = tile * (16 * CT) + ct * 16 + l;
+      const bool on = c < cols;
+      row[ct] = on ? row0 + c / R : -1;
+      head[ct] = kvh * R + c % R;
+      pos[ct] = on ? (SEL ? len - 1 : len - n + c / R) : -1;
+      const uint16_t* q = a.q + (on ? row[ct] * a.q_row + head[ct] * a.q_head : 0);
+      u4v qv[G];
+      float top = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        qv[g] = on ? *reinterpret_cast<const u4v*>(q + 32 * g + 8 * r) : u4v{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          top = fmaxf(top, fabsf(to_float<DT>((uint16_t)(qv[g][i >> 1] >> (16 * (i & 1))))));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+      e = top == 0.f || e > 127 ? 14 : max(e, -100);
+      u4v sq = {0, 0, 0, 0};
+      uint32_t sqw[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float y =
+              ldexpf(to_float<DT>((uint16_t)(qv[g][i >> 1] >> (16 * (i & 1)))), 14 - e);
+          sum += y;
+          Q[ct][g][i] = (_Float16)(i & 2 ? y * 0.0625f : y);
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        sum *= 0.015625f;
+        const _Float16 hi = (_Float16)sum, lo = (_Float16)(sum - (float)hi);
+        const uint32_t bits = r == 0 ? __builtin_bit_cast(uint16_t, hi)
+                                     : r == 1 ? __builtin_bit_cast(uint16_t, lo) : 0u;
+        sqw[g >> 1] |= bits << (16 * (g & 1));
+      }
+      sq = u4v{sqw[0], sqw[1], sqw[2], sqw[3]};
+      SQ[ct] = __builtin_bit_cast(h8, sq);
+      const float k = p.scale * 1.44269504f;
+      c1[ct] = ldexpf(k, e - 14 + 24);
+      c2[ct] = ldexpf(k, e - 14 + 6);
+      const int c_lo = tile * (16 * CT) + ct * 16, c_hi = min(c_lo + 15, cols - 1);
+      if (c_lo < cols) {
+        pos_lo = min(pos_lo, SEL ? len - 1 : len - n + c_lo / R);
+        pos_hi = max(pos_hi, SEL ? len - 1 : len - n + c_hi / R);
+      }
+    }
+    pos_lo = __builtin_amdgcn_readfirstlane(pos_lo);
+    pos_hi = __builtin_amdgcn_readfirstlane(pos_hi);
+
+    // pages of this workgroup: positions in the block table, or in the row's list
+    const int64_t pages64 = ((int64_t)pos_hi + 64) / 64;
+    const int pages = (int)(pages64 < a.width ? pages64 : a.width);
+    const int first = !SEL && p.window > 0 ? max(pos_lo - p.window + 1, 0) / 64 : 0;
+    const int total = SEL ? p.n_sel : max(pages - first, 0);
+    const int per = max(p.split_pages, (total + p.splits - 1) / p.splits);
+    const int j0 = min(split * per, total), j1 = min(j0 + per, total);
+    const int32_t* const table = a.table + (int64_t)b * a.width;
+    const int32_t* const list =
+        SEL ? p.sel + ((int64_t)row0 * p.kv_heads + kvh) * p.n_sel : nullptr;
+
+    f4 O[CT][J], OZ[CT];
+    float m[CT], m_kept[CT];
+    int vexp = 0;           // value scales since the last fold are below 2^(vexp + 1)
+    bool kept = false;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      m[ct] = m_kept[ct] = -INFINITY;
+      OZ[ct] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < J; ++j) O[ct][j] = f4{0, 0, 0, 0};
+    }
+    // Folds code sums and offsets into the wave's values in LDS.  The two nearly
+    // cancel, and a matrix-core sum loses a little to every addition: over a long
+    // cache what they have in common would swallow the result's last bits.
+    auto fold = [&]() {
+      const float up = ldexpf(1.f, vexp);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float* const s = s_merge + (wave * CT + ct) * kPart;
+        f4* const s4 = reinterpret_cast<f4*>(s) + lane;
+        const float f = m_kept[ct] == m[ct] ? 1.f : __builtin_amdgcn_exp2f(m_kept[ct] - m[ct]);
+        float z[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) z[g] = __shfl(OZ[ct][g & 3], (g >> 2) * 16 + l);
+        float sum = __shfl(OZ[ct][0], 32 + l);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          f4 v = O[ct][j] * up + z[j >> 1];
+          if (kept) v += s4[j * 64] * f;
+          s4[j * 64] = v;
+          O[ct][j] = f4{0, 0, 0, 0};
+        }
+        if (kept) sum += s[4 * J * 64 + lane] * f;
+        s[4 * J * 64 + lane] = sum;
+        s[(4 * J + 1) * 64 + lane] = m[ct];
+        OZ[ct] = f4{0, 0, 0, 0};
+        m_kept[ct] = m[ct];
+      }
+      vexp = 0;
+      kept = true;
+    };
+
+    // page position and number at list index j (number -1: nothing there)
+    auto find = [&](int j, int& at, int& id) {
+      at = j < j1 ? (SEL ? list[j] : first + j) : -1;
+      id = at >= 0 && at < pages ? table[at] : -1;
+      at = __builtin_amdgcn_readfirstlane(at);
+      id = __builtin_amdgcn_readfirstlane(id);
+      if (id >= p.n_pages) id = -1;
+    };
+    const int64_t stride = (int64_t)p.kv_heads * (80 * D);
+    const uint8_t* const base = p.data + (int64_t)kvh * (80 * D);
+
+    int since = 0;          // pages since the last fold
+    for (int j = j0 + wave; j < j1; j += kAttnWaves) {
+      int at, id;
+      find(j, at, id);
+      if (id < 0) continue;
+      if (since == kFoldPages) {
+        fold();
+        since = 0;
+      }
+      ++since;
+#pragma unroll 1
+      for (int part = 0; part < 2 / NT; ++part) {
+        const int t0 = at * 64 + part * (32 * NT);
+        Tl tp[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          tp[t].load(base + id * stride + (part * NT + t) * (40 * D), lane);
+        if (t0 + 32 * NT > written) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) tp[t].cut(written - t0 - 32 * t, lane);
+        }
+        // logits: sums of codes times queries by group, and of offsets
+        f4 sc[CT][2 * NT], zt[CT][2 * NT];
+        unroll<2 * NT>([&](auto uu) {
+          constexpr int u = uu, t = u / 2, h = u % 2;
+          uint32_t zw[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < Tl::ZN; ++i) zw[i] = tp[t].kz[h][i];
+          const h8 za = __builtin_bit_cast(h8, u4v{zw[0], zw[1], zw[2], zw[3]});
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            zt[ct][u] = mfma(za, SQ[ct], f4{0, 0, 0, 0});
+            sc[ct][u] = f4{0, 0, 0, 0};
+          }
+          unroll<G>([&](auto g) {
+            const h8 ka = code_operand(tp[t].kc[h][g]);
+            const h2 s0 = Tl::template scale2<g * 4 + 2 * h>(tp[t].ks);
+            const h2 s1 = Tl::template scale2<g * 4 + 2 * h + 1>(tp[t].ks);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              const f4 d = mfma(ka, Q[ct][g], f4{0, 0, 0, 0});
+              f4& s = sc[ct][u];
+              s[0] = __builtin_fmaf((float)s0[0], d[0], s[0]);
+              s[1] = __builtin_fmaf((float)s0[1], d[1], s[1]);
+              s[2] = __builtin_fmaf((float)s1[0], d[2], s[2]);
+              s[3] = __builtin_fmaf((float)s1[1], d[3], s[3]);
+            }
+          });
+        });
+
+        // base-2 logits above the running maximum, plus kWeightExp
+        constexpr int NY = 8 * NT;
+        const bool edge = t0 + 32 * NT - 1 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
+        float y[CT][NY];
+        bool raise = false;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const bool none = m[ct] == -INFINITY;
+          const float m8 = none ? -kWeightExp : m[ct] - kWeightExp;
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < NY; ++i)
+            y[ct][i] = __builtin_fmaf(sc[ct][i >> 2][i & 3], c1[ct],
+                                      __builtin_fmaf(zt[ct][i >> 2][i & 3], c2[ct], -m8));
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < NY; ++i) {
+              const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
+              if (t > pos[ct] || (p.window > 0 && t <= pos[ct] - p.window)) y[ct][i] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NY; ++i) top = fmaxf(top, y[ct][i]);
+          raise |= top > (none ? -INFINITY : kWeightExp + kRaise);
+        }
+        if (__any(raise)) {
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const bool none = m[ct] == -INFINITY;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NY; ++i) top = fmaxf(top, y[ct][i]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // the maximum in y's scale stands at kWeightExp
+            const float up = none ? (top == -INFINITY ? 0.f : top - kWeightExp)
+                                  : fmaxf(top - kWeightExp, 0.f);
+            const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
+            if (!none) m[ct] += up;
+            else if (top != -INFINITY) m[ct] = up;
+#pragma unroll
+            for (int i = 0; i < NY; ++i) y[ct][i] -= up;
+#pragma unroll
+            for (int j2 = 0; j2 < J; ++j2) O[ct][j2] *= f;
+            OZ[ct] *= f;
+          }
+        }
+        // value scales of 2 and more: lower the weights' power of two
+        uint32_t big = 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < Tl::M; ++x) big |= tp[t].vs[x];
+        if (__any((big & 0x40004000u) != 0)) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int x = 0; x < Tl::M; ++x)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              top = max(top, max(tp[t].vs[x] >> 16, tp[t].vs[x] & 0xFFFFu));
+          int e = (int)(top >> 10) - 15;
+#pragma unroll
+          for (int d = 1; d < 64; d <<= 1) e = max(e, __shfl_xor(e, d));
+          e = __builtin_amdgcn_readfirstlane(e);
+          if (e > vexp) {
+            const float f = ldexpf(1.f, vexp - e);
+            vexp = e;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+              for (int j2 = 0; j2 < J; ++j2) O[ct][j2] *= f;
+          }
+        }
+        const float vdown = ldexpf(1.f, -vexp);
+
+        const uint32_t fill = l == 8 ? 0x3C003C00u : 0u;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          u4v z = tp[t].vz;
+          if (l >= G) z = u4v{fill, fill, fill, fill};
+          const h8 za = __builtin_bit_cast(h8, z);
+          float ws[CT][8];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            h8 hi, lo;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float w = __builtin_amdgcn_exp2f(y[ct][8 * t + e]);
+              hi[e] = (_Float16)w;
+              lo[e] = (_Float16)(w - (float)hi[e]);
+              ws[ct][e] = w * (e & 2 ? vdown * 0.0625f : vdown);
+            }
+            OZ[ct] = mfma(za, hi, OZ[ct]);
+            OZ[ct] = mfma(za, lo, OZ[ct]);
+          }
+          unroll<G>([&](auto g) {
+            h2 s[4];
+            unroll<4>([&](auto x) { s[x] = Tl::template scale2<g * 4 + x>(tp[t].vs); });
+            const h8 v0 = normal_operand(tp[t].vc[2 * g]), v1 = normal_operand(tp[t].vc[2 * g + 1]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              h8 hi, lo;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float sv = (float)s[e >> 1][e & 1];
+                hi[e] = (_Float16)(ws[ct][e] * sv);
+                lo[e] = (_Float16)__builtin_fmaf(ws[ct][e], sv, -(float)hi[e]);
+              }
+              O[ct][2 * g] = mfma(v0, hi, O[ct][2 * g]);
+              O[ct][2 * g + 1] = mfma(v1, hi, O[ct][2 * g + 1]);
+              O[ct][2 * g] = mfma(v0, lo, O[ct][2 * g]);
+              O[ct][2 * g + 1] = mfma(v1, lo, O[ct][2 * g + 1]);
+            }
+          });
+        }
+      }
+    }
+
+    fold();
+    // the waves' parts joined in order
+    __syncthreads();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float mw[kAttnWaves], mx = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        mw[w] = s_merge[(w * CT + ct) * kPart + (4 * J + 1) * 64 + lane];
+        mx = fmaxf(mx, mw[w]);
+      }
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        mw[w] = mw[w] == mx ? 1.f : __builtin_amdgcn_exp2f(mw[w] - mx);
+        sum += mw[w] * s_merge[(w * CT + ct) * kPart + 4 * J * 64 + lane];
+      }
+      if (row[ct] < 0) continue;
+      const int64_t at = (int64_t)row[ct] * a.heads + head[ct];
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      for (int j = wave; j < J; j += kAttnWaves) {
+        f4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w)
+          o += mw[w] * reinterpret_cast<const f4*>(s_merge + (w * CT + ct) * kPart)[j * 64 + lane];
+        const int d = 16 * j + 4 * r;
+        if (p.splits == 1) {
+          uint16_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = from_float<DT>(sum == 0.f ? 0.f : o[i] * inv);
+          *reinterpret_cast<u2*>(p.out + at * D + d) = u2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+        } else {
+          *reinterpret_cast<f4*>(p.part + (at * p.splits + split) * D + d) = o;
+        }
+      }
+      if (wave == 0 && r == 0) {
+        if (p.splits == 1) {
+          if (p.lse != nullptr)
+            p.lse[at] = sum == 0.f ? -INFINITY
+                                   : (mx == -INFINITY ? 0.f : mx) * 0.69314718f +
+                                         __logf(sum) - kWeightExp * 0.69314718f;
+        } else {
+          float* ml = p.part + (int64_t)a.rows * a.heads * p.splits * D + (at * p.splits + split) * 2;
+          ml[0] = sum;
+          ml[1] = mx;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the splits of every (row, head), one wave each: split s's weight is
+// 2^(m_s - max m).
+template <int DT, int D>
+__global__ void __launch_bounds__(kAttnWaves * kWave)
+join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t* __restrict__ out,
+            float* __restrict__ lse) {
+  constexpr int C = D / 64;
+  const int64_t at = (int64_t)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (at >= items) return;
+  const float* ml = part + items * splits * D + at * splits * 2;
+  const float* o = part + at * splits * D + lane * C;
+  float mx = -INFINITY;
+  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, ml[2 * s + 1]);
+  float sum = 0.f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    const float w = ml[2 * s + 1] == mx ? 1.f : __builtin_amdgcn_exp2f(ml[2 * s + 1] - mx);
+    sum += w * ml[2 * s];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += w * o[(int64_t)s * D + c];
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    out[at * D + lane * C + c] = from_float<DT>(sum == 0.f ? 0.f : acc[c] / sum);
+  if (lane == 0 && lse != nullptr)
+    lse[at] = sum == 0.f ? -INFINITY
+                         : (mx == -INFINITY ? 0.f : mx) * 0.69314718f + __logf(sum) -
+                               kWeightExp * 0.69314718f;
+}
+
+// How a call is split: column tiles a sequence (or row) and splits of its pages.
+struct AttnPlan {
+  int ct;                  // column tiles of 16 a wave
+  int64_t pairs, tiles, splits, split_pages;
+};
+static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t max_rows,
+                          int64_t max_len, int64_t n_sel, bool sel) {
+  AttnPlan p{};
+  const int64_t R = a->n_heads / c->n_kv_heads;
+  const int64_t cols = (sel || max_rows < 1 ? 1 : max_rows) * R;
+  p.ct = cols > 16 && c->head_dim <= 128 ? 2 : 1;
+  p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
+  p.pairs = (sel ? a->n_rows : a->n_seqs) * c->n_kv_heads;
+  int64_t pages = sel ? n_sel : (max_len + 63) / 64;
+  if (!sel && pages > a->table_width) pages = a->table_width;
+  if (pages < 1) pages = 1;
+  // enough workgroups for every compute unit twice; a split has at least two
+  // pages a wave
+  const int64_t items = p.pairs * p.tiles;
+  int64_t splits = (1024 + items - 1) / items;
+  const int64_t most = (pages + 2 * kAttnWaves - 1) / (2 * kAttnWaves);
+  if (splits > most) splits = most;
+  p.split_pages = (pages + splits - 1) / splits;
+  p.splits = (pages + p.split_pages - 1) / p.split_pages;
+  return p;
 }
 
 }  // namespace wqd
@@ -112,7 +602,9 @@ extern "C" int64_t wq_kv4_attention_workspace(const wq_kv4_cache* cache, const w
   if (int e = check_attention(cache, rows, max_rows, max_len, n_sel, "wq_kv4_attention_workspace"))
     return e;
   wq::ok();
-  return 0;
+  const AttnPlan p = attn_plan(cache, rows, max_rows, max_len, n_sel, n_sel > 0);
+  if (p.splits == 1) return 0;
+  return (rows->n_rows * rows->n_heads * p.splits * (cache->head_dim + 2) * 4 + 15) / 16 * 16;
 }
 
 extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
@@ -122,6 +614,8 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   const char* who = "wq_kv4_attention";
   if (int e = check_attention(cache, rows, max_rows, max_len, n_sel, who)) return e;
   if (window < 0) return wq::fail(WQ_ERR_INVALID_ARG, "%s: window must be at least 0", who);
+  if ((sel != nullptr) != (n_sel > 0))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: sel and n_sel go together", who);
   if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
   const int64_t need = wq_kv4_attention_workspace(cache, rows, max_rows, max_len, n_sel);
   if (!out || (need && !workspace)) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -130,15 +624,48 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
                     (long long)workspace_bytes, (long long)need);
   if (!aligned16(out) || !aligned4(lse) || !aligned4(sel) || !aligned16(workspace))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
-  if (rows->n_rows * rows->n_heads > 0x7FFFFFFFll)
+  const AttnPlan plan = attn_plan(cache, rows, max_rows, max_len, n_sel, sel != nullptr);
+  const int64_t grid = plan.pairs * plan.tiles * plan.splits;
+  const int64_t items = rows->n_rows * rows->n_heads;
+  if (grid > 0x7FFFFFFFll || items > 0x7FFFFFFFll)
     return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
-  const KvRows a = kv4_rows(rows);
-  const int win = window > 0x40000000 ? 0 : (int)window;
+  AttnArgs p{};
+  p.a = kv4_rows(rows);
+  p.data = cache->data;
+  p.n_pages = cache->n_pages;
+  p.kv_heads = (int)cache->n_kv_heads;
+  p.window = window > 0x40000000 ? 0 : (int)window;
+  p.n_sel = (int)n_sel;
+  p.tiles = (int)plan.tiles;
+  p.splits = (int)plan.splits;
+  p.split_pages = (int)plan.split_pages;
+  p.scale = scale;
+  p.sel = sel;
+  p.out = out;
+  p.lse = lse;
+  p.part = static_cast<float*>(workspace);
+  int status = WQ_OK;
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
-    attn_kernel<decltype(dt)::value, decltype(d)::value>
-        <<<dim3((unsigned)(rows->n_rows * rows->n_heads)), kAttnThreads, 0, (hipStream_t)stream>>>(
-            a, cache->data, cache->n_pages, (int)cache->n_kv_heads, scale, win, sel, (int)n_sel,
-            out, lse);
+    constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
+    auto launch = [&](auto kernel) {
+      const size_t lds = (size_t)kAttnWaves * plan.ct * (D / 4 + 2) * 64 * 4;
+      if (!allow_lds((const void*)kernel, lds)) {
+        status = wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
+        return;
+      }
+      kernel<<<dim3((unsigned)grid), kAttnWaves * kWave, lds, (hipStream_t)stream>>>(p);
+    };
+    if (sel != nullptr) {
+      if (plan.ct == 1) launch(attn_kernel<DT, D, 1, true>);
+      else if constexpr (D <= 128) launch(attn_kernel<DT, D, 2, true>);
+    } else {
+      if (plan.ct == 1) launch(attn_kernel<DT, D, 1, false>);
+      else if constexpr (D <= 128) launch(attn_kernel<DT, D, 2, false>);
+    }
+    if (status == WQ_OK && plan.splits > 1)
+      join_kernel<DT, D><<<dim3((unsigned)((items + kAttnWaves - 1) / kAttnWaves)),
+                           kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
+          p.part, items, p.splits, out, lse);
   });
-  return check_launch(who);
+  return status == WQ_OK ? check_launch(who) : status;
 }
