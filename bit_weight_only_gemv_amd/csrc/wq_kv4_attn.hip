@@ -14,14 +14,17 @@
 // product's B operand: the weights never leave their registers.
 //
 // Precision.  Queries are scaled by a power of two to [2^14, 2^15) and so are
-// exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  The weights
-// times their scales enter as an FP16 head and, for FP16 outputs, an FP16
-// remainder (22 bits); for BF16 outputs the head alone (2^-12, against the
-// output's 2^-9).  They carry 2^8, and value scales of 2 and more lower that by a
-// running power of two, so that neither end of FP16's range is met: a weight
-// 2^-30 of the largest still counts.  The running maximum is only raised when a
-// logit passes it by 2^6, which spares most pages the cross-lane maximum and
-// the rescale of the sums.
+// exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  A softmax
+// weight is rounded to FP16 once, and that rounded weight is what every sum
+// uses, the denominator's too: it moves a result by at most 2^-11 of the values'
+// spread, and by 2^-12 / sqrt(n) of it where n tokens count.  A weight times a
+// scale enters the product exactly, as an FP16 head and remainder: the codes'
+// part and the offsets' part nearly cancel where a group lies far from 0, so a
+// rounding there would not stay small.  Weights carry 2^8, and value scales of 2
+// and more lower that by a running power of two, so that neither end of FP16's
+// range is met: a weight 2^-30 of the largest still counts.  The running maximum
+// is only raised when a logit passes it by 2^6, which spares most pages the
+// cross-lane maximum and the rescale of the sums.
 
 #include "wq_common.cuh"
 #include "wq_device.h"
@@ -32,7 +35,7 @@
 namespace wqd {
 
 constexpr int kAttnWaves = 4;
-constexpr int kFoldPages = 2;
+constexpr int kFoldPages = 8;
 constexpr float kWeightExp = 8.f;    // weights carry 2^8 ...
 constexpr float kRaise = 6.f;        // ... and grow by up to 2^6 before the maximum is raised
 
@@ -64,17 +67,15 @@ __device__ __forceinline__ h8 code_operand(uint32_t w) {
 // cores drops what lies below its largest operand's exponent, which subnormals
 // make 2^10 too large: here that would be a bias of 2^-19, and it matters where
 // many values average out.
-__device__ __forceinline__ h8 normal_operand(uint32_t w) {
-  uint32_t v[4];
-  w4_word_magic(w, v[0], v[1], v[2], v[3]);
-  h8 o;
+__device__ __forceinline__ h8 normal_operand(uint32_t w, uint32_t magic) {
+  const uint32_t w8 = w >> 8;
+  const uint32_t v[4] = {(w & 0x000F000Fu) | magic, (w & 0x00F000F0u) | magic,
+                         (w8 & 0x000F000Fu) | magic, (w8 & 0x00F000F0u) | magic};
+  u4v o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const h2 x = as_h2(v[i]) - h2{(_Float16)1024.f, (_Float16)1024.f};
-    o[2 * i] = x[0];
-    o[2 * i + 1] = x[1];
-  }
-  return o;
+  for (int i = 0; i < 4; ++i)
+    o[i] = as_u32(as_h2(v[i]) - h2{(_Float16)1024.f, (_Float16)1024.f});
+  return __builtin_bit_cast(h8, o);
 }
 
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
@@ -133,6 +134,12 @@ struct Tile {
   }
 };
 
+// Logarithm of a sum of weights that carry 2^kWeightExp, at maximum mx (base 2).
+__device__ __forceinline__ float log_sum(float sum, float mx) {
+  return sum == 0.f ? -INFINITY
+                    : ((mx == -INFINITY ? 0.f : mx) - kWeightExp) * 0.69314718f + __logf(sum);
+}
+
 struct AttnArgs {
   KvRows a;
   const uint8_t* data;
@@ -142,7 +149,7 @@ struct AttnArgs {
   const int32_t* sel;
   uint16_t* out;
   float* lse;
-  float* part;            // [row][head][split][D], then [row][head][split][2]
+  float* part;            // [row][head][split][D], then [row][head][split][4]: sum, maximum, exact sum
 };
 
 template <int DT, int D, int CT, bool SEL>
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
   using Tl = Tile<D>;
   constexpr int G = Tl::G, J = Tl::J;
   constexpr int NT = CT == 1 && D <= 128 ? 2 : 1;     // tiles taken together
-  constexpr int kPart = (4 * J + 2) * 64;    // floats a wave keeps for a column tile
+  constexpr int kPart = (4 * J + 3) * 64;    // floats a wave keeps for a column tile
   extern __shared__ __attribute__((aligned(16))) float s_merge[];
   const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -255,11 +262,13 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
 
     f4 O[CT][J], OZ[CT];
     float m[CT], m_kept[CT];
+    float exact[CT];        // this lane's weights before their rounding, for lse
     int vexp = 0;           // value scales since the last fold are below 2^(vexp + 1)
     bool kept = false;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       m[ct] = m_kept[ct] = -INFINITY;
+      exact[ct] = 0.f;
       OZ[ct] = f4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < J; ++j) O[ct][j] = f4{0, 0, 0, 0};
@@ -303,6 +312,8 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
       id = __builtin_amdgcn_readfirstlane(id);
       if (id >= p.n_pages) id = -1;
     };
+    uint32_t magic = 0x64006400u;   // in a VGPR: the mask and it are then one instruction
+    asm("" : "+v"(magic));
     const int64_t stride = (int64_t)p.kv_heads * (80 * D);
     const uint8_t* const base = p.data + (int64_t)kvh * (80 * D);
 
@@ -371,6 +382,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
             y[ct][i] = __builtin_fmaf(sc[ct][i >> 2][i & 3], c1[ct],
                                       __builtin_fmaf(zt[ct][i >> 2][i & 3], c2[ct], -m8));
           if (edge) {
+            asm volatile("");      // stays a branch: few pages have an edge
 #pragma unroll
             for (int i = 0; i < NY; ++i) {
               const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
@@ -401,6 +413,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
 #pragma unroll
             for (int j2 = 0; j2 < J; ++j2) O[ct][j2] *= f;
             OZ[ct] *= f;
+            exact[ct] *= f;
           }
         }
         // value scales of 2 and more: lower the weights' power of two
@@ -429,7 +442,8 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
               for (int j2 = 0; j2 < J; ++j2) O[ct][j2] *= f;
           }
         }
-        const float vdown = ldexpf(1.f, -vexp);
+        const _Float16 d1 = (_Float16)ldexpf(1.f, -vexp), d16 = (_Float16)ldexpf(0.0625f, -vexp);
+        const h2 down = {d1, d1}, down16 = {d16, d16};
 
         const uint32_t fill = l == 8 ? 0x3C003C00u : 0u;
 #pragma unroll
@@ -437,37 +451,45 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
           u4v z = tp[t].vz;
           if (l >= G) z = u4v{fill, fill, fill, fill};
           const h8 za = __builtin_bit_cast(h8, z);
-          float ws[CT][8];
+          h2 ws[CT][4];
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
-            h8 hi, lo;
+            u4v wv;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float w = __builtin_amdgcn_exp2f(y[ct][8 * t + e]);
-              hi[e] = (_Float16)w;
-              lo[e] = (_Float16)(w - (float)hi[e]);
-              ws[ct][e] = w * (e & 2 ? vdown * 0.0625f : vdown);
+            for (int e = 0; e < 8; ++e)
+              y[ct][8 * t + e] = __builtin_amdgcn_exp2f(y[ct][8 * t + e]);
+            if (p.lse != nullptr) {
+              asm volatile("");    // stays a branch
+#pragma unroll
+              for (int e = 0; e < 8; ++e) exact[ct] += y[ct][8 * t + e];
             }
-            OZ[ct] = mfma(za, hi, OZ[ct]);
-            OZ[ct] = mfma(za, lo, OZ[ct]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const h2 w = {(_Float16)y[ct][8 * t + 2 * x], (_Float16)y[ct][8 * t + 2 * x + 1]};
+              wv[x] = as_u32(w);
+              ws[ct][x] = w * (x & 1 ? down16 : down);
+            }
+            OZ[ct] = mfma(za, __builtin_bit_cast(h8, wv), OZ[ct]);
           }
           unroll<G>([&](auto g) {
             h2 s[4];
             unroll<4>([&](auto x) { s[x] = Tl::template scale2<g * 4 + x>(tp[t].vs); });
-            const h8 v0 = normal_operand(tp[t].vc[2 * g]), v1 = normal_operand(tp[t].vc[2 * g + 1]);
+            const h8 v0 = normal_operand(tp[t].vc[2 * g], magic);
+            const h8 v1 = normal_operand(tp[t].vc[2 * g + 1], magic);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-              h8 hi, lo;
+              u4v hi, lo;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float sv = (float)s[e >> 1][e & 1];
-                hi[e] = (_Float16)(ws[ct][e] * sv);
-                lo[e] = (_Float16)__builtin_fmaf(ws[ct][e], sv, -(float)hi[e]);
+              for (int x = 0; x < 4; ++x) {
+                const h2 h = ws[ct][x] * s[x];
+                hi[x] = as_u32(h);
+                lo[x] = as_u32(__builtin_elementwise_fma(ws[ct][x], s[x], -h));
               }
-              O[ct][2 * g] = mfma(v0, hi, O[ct][2 * g]);
-              O[ct][2 * g + 1] = mfma(v1, hi, O[ct][2 * g + 1]);
-              O[ct][2 * g] = mfma(v0, lo, O[ct][2 * g]);
-              O[ct][2 * g + 1] = mfma(v1, lo, O[ct][2 * g + 1]);
+              const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
+              O[ct][2 * g] = mfma(v0, hb, O[ct][2 * g]);
+              O[ct][2 * g + 1] = mfma(v1, hb, O[ct][2 * g + 1]);
+              O[ct][2 * g] = mfma(v0, lb, O[ct][2 * g]);
+              O[ct][2 * g + 1] = mfma(v1, lb, O[ct][2 * g + 1]);
             }
           });
         }
@@ -475,6 +497,14 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
     }
 
     fold();
+    if (p.lse != nullptr) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        exact[ct] += __shfl_xor(exact[ct], 16);
+        exact[ct] += __shfl_xor(exact[ct], 32);
+        s_merge[(wave * CT + ct) * kPart + (4 * J + 2) * 64 + lane] = exact[ct];
+      }
+    }
     // the waves' parts joined in order
     __syncthreads();
 #pragma unroll
@@ -509,15 +539,16 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
         }
       }
       if (wave == 0 && r == 0) {
+        float ex = 0.f;
+        if (p.lse != nullptr)
+#pragma unroll
+          for (int w = 0; w < kAttnWaves; ++w)
+            ex += mw[w] * s_merge[(w * CT + ct) * kPart + (4 * J + 2) * 64 + lane];
         if (p.splits == 1) {
-          if (p.lse != nullptr)
-            p.lse[at] = sum == 0.f ? -INFINITY
-                                   : (mx == -INFINITY ? 0.f : mx) * 0.69314718f +
-                                         __logf(sum) - kWeightExp * 0.69314718f;
+          if (p.lse != nullptr) p.lse[at] = log_sum(ex, mx);
         } else {
-          float* ml = p.part + (int64_t)a.rows * a.heads * p.splits * D + (at * p.splits + split) * 2;
-          ml[0] = sum;
-          ml[1] = mx;
+          reinterpret_cast<f4*>(p.part + (int64_t)a.rows * a.heads * p.splits * D)[at * p.splits + split] =
+              f4{sum, mx, ex, 0.f};
         }
       }
     }
@@ -535,26 +566,25 @@ join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t*
   const int64_t at = (int64_t)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (at >= items) return;
-  const float* ml = part + items * splits * D + at * splits * 2;
+  const f4* ml = reinterpret_cast<const f4*>(part + items * splits * D) + at * splits;
   const float* o = part + at * splits * D + lane * C;
   float mx = -INFINITY;
-  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, ml[2 * s + 1]);
-  float sum = 0.f, acc[C];
+  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, ml[s][1]);
+  float sum = 0.f, ex = 0.f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
   for (int s = 0; s < splits; ++s) {
-    const float w = ml[2 * s + 1] == mx ? 1.f : __builtin_amdgcn_exp2f(ml[2 * s + 1] - mx);
-    sum += w * ml[2 * s];
+    const f4 x = ml[s];
+    const float w = x[1] == mx ? 1.f : __builtin_amdgcn_exp2f(x[1] - mx);
+    sum += w * x[0];
+    ex += w * x[2];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] += w * o[(int64_t)s * D + c];
   }
 #pragma unroll
   for (int c = 0; c < C; ++c)
     out[at * D + lane * C + c] = from_float<DT>(sum == 0.f ? 0.f : acc[c] / sum);
-  if (lane == 0 && lse != nullptr)
-    lse[at] = sum == 0.f ? -INFINITY
-                         : (mx == -INFINITY ? 0.f : mx) * 0.69314718f + __logf(sum) -
-                               kWeightExp * 0.69314718f;
+  if (lane == 0 && lse != nullptr) lse[at] = log_sum(ex, mx);
 }
 
 // How a call is split: column tiles a sequence (or row) and splits of its pages.
@@ -604,7 +634,7 @@ extern "C" int64_t wq_kv4_attention_workspace(const wq_kv4_cache* cache, const w
   wq::ok();
   const AttnPlan p = attn_plan(cache, rows, max_rows, max_len, n_sel, n_sel > 0);
   if (p.splits == 1) return 0;
-  return (rows->n_rows * rows->n_heads * p.splits * (cache->head_dim + 2) * 4 + 15) / 16 * 16;
+  return (rows->n_rows * rows->n_heads * p.splits * (cache->head_dim + 4) * 4 + 15) / 16 * 16;
 }
 
 extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
@@ -648,7 +678,7 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
     constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
     auto launch = [&](auto kernel) {
-      const size_t lds = (size_t)kAttnWaves * plan.ct * (D / 4 + 2) * 64 * 4;
+      const size_t lds = (size_t)kAttnWaves * plan.ct * (D / 4 + 3) * 64 * 4;
       if (!allow_lds((const void*)kernel, lds)) {
         status = wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
         return;
