@@ -40,6 +40,8 @@ struct SeqRow {
 };
 __device__ __forceinline__ SeqRow find_row(const KvRows& a, int row) {
   int lo = 0, hi = a.seqs;
+  if (row < hi && a.cu[row] == row && a.cu[row + 1] == row + 1)   // one row each: no search
+    return {row, max(a.lens[row] - 1, -1)};
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
     if (a.cu[m] <= row) lo = m; else hi = m;

@@ -5,6 +5,7 @@
 #include "wq_common.cuh"
 #include "wq_device.h"
 #include "wq_kv4.cuh"
+#include "wq_select.cuh"
 
 namespace wqd {
 
@@ -229,36 +230,90 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 
 // ----------------------------------------------------------------- select
 // Scores (float32 in the workspace, [row][head][page]), then the n_sel highest.
-constexpr int kScoreThreads = 64;
+//
+// A page's bound is sum_d max(q min, q max) = sum_d q mid + |q| half with mid =
+// (max + min) / 2 and half = (max - min) / 2.  FP16 values and their products are
+// far inside 64 bits, so those sums are exact but for operands that lie 2^20
+// apart, and the choice does not depend on their order: two fused multiply-adds
+// a channel and head, at the rate of 32-bit ones.  A wave takes 512 / D pages at
+// a time, 8 channels a lane, up to 8 heads' queries in registers.
+constexpr int kScoreWaves = 4;
+constexpr int kScoreHeads = 8;       // heads of one pass
+
+__device__ __forceinline__ double lane_add(double v, int d) { return v + __shfl_xor(v, d); }
+
+// v + v of the lane at the DPP control, within rows of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ double row_add(double v) {
+  const u2 b = __builtin_bit_cast(u2, v);
+  const u2 m = {dpp_mov<CTRL>(b[0]), dpp_mov<CTRL>(b[1])};
+  return v + __builtin_bit_cast(double, m);
+}
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kScoreThreads)
+__global__ void __launch_bounds__(kScoreWaves * kWave)
 score_kernel(KvRows a, const uint16_t* __restrict__ summary, int64_t n_pages, int kv_heads,
-             float* __restrict__ scores) {
-  __shared__ double s_q[D];
-  const int row = blockIdx.y, head = blockIdx.z;
+             int n_sel, int chunk, float* __restrict__ scores) {
+  constexpr int L = D / 8, P = kWave / L;   // lanes a page, pages a wave
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int head = blockIdx.x % kv_heads, row = blockIdx.x / kv_heads;
   const SeqRow sr = find_row(a, row);
   const int pages = sr.pos >= 0 ? (int)min((int64_t)(sr.pos / 64 + 1), a.width) : 0;
-  const int p = blockIdx.x * kScoreThreads + threadIdx.x;
-  if ((int)(blockIdx.x * kScoreThreads) >= pages) return;
-  const int R = a.heads / kv_heads;
-  const int page = p < pages ? a.table[sr.b * a.width + p] : -1;
-  const bool ok = page >= 0 && page < n_pages;
-  const uint16_t* sm = summary + ((int64_t)(ok ? page : 0) * kv_heads + head) * (2 * D);
-  double best = -INFINITY;
-  for (int h = 0; h < R; ++h) {
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kScoreThreads)
-      s_q[d] = (double)to_float<DT>(a.q[row * a.q_row + (head * R + h) * a.q_head + d]);
-    __syncthreads();
-    double s = 0;
-    for (int d = 0; d < D; ++d)
-      s += s_q[d] * (double)h2f(s_q[d] > 0 ? sm[D + d] : sm[d]);
-    best = s > best ? s : best;
+  if (pages <= n_sel) return;               // all of them are taken
+  const int p_end = min((int)(blockIdx.y + 1) * chunk, pages);
+  const int p_first = blockIdx.y * chunk + wave * P + lane / L;
+  if ((int)blockIdx.y * chunk >= pages) return;
+  const int R = a.heads / kv_heads, c0 = (lane % L) * 8;
+  const int32_t* const table = a.table + (int64_t)sr.b * a.width;
+  float* const out = scores + ((int64_t)row * kv_heads + head) * a.width;
+  for (int h0 = 0; h0 < R; h0 += kScoreHeads) {
+    double q[kScoreHeads][8];
+#pragma unroll
+    for (int h = 0; h < kScoreHeads; ++h) {
+      // heads past the last repeat it, which changes no maximum
+      const uint16_t* src = a.q + row * a.q_row + (head * R + min(h0 + h, R - 1)) * a.q_head + c0;
+      const u4v v = *reinterpret_cast<const u4v*>(src);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[h][i] = (double)to_float<DT>((uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+    }
+    for (int p = p_first; p - lane / L < p_end; p += kScoreWaves * P) {
+      const int page = p < p_end ? table[p] : -1;
+      const bool ok = page >= 0 && page < n_pages;
+      const uint16_t* sm = summary + ((int64_t)(ok ? page : 0) * kv_heads + head) * (2 * D) + c0;
+      const u4v lo = *reinterpret_cast<const u4v*>(sm), hi = *reinterpret_cast<const u4v*>(sm + D);
+      double s[kScoreHeads];
+#pragma unroll
+      for (int h = 0; h < kScoreHeads; ++h) s[h] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double mn = (double)h2f((uint16_t)(lo[i >> 1] >> (16 * (i & 1))));
+        const double mx = (double)h2f((uint16_t)(hi[i >> 1] >> (16 * (i & 1))));
+        const double mid = (mx + mn) * 0.5, half = (mx - mn) * 0.5;
+#pragma unroll
+        for (int h = 0; h < kScoreHeads; ++h) {
+          s[h] = __builtin_fma(q[h][i], mid, s[h]);
+          s[h] = __builtin_fma(__builtin_fabs(q[h][i]), half, s[h]);
+        }
+      }
+      double best = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < kScoreHeads; ++h) {
+        double v = s[h];
+        v = row_add<0xB1>(v);                 // quad_perm [1,0,3,2]
+        v = row_add<0x4E>(v);                 // quad_perm [2,3,0,1]
+        v = row_add<0x141>(v);                // row_half_mirror
+        if constexpr (L >= 16) v = row_add<0x140>(v);   // row_mirror
+        if constexpr (L == 32) v = lane_add(v, 16);
+        best = v > best ? v : best;
+      }
+      if (lane % L == 0 && p < p_end) {
+        float f = p == 0 || p == pages - 1 ? INFINITY : (ok ? (float)best : -INFINITY);
+        if (h0 > 0) f = fmaxf(f, out[p]);
+        out[p] = f;
+      }
+    }
   }
-  if (p < pages)
-    scores[((int64_t)row * kv_heads + head) * a.width + p] =
-        p == 0 || p == pages - 1 ? INFINITY : (ok ? (float)best : -INFINITY);
 }
 
 // Order of a float32 score as an unsigned key (NaN lowest).
@@ -268,66 +323,95 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// The n_sel highest scores of one (row, head), rising: the n_sel-th highest key
+// 8 bits at a time from histograms in LDS, then each thread a stretch of pages
+// with its place from sums over the threads before it.
 constexpr int kPickThreads = 256;
+constexpr int kPickHeld = 8192;      // keys held in LDS; more are read again
+
+// Sum of v over the threads before this one, and over all in `total`.
+__device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_wave, uint32_t& total) {
+  uint32_t t;
+  const uint32_t in_wave = wave_excl_sum(v, t);
+  const int w = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_wave[w] = t;
+  __syncthreads();
+  uint32_t base = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kPickThreads / kWave; ++i) {
+    if (i < w) base += s_wave[i];
+    total += s_wave[i];
+  }
+  return base + in_wave;
+}
 
 __global__ void __launch_bounds__(kPickThreads)
 pick_kernel(KvRows a, int kv_heads, const float* __restrict__ scores, int n_sel,
             int32_t* __restrict__ sel) {
-  __shared__ uint32_t s_hist[256];
-  __shared__ uint32_t s_prefix, s_rank;
-  __shared__ int s_count[2][kPickThreads];
-  const int row = blockIdx.x / kv_heads;
+  __shared__ uint32_t s_hist[4][256];
+  __shared__ uint32_t s_found[2], s_wave[kPickThreads / kWave];
+  extern __shared__ uint32_t s_key[];
+  const int tid = threadIdx.x, row = blockIdx.x / kv_heads;
   const SeqRow sr = find_row(a, row);
   const int pages = sr.pos >= 0 ? (int)min((int64_t)(sr.pos / 64 + 1), a.width) : 0;
   const float* sc = scores + (int64_t)blockIdx.x * a.width;
   int32_t* out = sel + (int64_t)blockIdx.x * n_sel;
   const int n = min(n_sel, pages);
-  for (int j = n + threadIdx.x; j < n_sel; j += kPickThreads) out[j] = -1;
+  for (int j = n + tid; j < n_sel; j += kPickThreads) out[j] = -1;
   if (n == pages) {
-    for (int j = threadIdx.x; j < n; j += kPickThreads) out[j] = j;
+    for (int j = tid; j < n; j += kPickThreads) out[j] = j;
     return;
   }
-  // the n-th highest key, 8 bits at a time
-  if (threadIdx.x == 0) { s_prefix = 0; s_rank = n; }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    for (int p = threadIdx.x; p < pages; p += kPickThreads) {
-      const uint32_t key = score_key(sc[p]);
-      if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&s_hist[(key >> shift) & 255], 1u);
+  const bool held = pages <= kPickHeld;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s_hist[i][tid] = 0;
+  __syncthreads();
+  auto key_at = [&](int p) { return held ? s_key[p] : score_key(sc[p]); };
+  uint32_t cut = 0, rank = (uint32_t)n;
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int p = tid; p < pages; p += kPickThreads) {
+      uint32_t key;
+      if (pass == 0) {
+        key = score_key(sc[p]);
+        if (held) s_key[p] = key;
+      } else {
+        key = key_at(p);
+        if ((key >> (shift + 8)) != cut) continue;
+      }
+      atomicAdd(&s_hist[pass][(key >> shift) & 255], 1u);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t above = 0;
-      int bin = 255;
-      while (above + s_hist[bin] < s_rank) above += s_hist[bin--];
-      s_rank -= above;
-      s_prefix = (prefix << 8) | (uint32_t)bin;
+    // thread t holds bin 255 - t: the one where the sum from above reaches the rank
+    uint32_t total;
+    const uint32_t mine = s_hist[pass][255 - tid];
+    const uint32_t above = block_before(mine, s_wave, total);
+    if (above < rank && rank <= above + mine) {
+      s_found[0] = (cut << 8) | (uint32_t)(255 - tid);
+      s_found[1] = rank - above;
     }
     __syncthreads();
+    cut = s_found[0];
+    rank = s_found[1];
   }
-  const uint32_t cut = s_prefix;
-  const int ties = (int)s_rank;        // of the keys equal to the cut, the first ones
-  // each thread a stretch of pages: counts, sums over threads, then the picks in order
+  // keys above the cut, and of those equal to it the first `rank`
   const int per = (pages + kPickThreads - 1) / kPickThreads;
-  const int p0 = min((int)threadIdx.x * per, pages), p1 = min(p0 + per, pages);
-  int above = 0, equal = 0;
+  const int p0 = min(tid * per, pages), p1 = min(p0 + per, pages);
+  uint32_t above = 0, equal = 0, total;
   for (int p = p0; p < p1; ++p) {
-    const uint32_t key = score_key(sc[p]);
+    const uint32_t key = key_at(p);
     above += key > cut;
     equal += key == cut;
   }
-  s_count[0][threadIdx.x] = above;
-  s_count[1][threadIdx.x] = equal;
-  __syncthreads();
-  int at = 0, eq = 0;
-  for (int j = 0; j < (int)threadIdx.x; ++j) { at += s_count[0][j]; eq += s_count[1][j]; }
-  at += min(eq, ties);
+  uint32_t at = block_before(above, s_wave, total);
+  uint32_t eq = block_before(equal, s_wave, total);
+  at += min(eq, rank);
   for (int p = p0; p < p1; ++p) {
-    const uint32_t key = score_key(sc[p]);
+    const uint32_t key = key_at(p);
     if (key > cut) out[at++] = p;
-    else if (key == cut && eq++ < ties) out[at++] = p;
+    else if (key == cut && eq++ < rank) out[at++] = p;
   }
 }
 
@@ -478,18 +562,28 @@ extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
                     (long long)workspace_bytes, (long long)need);
   if (!aligned4(sel) || !aligned16(workspace))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
-  if (rows->n_rows > 65535 || rows->n_rows * cache->n_kv_heads > 0x7FFFFFFFll)
-    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: at most 65535 rows", who);
+  if (rows->n_rows * cache->n_kv_heads > 0x7FFFFFFFll)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
   const KvRows a = kv4_rows(rows);
   float* scores = static_cast<float*>(workspace);
-  const dim3 grid((unsigned)((rows->table_width + kScoreThreads - 1) / kScoreThreads),
-                  (unsigned)rows->n_rows, (unsigned)cache->n_kv_heads);
+  // a workgroup takes `chunk` pages of a (row, head): up to 8 of its waves' turns
+  // (the queries' conversion is spread over them), fewer where that would leave
+  // compute units idle
+  const int64_t turn = kScoreWaves * (512 / cache->head_dim);
+  const int64_t pairs = rows->n_rows * cache->n_kv_heads;
+  int64_t turns = pairs * rows->table_width / (turn * 1024);
+  turns = turns < 1 ? 1 : turns > 8 ? 8 : turns;
+  while (rows->table_width > turn * turns * 65535) turns *= 2;   // the grid's limit
+  const int64_t chunk = turn * turns;
+  const dim3 grid((unsigned)pairs, (unsigned)((rows->table_width + chunk - 1) / chunk));
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
     score_kernel<decltype(dt)::value, decltype(d)::value>
-        <<<grid, kScoreThreads, 0, (hipStream_t)stream>>>(a, cache->summary, cache->n_pages,
-                                                          (int)cache->n_kv_heads, scores);
+        <<<grid, kScoreWaves * kWave, 0, (hipStream_t)stream>>>(
+            a, cache->summary, cache->n_pages, (int)cache->n_kv_heads, (int)n_sel, (int)chunk,
+            scores);
   });
-  pick_kernel<<<dim3((unsigned)(rows->n_rows * cache->n_kv_heads)), kPickThreads, 0,
-                (hipStream_t)stream>>>(a, (int)cache->n_kv_heads, scores, (int)n_sel, sel);
+  const int64_t held = rows->table_width < kPickHeld ? rows->table_width : kPickHeld;
+  pick_kernel<<<dim3((unsigned)pairs), kPickThreads, (size_t)held * 4, (hipStream_t)stream>>>(
+      a, (int)cache->n_kv_heads, scores, (int)n_sel, sel);
   return check_launch(who);
 }

@@ -556,35 +556,57 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
   }
 }
 
-// Joins the splits of every (row, head), one wave each: split s's weight is
-// 2^(m_s - max m).
+// Joins the splits of one (row, head): split s's weight is 2^(m_s - max m).  16
+// bytes a lane and D / 4 lanes a split, so that 1024 / D splits are read at a
+// time; their sums are added in order.
 template <int DT, int D>
 __global__ void __launch_bounds__(kAttnWaves * kWave)
 join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t* __restrict__ out,
             float* __restrict__ lse) {
-  constexpr int C = D / 64;
-  const int64_t at = (int64_t)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (at >= items) return;
+  constexpr int L = D / 4, S = kAttnWaves * kWave / L;
+  __shared__ f4 s_acc[S][L];
+  __shared__ float s_sum[S][3];
+  const int64_t at = blockIdx.x;
+  const int x = threadIdx.x % L, y = threadIdx.x / L;
   const f4* ml = reinterpret_cast<const f4*>(part + items * splits * D) + at * splits;
-  const float* o = part + at * splits * D + lane * C;
-  float mx = -INFINITY;
-  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, ml[s][1]);
-  float sum = 0.f, ex = 0.f, acc[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const f4 x = ml[s];
-    const float w = x[1] == mx ? 1.f : __builtin_amdgcn_exp2f(x[1] - mx);
-    sum += w * x[0];
-    ex += w * x[2];
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] += w * o[(int64_t)s * D + c];
+  const f4* o = reinterpret_cast<const f4*>(part + at * splits * D) + x;
+  float mx = -INFINITY, sum = 0.f, ex = 0.f;
+  f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = y; s < splits; s += S) {
+    const f4 h = ml[s], v = o[(int64_t)s * L];
+    const float top = fmaxf(mx, h[1]);
+    const float f = mx == top ? 1.f : __builtin_amdgcn_exp2f(mx - top);
+    const float w = h[1] == top ? 1.f : __builtin_amdgcn_exp2f(h[1] - top);
+    mx = top;
+    sum = sum * f + w * h[0];
+    ex = ex * f + w * h[2];
+    acc = acc * f + w * v;
   }
+  s_acc[y][x] = acc;
+  if (x == 0) {
+    s_sum[y][0] = mx;
+    s_sum[y][1] = sum;
+    s_sum[y][2] = ex;
+  }
+  __syncthreads();
+  if (y != 0) return;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    out[at * D + lane * C + c] = from_float<DT>(sum == 0.f ? 0.f : acc[c] / sum);
-  if (lane == 0 && lse != nullptr) lse[at] = log_sum(ex, mx);
+  for (int s = 1; s < S; ++s) mx = fmaxf(mx, s_sum[s][0]);
+  sum = ex = 0.f;
+  acc = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const float w = s_sum[s][0] == mx ? 1.f : __builtin_amdgcn_exp2f(s_sum[s][0] - mx);
+    sum += w * s_sum[s][1];
+    ex += w * s_sum[s][2];
+    acc += w * s_acc[s][x];
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = from_float<DT>(sum == 0.f ? 0.f : acc[i] / sum);
+  *reinterpret_cast<u2*>(out + at * D + 4 * x) = u2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+  if (x == 0 && lse != nullptr) lse[at] = log_sum(ex, mx);
 }
 
 // How a call is split: column tiles a sequence (or row) and splits of its pages.
@@ -693,8 +715,7 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
       else if constexpr (D <= 128) launch(attn_kernel<DT, D, 2, false>);
     }
     if (status == WQ_OK && plan.splits > 1)
-      join_kernel<DT, D><<<dim3((unsigned)((items + kAttnWaves - 1) / kAttnWaves)),
-                           kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
+      join_kernel<DT, D><<<dim3((unsigned)items), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
           p.part, items, p.splits, out, lse);
   });
   return status == WQ_OK ? check_launch(who) : status;
