@@ -1,8 +1,8 @@
 // Attention over the paged 4-bit key/value cache (wq.h, "4-bit key/value
 // cache"), on the matrix cores.
 //
-// A wave takes pages of 64 tokens and CT column tiles of 16 (row, head) pairs
-// of one key/value head.  With key code c, scale S and offset Z of a token and
+// A workgroup takes 16 columns, (row, head) pairs of one key/value head, and its
+// waves pages of 64 tokens in turn.  With key code c, scale S and offset Z of a token and
 // group g, and the group's part of the query Q_g,
 //   logit = scale (sum_g S_g (c_g . Q_g) + sum_g Z_g sum(Q_g)),
 // and with the softmax weights p,
@@ -85,52 +85,70 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
 // One tile of 32 tokens of one head in registers: lane (row r = lane / 16,
 // l = lane % 16).
 template <int D>
-struct Tile {
+struct TileShape {
   static constexpr int G = D / 32, W = G < 4 ? G : 4, J = D / 16, M = G == 8 ? 2 : 1, ZN = G / 2;
-  uint32_t kc[2][G];      // 16-token part, group: 8 codes of token l
-  uint32_t vc[J];         // 16 channels: 8 codes of channel l
-  uint32_t ks[M], vs[M];  // row r's scales, M dwords a lane (2 slots each)
-  uint32_t kz[2][ZN];     // token l's offsets, all groups
-  u4v vz;                 // group l's offsets of 8 tokens
-  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int lane) {
-    const int r = lane >> 4, l = lane & 15;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int c = 0; c < G / W; ++c)
-        __builtin_memcpy(&kc[u][c * W], q + u * (8 * D) + c * (256 * W) + lane * (4 * W), 4 * W);
-    const int at = G == 2 ? (l & 7) * 4 : l * (4 * M);
-    __builtin_memcpy(&ks[0], q + 32 * D + r * (16 * G) + at, 4 * M);
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      __builtin_memcpy(&kz[u][0], q + 34 * D + (16 * u + l) * (2 * G), 2 * G);
-#pragma unroll
-    for (int c = 0; c < J / 4; ++c)
-      __builtin_memcpy(&vc[c * 4], q + 16 * D + c * 1024 + lane * 16, 16);
-    __builtin_memcpy(&vs[0], q + 36 * D + r * (16 * G) + at, 4 * M);
-    __builtin_memcpy(&vz, q + 38 * D + r * (16 * G) + (l < G ? l : 0) * 16, 16);
-  }
-  // Clears the value scales and offsets of tokens n and later (they were never
-  // written and may be anything).
-  __device__ __forceinline__ void cut(int n, int lane) {
-    const int r = lane >> 4, l = lane & 15;
-#pragma unroll
-    for (int x = 0; x < M; ++x) {
-      const int j = (M == 1 ? l : 2 * l + x) & 3;
-      const int tok = 16 * (j >> 1) + 4 * r + 2 * (j & 1);
-      vs[x] = tok >= n ? 0 : tok + 1 >= n ? vs[x] & 0xFFFFu : vs[x];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int tok = 16 * (j >> 1) + 4 * r + 2 * (j & 1);
-      vz[j] = tok >= n ? 0 : tok + 1 >= n ? vz[j] & 0xFFFFu : vz[j];
-    }
+  // Byte of row r's scales that lane l holds: M dwords (2 slots each) of 4 G.
+  static __device__ __forceinline__ int scale_at(int r, int l) {
+    return r * (16 * G) + (G == 2 ? (l & 7) * 4 : l * (4 * M));
   }
   // Dword j (slots 2j, 2j + 1) of group g of row r's scales (GJ = 4 g + j), in all lanes.
   template <int GJ>
   static __device__ __forceinline__ h2 scale2(const uint32_t (&s)[M]) {
     if constexpr (M == 1) return as_h2(row_lane<GJ>(s[0]));
     else return as_h2(row_lane<GJ / 2>(s[GJ & 1]));
+  }
+};
+
+template <int D>
+struct KeyTile : TileShape<D> {
+  using S = TileShape<D>;
+  uint32_t codes[2][S::G];      // 16-token part, group: 8 codes of token l
+  uint32_t scales[S::M];
+  uint32_t offsets[2][S::ZN];   // token l's, all groups
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int lane) {
+    constexpr int G = S::G, W = S::W;
+    const int r = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < G / W; ++c)
+        __builtin_memcpy(&codes[u][c * W], q + u * (8 * D) + c * (256 * W) + lane * (4 * W), 4 * W);
+    __builtin_memcpy(&scales[0], q + 32 * D + S::scale_at(r, l), 4 * S::M);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      __builtin_memcpy(&offsets[u][0], q + 34 * D + (16 * u + l) * (2 * G), 2 * G);
+  }
+};
+
+template <int D>
+struct ValueTile : TileShape<D> {
+  using S = TileShape<D>;
+  uint32_t codes[S::J];         // 16 channels: 8 codes of channel l
+  uint32_t scales[S::M];
+  u4v offsets;                  // group l's, of 8 tokens
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int lane) {
+    const int r = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int c = 0; c < S::J / 4; ++c)
+      __builtin_memcpy(&codes[c * 4], q + 16 * D + c * 1024 + lane * 16, 16);
+    __builtin_memcpy(&scales[0], q + 36 * D + S::scale_at(r, l), 4 * S::M);
+    __builtin_memcpy(&offsets, q + 38 * D + r * (16 * S::G) + (l < S::G ? l : 0) * 16, 16);
+  }
+  // Clears the scales and offsets of tokens n and later (they were never
+  // written and may be anything).
+  __device__ __forceinline__ void cut(int n, int lane) {
+    const int r = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int x = 0; x < S::M; ++x) {
+      const int j = (S::M == 1 ? l : 2 * l + x) & 3;
+      const int tok = 16 * (j >> 1) + 4 * r + 2 * (j & 1);
+      scales[x] = tok >= n ? 0 : tok + 1 >= n ? scales[x] & 0xFFFFu : scales[x];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tok = 16 * (j >> 1) + 4 * r + 2 * (j & 1);
+      offsets[j] = tok >= n ? 0 : tok + 1 >= n ? offsets[j] & 0xFFFFu : offsets[j];
+    }
   }
 };
 
@@ -152,12 +170,12 @@ struct AttnArgs {
   float* part;            // [row][head][split][D], then [row][head][split][4]: sum, maximum, exact sum
 };
 
-template <int DT, int D, int CT, bool SEL>
+template <int DT, int D, bool SEL>
 __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p) {
-  using Tl = Tile<D>;
-  constexpr int G = Tl::G, J = Tl::J;
-  constexpr int NT = CT == 1 && D <= 128 ? 2 : 1;     // tiles taken together
-  constexpr int kPart = (4 * J + 3) * 64;    // floats a wave keeps for a column tile
+  using TS = TileShape<D>;
+  constexpr int G = TS::G, J = TS::J;
+  constexpr int NT = D <= 128 ? 2 : 1;        // tiles taken together
+  constexpr int kPart = (4 * J + 3) * 64;     // floats a wave keeps in LDS
   extern __shared__ __attribute__((aligned(16))) float s_merge[];
   const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -188,20 +206,76 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
   }
   const int cols = n * R;
   const int written = SEL ? a.lens[b] : len;      // tokens that the cache holds
-  for (int tile = tile0; tile * (16 * CT) < cols; tile += p.tiles) {
-    // this lane's columns, and the scaled queries
-    int pos[CT], row[CT], head[CT];
-    h8 Q[CT][G], SQ[CT];
-    float c1[CT], c2[CT];
-    int pos_lo = 0x7FFFFFFF, pos_hi = -1;
+  const int32_t* const table = a.table + (int64_t)b * a.width;
+  const int32_t* const list = SEL ? p.sel + ((int64_t)row0 * p.kv_heads + kvh) * p.n_sel : nullptr;
+  const int64_t stride = (int64_t)p.kv_heads * (80 * D);
+  const uint8_t* const base = p.data + (int64_t)kvh * (80 * D);
+  uint32_t magic = 0x64006400u;   // in a VGPR: the mask and it are then one instruction
+  asm("" : "+v"(magic));
+
+  for (int tile = tile0; tile * 16 < cols; tile += p.tiles) {
+    // positions of the tile's columns, and this workgroup's pages: positions in
+    // the block table, or in the row's list; a wave takes every fourth
+    const int c_hi = min(tile * 16 + 15, cols - 1);
+    const int pos_lo = SEL ? len - 1 : len - n + tile * 16 / R;
+    const int pos_hi = SEL ? len - 1 : len - n + c_hi / R;
+    const int64_t pages64 = ((int64_t)pos_hi + 64) / 64;
+    const int pages = (int)(pages64 < a.width ? pages64 : a.width);
+    const int first = !SEL && p.window > 0 ? max(pos_lo - p.window + 1, 0) / 64 : 0;
+    const int total = SEL ? p.n_sel : max(pages - first, 0);
+    const int per = max(p.split_pages, (total + p.splits - 1) / p.splits);
+    const int j0 = min(split * per, total), j1 = min(j0 + per, total);
+    const int count = (j1 - j0 - wave + kAttnWaves - 1) / kAttnWaves;
+
+    // the next step of this wave: a page, or where NT is 1 a tile of it.  Lanes
+    // hold the places and numbers of 64 pages at a time.
+    int k = -1, held_at = 0, held_id = 0, at = -1, part = 2 / NT - 1;
+    const uint8_t* src = base;
+    auto next = [&]() {
+      if (NT == 1 && part == 0) {
+        part = 1;
+        src += 40 * D;
+        return;
+      }
+      part = 0;
+      for (at = -1; ++k < count;) {
+        if ((k & 63) == 0) {
+          const int j = j0 + wave + kAttnWaves * (k + lane);
+          held_at = j < j1 ? (SEL ? list[j] : first + j) : -1;
+          held_id = held_at >= 0 && held_at < pages ? table[held_at] : -1;
+        }
+        const int id = __builtin_amdgcn_readlane(held_id, k & 63);
+        if (id < 0 || id >= p.n_pages) continue;      // no tokens there
+        at = __builtin_amdgcn_readlane(held_at, k & 63);
+        src = base + id * stride;
+        break;
+      }
+    };
+    KeyTile<D> kt[NT];
+    ValueTile<D> vt[NT];
+    auto load_keys = [&]() {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const int c = tile * (16 * CT) + ct * 16 + l;
-      const bool on = c < cols;
-      row[ct] = on ? row0 + c / R : -1;
-      head[ct] = kvh * R + c % R;
-      pos[ct] = on ? (SEL ? len - 1 : len - n + c / R) : -1;
-      const uint16_t* q = a.q + (on ? row[ct] * a.q_row + head[ct] * a.q_head : 0);
+      for (int t = 0; t < NT; ++t) kt[t].load(src + t * (40 * D), lane);
+    };
+    auto load_values = [&]() {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) vt[t].load(src + t * (40 * D), lane);
+    };
+    next();
+    if (at >= 0) {
+      load_keys();
+      load_values();
+    }
+
+    // this lane's column, and its scaled query
+    const int col = tile * 16 + l;
+    const bool on = col < cols;
+    const int row = on ? row0 + col / R : -1, head = kvh * R + col % R;
+    const int pos = on ? (SEL ? len - 1 : len - n + col / R) : -1;
+    h8 Q[G], SQ;
+    float c1, c2;
+    {
+      const uint16_t* q = a.q + (on ? row * a.q_row + head * a.q_head : 0);
       u4v qv[G];
       float top = 0.f;
 #pragma unroll
@@ -215,8 +289,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
       top = fmaxf(top, __shfl_xor(top, 32));
       int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
       e = top == 0.f || e > 127 ? 14 : max(e, -100);
-      u4v sq = {0, 0, 0, 0};
-      uint32_t sqw[4] = {0, 0, 0, 0};
+      uint32_t sq[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float sum = 0.f;
@@ -225,7 +298,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
           const float y =
               ldexpf(to_float<DT>((uint16_t)(qv[g][i >> 1] >> (16 * (i & 1)))), 14 - e);
           sum += y;
-          Q[ct][g][i] = (_Float16)(i & 2 ? y * 0.0625f : y);
+          Q[g][i] = (_Float16)(i & 2 ? y * 0.0625f : y);
         }
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
@@ -233,309 +306,234 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
         const _Float16 hi = (_Float16)sum, lo = (_Float16)(sum - (float)hi);
         const uint32_t bits = r == 0 ? __builtin_bit_cast(uint16_t, hi)
                                      : r == 1 ? __builtin_bit_cast(uint16_t, lo) : 0u;
-        sqw[g >> 1] |= bits << (16 * (g & 1));
+        sq[g >> 1] |= bits << (16 * (g & 1));
       }
-      sq = u4v{sqw[0], sqw[1], sqw[2], sqw[3]};
-      SQ[ct] = __builtin_bit_cast(h8, sq);
-      const float k = p.scale * 1.44269504f;
-      c1[ct] = ldexpf(k, e - 14 + 24);
-      c2[ct] = ldexpf(k, e - 14 + 6);
-      const int c_lo = tile * (16 * CT) + ct * 16, c_hi = min(c_lo + 15, cols - 1);
-      if (c_lo < cols) {
-        pos_lo = min(pos_lo, SEL ? len - 1 : len - n + c_lo / R);
-        pos_hi = max(pos_hi, SEL ? len - 1 : len - n + c_hi / R);
-      }
+      SQ = __builtin_bit_cast(h8, u4v{sq[0], sq[1], sq[2], sq[3]});
+      const float f = p.scale * 1.44269504f;
+      c1 = ldexpf(f, e - 14 + 24);
+      c2 = ldexpf(f, e - 14 + 6);
     }
-    pos_lo = __builtin_amdgcn_readfirstlane(pos_lo);
-    pos_hi = __builtin_amdgcn_readfirstlane(pos_hi);
 
-    // pages of this workgroup: positions in the block table, or in the row's list
-    const int64_t pages64 = ((int64_t)pos_hi + 64) / 64;
-    const int pages = (int)(pages64 < a.width ? pages64 : a.width);
-    const int first = !SEL && p.window > 0 ? max(pos_lo - p.window + 1, 0) / 64 : 0;
-    const int total = SEL ? p.n_sel : max(pages - first, 0);
-    const int per = max(p.split_pages, (total + p.splits - 1) / p.splits);
-    const int j0 = min(split * per, total), j1 = min(j0 + per, total);
-    const int32_t* const table = a.table + (int64_t)b * a.width;
-    const int32_t* const list =
-        SEL ? p.sel + ((int64_t)row0 * p.kv_heads + kvh) * p.n_sel : nullptr;
-
-    f4 O[CT][J], OZ[CT];
-    float m[CT], m_kept[CT];
-    float exact[CT];        // this lane's weights before their rounding, for lse
+    f4 O[J], OZ = {0, 0, 0, 0};
+    float m = -INFINITY, m_kept = -INFINITY;
+    float exact = 0.f;      // this lane's weights before their rounding, for lse
     int vexp = 0;           // value scales since the last fold are below 2^(vexp + 1)
     bool kept = false;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      m[ct] = m_kept[ct] = -INFINITY;
-      exact[ct] = 0.f;
-      OZ[ct] = f4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < J; ++j) O[ct][j] = f4{0, 0, 0, 0};
-    }
+    for (int j = 0; j < J; ++j) O[j] = f4{0, 0, 0, 0};
     // Folds code sums and offsets into the wave's values in LDS.  The two nearly
     // cancel, and a matrix-core sum loses a little to every addition: over a long
     // cache what they have in common would swallow the result's last bits.
     auto fold = [&]() {
       const float up = ldexpf(1.f, vexp);
+      float* const s = s_merge + wave * kPart;
+      f4* const s4 = reinterpret_cast<f4*>(s) + lane;
+      const float f = m_kept == m ? 1.f : __builtin_amdgcn_exp2f(m_kept - m);
+      float z[G];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        float* const s = s_merge + (wave * CT + ct) * kPart;
-        f4* const s4 = reinterpret_cast<f4*>(s) + lane;
-        const float f = m_kept[ct] == m[ct] ? 1.f : __builtin_amdgcn_exp2f(m_kept[ct] - m[ct]);
-        float z[G];
+      for (int g = 0; g < G; ++g) z[g] = __shfl(OZ[g & 3], (g >> 2) * 16 + l);
+      float sum = __shfl(OZ[0], 32 + l);
 #pragma unroll
-        for (int g = 0; g < G; ++g) z[g] = __shfl(OZ[ct][g & 3], (g >> 2) * 16 + l);
-        float sum = __shfl(OZ[ct][0], 32 + l);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          f4 v = O[ct][j] * up + z[j >> 1];
-          if (kept) v += s4[j * 64] * f;
-          s4[j * 64] = v;
-          O[ct][j] = f4{0, 0, 0, 0};
-        }
-        if (kept) sum += s[4 * J * 64 + lane] * f;
-        s[4 * J * 64 + lane] = sum;
-        s[(4 * J + 1) * 64 + lane] = m[ct];
-        OZ[ct] = f4{0, 0, 0, 0};
-        m_kept[ct] = m[ct];
+      for (int j = 0; j < J; ++j) {
+        f4 v = O[j] * up + z[j >> 1];
+        if (kept) v += s4[j * 64] * f;
+        s4[j * 64] = v;
+        O[j] = f4{0, 0, 0, 0};
       }
+      if (kept) sum += s[4 * J * 64 + lane] * f;
+      s[4 * J * 64 + lane] = sum;
+      s[(4 * J + 1) * 64 + lane] = m;
+      OZ = f4{0, 0, 0, 0};
+      m_kept = m;
       vexp = 0;
       kept = true;
     };
 
-    // page position and number at list index j (number -1: nothing there)
-    auto find = [&](int j, int& at, int& id) {
-      at = j < j1 ? (SEL ? list[j] : first + j) : -1;
-      id = at >= 0 && at < pages ? table[at] : -1;
-      at = __builtin_amdgcn_readfirstlane(at);
-      id = __builtin_amdgcn_readfirstlane(id);
-      if (id >= p.n_pages) id = -1;
-    };
-    uint32_t magic = 0x64006400u;   // in a VGPR: the mask and it are then one instruction
-    asm("" : "+v"(magic));
-    const int64_t stride = (int64_t)p.kv_heads * (80 * D);
-    const uint8_t* const base = p.data + (int64_t)kvh * (80 * D);
-
-    int since = 0;          // pages since the last fold
-    for (int j = j0 + wave; j < j1; j += kAttnWaves) {
-      int at, id;
-      find(j, at, id);
-      if (id < 0) continue;
-      if (since == kFoldPages) {
+    int since = 0;          // steps since the last fold
+    while (at >= 0) {
+      if (since == kFoldPages * (2 / NT)) {
         fold();
         since = 0;
       }
       ++since;
-#pragma unroll 1
-      for (int part = 0; part < 2 / NT; ++part) {
-        const int t0 = at * 64 + part * (32 * NT);
-        Tl tp[NT];
+      const int t0 = at * 64 + part * 32;
+      // logits: sums of codes times queries by group, and of offsets
+      f4 sc[2 * NT], zt[2 * NT];
+      unroll<2 * NT>([&](auto uu) {
+        constexpr int u = uu, t = u / 2, h = u % 2;
+        uint32_t zw[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          tp[t].load(base + id * stride + (part * NT + t) * (40 * D), lane);
-        if (t0 + 32 * NT > written) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) tp[t].cut(written - t0 - 32 * t, lane);
-        }
-        // logits: sums of codes times queries by group, and of offsets
-        f4 sc[CT][2 * NT], zt[CT][2 * NT];
-        unroll<2 * NT>([&](auto uu) {
-          constexpr int u = uu, t = u / 2, h = u % 2;
-          uint32_t zw[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int i = 0; i < Tl::ZN; ++i) zw[i] = tp[t].kz[h][i];
-          const h8 za = __builtin_bit_cast(h8, u4v{zw[0], zw[1], zw[2], zw[3]});
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            zt[ct][u] = mfma(za, SQ[ct], f4{0, 0, 0, 0});
-            sc[ct][u] = f4{0, 0, 0, 0};
-          }
-          unroll<G>([&](auto g) {
-            const h8 ka = code_operand(tp[t].kc[h][g]);
-            const h2 s0 = Tl::template scale2<g * 4 + 2 * h>(tp[t].ks);
-            const h2 s1 = Tl::template scale2<g * 4 + 2 * h + 1>(tp[t].ks);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-              const f4 d = mfma(ka, Q[ct][g], f4{0, 0, 0, 0});
-              f4& s = sc[ct][u];
-              s[0] = __builtin_fmaf((float)s0[0], d[0], s[0]);
-              s[1] = __builtin_fmaf((float)s0[1], d[1], s[1]);
-              s[2] = __builtin_fmaf((float)s1[0], d[2], s[2]);
-              s[3] = __builtin_fmaf((float)s1[1], d[3], s[3]);
-            }
-          });
+        for (int i = 0; i < TS::ZN; ++i) zw[i] = kt[t].offsets[h][i];
+        if (u == 2) __builtin_amdgcn_sched_barrier(0);
+        zt[u] = mfma(__builtin_bit_cast(h8, u4v{zw[0], zw[1], zw[2], zw[3]}), SQ, f4{0, 0, 0, 0});
+        f4 s = {0, 0, 0, 0};
+        unroll<G>([&](auto g) {
+          const f4 d = mfma(code_operand(kt[t].codes[h][g]), Q[g], f4{0, 0, 0, 0});
+          const h2 s0 = TS::template scale2<g * 4 + 2 * h>(kt[t].scales);
+          const h2 s1 = TS::template scale2<g * 4 + 2 * h + 1>(kt[t].scales);
+          s[0] = __builtin_fmaf((float)s0[0], d[0], s[0]);
+          s[1] = __builtin_fmaf((float)s0[1], d[1], s[1]);
+          s[2] = __builtin_fmaf((float)s1[0], d[2], s[2]);
+          s[3] = __builtin_fmaf((float)s1[1], d[3], s[3]);
         });
+        sc[u] = s;
+      });
+      // the keys' registers are free: the next step's keys arrive behind the
+      // values' product, its values behind the next logits
+#pragma unroll
+      for (int u = 0; u < 2 * NT; ++u)
+        asm volatile("" : "+v"(sc[u]), "+v"(zt[u]));   // done here, not after the loads
+      __builtin_amdgcn_sched_barrier(0);
+      next();
+      load_keys();           // past the last step: that step's again, not used
+      __builtin_amdgcn_sched_barrier(0);
 
-        // base-2 logits above the running maximum, plus kWeightExp
-        constexpr int NY = 8 * NT;
-        const bool edge = t0 + 32 * NT - 1 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
-        float y[CT][NY];
-        bool raise = false;
+      // base-2 logits above the running maximum, plus kWeightExp
+      constexpr int NY = 8 * NT;
+      const bool none = m == -INFINITY;
+      const float m8 = none ? -kWeightExp : m - kWeightExp;
+      float y[NY], top = -INFINITY;
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const bool none = m[ct] == -INFINITY;
-          const float m8 = none ? -kWeightExp : m[ct] - kWeightExp;
-          float top = -INFINITY;
+      for (int i = 0; i < NY; ++i)
+        y[i] = __builtin_fmaf(sc[i >> 2][i & 3], c1, __builtin_fmaf(zt[i >> 2][i & 3], c2, -m8));
+      if (t0 + 32 * NT - 1 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window)) {
+        asm volatile("");      // stays a branch: few pages have an edge
 #pragma unroll
-          for (int i = 0; i < NY; ++i)
-            y[ct][i] = __builtin_fmaf(sc[ct][i >> 2][i & 3], c1[ct],
-                                      __builtin_fmaf(zt[ct][i >> 2][i & 3], c2[ct], -m8));
-          if (edge) {
-            asm volatile("");      // stays a branch: few pages have an edge
-#pragma unroll
-            for (int i = 0; i < NY; ++i) {
-              const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
-              if (t > pos[ct] || (p.window > 0 && t <= pos[ct] - p.window)) y[ct][i] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < NY; ++i) top = fmaxf(top, y[ct][i]);
-          raise |= top > (none ? -INFINITY : kWeightExp + kRaise);
-        }
-        if (__any(raise)) {
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            const bool none = m[ct] == -INFINITY;
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NY; ++i) top = fmaxf(top, y[ct][i]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            // the maximum in y's scale stands at kWeightExp
-            const float up = none ? (top == -INFINITY ? 0.f : top - kWeightExp)
-                                  : fmaxf(top - kWeightExp, 0.f);
-            const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
-            if (!none) m[ct] += up;
-            else if (top != -INFINITY) m[ct] = up;
-#pragma unroll
-            for (int i = 0; i < NY; ++i) y[ct][i] -= up;
-#pragma unroll
-            for (int j2 = 0; j2 < J; ++j2) O[ct][j2] *= f;
-            OZ[ct] *= f;
-            exact[ct] *= f;
-          }
-        }
-        // value scales of 2 and more: lower the weights' power of two
-        uint32_t big = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int x = 0; x < Tl::M; ++x) big |= tp[t].vs[x];
-        if (__any((big & 0x40004000u) != 0)) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int x = 0; x < Tl::M; ++x)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              top = max(top, max(tp[t].vs[x] >> 16, tp[t].vs[x] & 0xFFFFu));
-          int e = (int)(top >> 10) - 15;
-#pragma unroll
-          for (int d = 1; d < 64; d <<= 1) e = max(e, __shfl_xor(e, d));
-          e = __builtin_amdgcn_readfirstlane(e);
-          if (e > vexp) {
-            const float f = ldexpf(1.f, vexp - e);
-            vexp = e;
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-              for (int j2 = 0; j2 < J; ++j2) O[ct][j2] *= f;
-          }
-        }
-        const _Float16 d1 = (_Float16)ldexpf(1.f, -vexp), d16 = (_Float16)ldexpf(0.0625f, -vexp);
-        const h2 down = {d1, d1}, down16 = {d16, d16};
-
-        const uint32_t fill = l == 8 ? 0x3C003C00u : 0u;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          u4v z = tp[t].vz;
-          if (l >= G) z = u4v{fill, fill, fill, fill};
-          const h8 za = __builtin_bit_cast(h8, z);
-          h2 ws[CT][4];
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            u4v wv;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              y[ct][8 * t + e] = __builtin_amdgcn_exp2f(y[ct][8 * t + e]);
-            if (p.lse != nullptr) {
-              asm volatile("");    // stays a branch
-#pragma unroll
-              for (int e = 0; e < 8; ++e) exact[ct] += y[ct][8 * t + e];
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const h2 w = {(_Float16)y[ct][8 * t + 2 * x], (_Float16)y[ct][8 * t + 2 * x + 1]};
-              wv[x] = as_u32(w);
-              ws[ct][x] = w * (x & 1 ? down16 : down);
-            }
-            OZ[ct] = mfma(za, __builtin_bit_cast(h8, wv), OZ[ct]);
-          }
-          unroll<G>([&](auto g) {
-            h2 s[4];
-            unroll<4>([&](auto x) { s[x] = Tl::template scale2<g * 4 + x>(tp[t].vs); });
-            const h8 v0 = normal_operand(tp[t].vc[2 * g], magic);
-            const h8 v1 = normal_operand(tp[t].vc[2 * g + 1], magic);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-              u4v hi, lo;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const h2 h = ws[ct][x] * s[x];
-                hi[x] = as_u32(h);
-                lo[x] = as_u32(__builtin_elementwise_fma(ws[ct][x], s[x], -h));
-              }
-              const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
-              O[ct][2 * g] = mfma(v0, hb, O[ct][2 * g]);
-              O[ct][2 * g + 1] = mfma(v1, hb, O[ct][2 * g + 1]);
-              O[ct][2 * g] = mfma(v0, lb, O[ct][2 * g]);
-              O[ct][2 * g + 1] = mfma(v1, lb, O[ct][2 * g + 1]);
-            }
-          });
+        for (int i = 0; i < NY; ++i) {
+          const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
+          if (t > pos || (p.window > 0 && t <= pos - p.window)) y[i] = -INFINITY;
         }
       }
+#pragma unroll
+      for (int i = 0; i < NY; ++i) top = fmaxf(top, y[i]);
+      if (__any(top > (none ? -INFINITY : kWeightExp + kRaise))) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // the maximum in y's scale stands at kWeightExp
+        const float up = none ? (top == -INFINITY ? 0.f : top - kWeightExp)
+                              : fmaxf(top - kWeightExp, 0.f);
+        const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
+        if (!none) m += up;
+        else if (top != -INFINITY) m = up;
+#pragma unroll
+        for (int i = 0; i < NY; ++i) y[i] -= up;
+#pragma unroll
+        for (int j = 0; j < J; ++j) O[j] *= f;
+        OZ *= f;
+        exact *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < NY; ++i) y[i] = __builtin_amdgcn_exp2f(y[i]);
+      if (p.lse != nullptr) {
+        asm volatile("");      // stays a branch
+#pragma unroll
+        for (int i = 0; i < NY; ++i) exact += y[i];
+      }
+
+      if (t0 + 32 * NT > written) {
+        asm volatile("");
+#pragma unroll
+        for (int t = 0; t < NT; ++t) vt[t].cut(written - t0 - 32 * t, lane);
+      }
+      // value scales of 2 and more: lower the weights' power of two
+      uint32_t big = 0;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < TS::M; ++x) big |= vt[t].scales[x];
+      if (__any((big & 0x40004000u) != 0)) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < TS::M; ++x)
+            most = max(most, max(vt[t].scales[x] >> 16, vt[t].scales[x] & 0xFFFFu));
+        int e = (int)(most >> 10) - 15;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) e = max(e, __shfl_xor(e, d));
+        e = __builtin_amdgcn_readfirstlane(e);
+        if (e > vexp) {
+          const float f = ldexpf(1.f, vexp - e);
+          vexp = e;
+#pragma unroll
+          for (int j = 0; j < J; ++j) O[j] *= f;
+        }
+      }
+      const _Float16 d1 = (_Float16)ldexpf(1.f, -vexp), d16 = (_Float16)ldexpf(0.0625f, -vexp);
+      const h2 down = {d1, d1}, down16 = {d16, d16};
+
+      const uint32_t fill = l == 8 ? 0x3C003C00u : 0u;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
+        u4v z = vt[t].offsets, wv;
+        if (l >= G) z = u4v{fill, fill, fill, fill};
+        h2 ws[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const h2 w = {(_Float16)y[8 * t + 2 * x], (_Float16)y[8 * t + 2 * x + 1]};
+          wv[x] = as_u32(w);
+          ws[x] = w * (x & 1 ? down16 : down);
+        }
+        OZ = mfma(__builtin_bit_cast(h8, z), __builtin_bit_cast(h8, wv), OZ);
+        unroll<G>([&](auto g) {
+          h2 s[4];
+          unroll<4>([&](auto x) { s[x] = TS::template scale2<g * 4 + x>(vt[t].scales); });
+          const h8 v0 = normal_operand(vt[t].codes[2 * g], magic);
+          const h8 v1 = normal_operand(vt[t].codes[2 * g + 1], magic);
+          u4v hi, lo;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const h2 h = ws[x] * s[x];
+            hi[x] = as_u32(h);
+            lo[x] = as_u32(__builtin_elementwise_fma(ws[x], s[x], -h));
+          }
+          const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
+          O[2 * g] = mfma(v0, hb, O[2 * g]);
+          O[2 * g + 1] = mfma(v1, hb, O[2 * g + 1]);
+          O[2 * g] = mfma(v0, lb, O[2 * g]);
+          O[2 * g + 1] = mfma(v1, lb, O[2 * g + 1]);
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load_values();
     }
 
     fold();
     if (p.lse != nullptr) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        exact[ct] += __shfl_xor(exact[ct], 16);
-        exact[ct] += __shfl_xor(exact[ct], 32);
-        s_merge[(wave * CT + ct) * kPart + (4 * J + 2) * 64 + lane] = exact[ct];
-      }
+      exact += __shfl_xor(exact, 16);
+      exact += __shfl_xor(exact, 32);
+      s_merge[wave * kPart + (4 * J + 2) * 64 + lane] = exact;
     }
     // the waves' parts joined in order
     __syncthreads();
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
+    if (on) {
       float mw[kAttnWaves], mx = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) {
-        mw[w] = s_merge[(w * CT + ct) * kPart + (4 * J + 1) * 64 + lane];
+        mw[w] = s_merge[w * kPart + (4 * J + 1) * 64 + lane];
         mx = fmaxf(mx, mw[w]);
       }
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) {
         mw[w] = mw[w] == mx ? 1.f : __builtin_amdgcn_exp2f(mw[w] - mx);
-        sum += mw[w] * s_merge[(w * CT + ct) * kPart + 4 * J * 64 + lane];
+        sum += mw[w] * s_merge[w * kPart + 4 * J * 64 + lane];
       }
-      if (row[ct] < 0) continue;
-      const int64_t at = (int64_t)row[ct] * a.heads + head[ct];
+      const int64_t out_at = (int64_t)row * a.heads + head;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       for (int j = wave; j < J; j += kAttnWaves) {
         f4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kAttnWaves; ++w)
-          o += mw[w] * reinterpret_cast<const f4*>(s_merge + (w * CT + ct) * kPart)[j * 64 + lane];
+          o += mw[w] * reinterpret_cast<const f4*>(s_merge + w * kPart)[j * 64 + lane];
         const int d = 16 * j + 4 * r;
         if (p.splits == 1) {
           uint16_t h[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = from_float<DT>(sum == 0.f ? 0.f : o[i] * inv);
-          *reinterpret_cast<u2*>(p.out + at * D + d) = u2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+          *reinterpret_cast<u2*>(p.out + out_at * D + d) = u2{pack2(h[0], h[1]), pack2(h[2], h[3])};
         } else {
-          *reinterpret_cast<f4*>(p.part + (at * p.splits + split) * D + d) = o;
+          *reinterpret_cast<f4*>(p.part + (out_at * p.splits + split) * D + d) = o;
         }
       }
       if (wave == 0 && r == 0) {
@@ -543,12 +541,12 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
         if (p.lse != nullptr)
 #pragma unroll
           for (int w = 0; w < kAttnWaves; ++w)
-            ex += mw[w] * s_merge[(w * CT + ct) * kPart + (4 * J + 2) * 64 + lane];
+            ex += mw[w] * s_merge[w * kPart + (4 * J + 2) * 64 + lane];
         if (p.splits == 1) {
-          if (p.lse != nullptr) p.lse[at] = log_sum(ex, mx);
+          if (p.lse != nullptr) p.lse[out_at] = log_sum(ex, mx);
         } else {
-          reinterpret_cast<f4*>(p.part + (int64_t)a.rows * a.heads * p.splits * D)[at * p.splits + split] =
-              f4{sum, mx, ex, 0.f};
+          reinterpret_cast<f4*>(p.part + (int64_t)a.rows * a.heads * p.splits *
+                                             D)[out_at * p.splits + split] = f4{sum, mx, ex, 0.f};
         }
       }
     }
@@ -609,9 +607,8 @@ join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t*
   if (x == 0 && lse != nullptr) lse[at] = log_sum(ex, mx);
 }
 
-// How a call is split: column tiles a sequence (or row) and splits of its pages.
+// How a call is split: column tiles of a sequence (or row) and splits of its pages.
 struct AttnPlan {
-  int ct;                  // column tiles of 16 a wave
   int64_t pairs, tiles, splits, split_pages;
 };
 static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t max_rows,
@@ -619,16 +616,15 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
   AttnPlan p{};
   const int64_t R = a->n_heads / c->n_kv_heads;
   const int64_t cols = (sel || max_rows < 1 ? 1 : max_rows) * R;
-  p.ct = cols > 16 && c->head_dim <= 128 ? 2 : 1;
-  p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
+  p.tiles = (cols + 15) / 16;
   p.pairs = (sel ? a->n_rows : a->n_seqs) * c->n_kv_heads;
   int64_t pages = sel ? n_sel : (max_len + 63) / 64;
   if (!sel && pages > a->table_width) pages = a->table_width;
   if (pages < 1) pages = 1;
-  // enough workgroups for every compute unit twice; a split has at least two
-  // pages a wave
+  // two workgroups for every compute unit, as many as run at once; a split has
+  // at least two pages a wave
   const int64_t items = p.pairs * p.tiles;
-  int64_t splits = (1024 + items - 1) / items;
+  int64_t splits = (512 + items - 1) / items;
   const int64_t most = (pages + 2 * kAttnWaves - 1) / (2 * kAttnWaves);
   if (splits > most) splits = most;
   p.split_pages = (pages + splits - 1) / splits;
@@ -700,20 +696,15 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
     constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
     auto launch = [&](auto kernel) {
-      const size_t lds = (size_t)kAttnWaves * plan.ct * (D / 4 + 3) * 64 * 4;
+      const size_t lds = (size_t)kAttnWaves * (D / 4 + 3) * 64 * 4;
       if (!allow_lds((const void*)kernel, lds)) {
         status = wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
         return;
       }
       kernel<<<dim3((unsigned)grid), kAttnWaves * kWave, lds, (hipStream_t)stream>>>(p);
     };
-    if (sel != nullptr) {
-      if (plan.ct == 1) launch(attn_kernel<DT, D, 1, true>);
-      else if constexpr (D <= 128) launch(attn_kernel<DT, D, 2, true>);
-    } else {
-      if (plan.ct == 1) launch(attn_kernel<DT, D, 1, false>);
-      else if constexpr (D <= 128) launch(attn_kernel<DT, D, 2, false>);
-    }
+    if (sel != nullptr) launch(attn_kernel<DT, D, true>);
+    else launch(attn_kernel<DT, D, false>);
     if (status == WQ_OK && plan.splits > 1)
       join_kernel<DT, D><<<dim3((unsigned)items), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
           p.part, items, p.splits, out, lse);
