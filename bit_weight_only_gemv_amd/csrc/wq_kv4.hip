@@ -109,19 +109,32 @@ plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ cu, in
 
 // ----------------------------------------------------------------- append
 // One workgroup per (run, head, keys or values).  A thread takes 8 channels of
-// a token, 4 neighbouring lanes one group of 32.
+// a token at a time, 4 neighbouring lanes one group of 32; all of a page's
+// loads are in flight before the first is used.  Keys leave as whole words.
+// Values go through LDS as bytes, 4 channels of 8 tokens to a thread, and come
+// out as 4 words by a byte transpose.
 constexpr int kAppendThreads = 256;
 
-template <int DT>
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const u4v v = *reinterpret_cast<const u4v*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Codes as floats of 8 channels, in the header's arithmetic.  (w - Z) / S is
+// first taken with the reciprocal, which is within 2^-16 of the rounded
+// quotient (|q| < 32, three roundings of 2^-23); where that lies so near to a
+// half that rounding could go another way, the wave divides.
+__device__ __forceinline__ void codes_of(const float (&x)[8], float z, float s, float (&q)[8]) {
+  const float inv = s > 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;
+  float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint16_t b = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-    x[i] = to_float<DT>(b);
-    x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -65504.f), 65504.f);
+    const float t = (x[i] - z) * inv;
+    q[i] = rintf(t);
+    far = fmaxf(far, fabsf(t - q[i]));
   }
+  if (__any(far > 0.5f - 0x1p-16f)) {
+    asm volatile("");          // stays a branch
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = s > 0.f ? rintf((x[i] - z) / s) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(q[i], 0.f), 15.f);
 }
 
 template <int DT, int D>
@@ -131,58 +144,74 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
               const int32_t* __restrict__ slots, const int2* __restrict__ runs,
               uint8_t* __restrict__ data, uint16_t* __restrict__ summary, int64_t n_pages,
               int heads) {
-  constexpr int G = D / 32, W = G < 4 ? G : 4, O = D / 8, TS = kAppendThreads / O;
+  constexpr int G = D / 32, W = G < 4 ? G : 4, O = D / 8, TS = kAppendThreads / O, IT = 64 / TS;
   const bool values = blockIdx.x & 1;
   const int head = (int)((blockIdx.x >> 1) % (unsigned)heads);
   const int run = (int)((blockIdx.x >> 1) / (unsigned)heads);
   const int2 rc = runs[run];
   if (rc.x < 0 || rc.y <= 0 || rc.y > 64 || rc.x > T - rc.y) return;
+  const uint16_t* const src =
+      values ? v + rc.x * v_row + head * v_head : k + rc.x * k_row + head * k_head;
+  const int64_t row = values ? v_row : k_row;
+  const int tid = threadIdx.x, oc = tid % O, g = oc >> 2, r8 = oc & 3;
+  u4v raw[IT];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int n = tid / O + it * TS;
+    if (n < rc.y) raw[it] = *reinterpret_cast<const u4v*>(src + n * row + oc * 8);
+  }
   const int slot = slots[rc.x];
   const int o = slot & 63;
   if (slot < 0 || (slot >> 6) >= n_pages || o + rc.y > 64) return;
   if (slots[rc.x + rc.y - 1] != slot + rc.y - 1) return;
   const int64_t ph = (int64_t)(slot >> 6) * heads + head;
   uint8_t* const page = data + ph * (80 * D);
-  const uint16_t* const src =
-      values ? v + rc.x * v_row + head * v_head : k + rc.x * k_row + head * k_head;
-  const int64_t row = values ? v_row : k_row;
 
-  __shared__ uint8_t s_code[64 * D];          // values: codes by token and channel
-  __shared__ float s_min[TS][D], s_max[TS][D];
-  const int oc = threadIdx.x % O, g = oc >> 2, r8 = oc & 3;
+  // values: codes by token and channel; keys: the threads' minima and maxima
+  __shared__ __attribute__((aligned(16))) uint32_t s_mem[16 * D];
   float lo8[8], hi8[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) { lo8[i] = INFINITY; hi8[i] = -INFINITY; }
-  for (int n = threadIdx.x / O; n < rc.y; n += TS) {
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int n = tid / O + it * TS;
+    if (n >= rc.y) continue;           // the 4 lanes of a group go together
     const int t = o + n, tt = t & 31, u = tt >> 4, r = (tt >> 2) & 3, e = 4 * u + (tt & 3);
-    float x[8];
-    load8<DT>(src + n * row + oc * 8, x);
+    float x[8], q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = to_float<DT>((uint16_t)(raw[it][i >> 1] >> (16 * (i & 1))));
+      x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -65504.f), 65504.f);
+    }
     float lo = x[0], hi = x[0];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       lo = fminf(lo, x[i]);
       hi = fmaxf(hi, x[i]);
-      lo8[i] = fminf(lo8[i], x[i]);
-      hi8[i] = fmaxf(hi8[i], x[i]);
+      if (!values) {
+        lo8[i] = fminf(lo8[i], x[i]);
+        hi8[i] = fmaxf(hi8[i], x[i]);
+      }
     }
-    lo = fminf(lo, __shfl_xor(lo, 1)); lo = fminf(lo, __shfl_xor(lo, 2));
-    hi = fmaxf(hi, __shfl_xor(hi, 1)); hi = fmaxf(hi, __shfl_xor(hi, 2));
+    lo = fminf(lo, dpp_mov<0xB1>(lo));   // quad_perm [1,0,3,2]
+    hi = fmaxf(hi, dpp_mov<0xB1>(hi));
+    lo = fminf(lo, dpp_mov<0x4E>(lo));   // quad_perm [2,3,0,1]
+    hi = fmaxf(hi, dpp_mov<0x4E>(hi));
     const uint16_t zb = f2h(h2f(f2h(lo)) + 0.0f), sb = f2h((hi - lo) / 15.0f);
-    const float z = h2f(zb), s = h2f(sb);
-    int q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q[i] = s > 0.f ? (int)fminf(fmaxf(rintf((x[i] - z) / s), 0.f), 15.f) : 0;
+    codes_of(x, h2f(zb), h2f(sb), q);
     uint8_t* const tile = page + (t >> 5) * (40 * D);
     if (!values) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w |= (uint32_t)q[i] << (4 * ((i >> 1) + 4 * (i & 1)));
+      // slots 0, 2, 4, 6 are the low half's nibbles, 1, 3, 5, 7 the high half's
+      const float a = __builtin_fmaf(4096.f, q[6], __builtin_fmaf(256.f, q[4], __builtin_fmaf(16.f, q[2], q[0])));
+      const float b = __builtin_fmaf(4096.f, q[7], __builtin_fmaf(256.f, q[5], __builtin_fmaf(16.f, q[3], q[1])));
       *reinterpret_cast<uint32_t*>(tile + u * (8 * D) + (g / W) * (256 * W) +
-                                   ((r8 * 16 + (tt & 15)) * W + g % W) * 4) = w;
+                                   ((r8 * 16 + (tt & 15)) * W + g % W) * 4) =
+          (uint32_t)a | (uint32_t)b << 16;
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s_code[t * D + oc * 8 + i] = (uint8_t)q[i];
+      // bytes from sums that stay below 2^24
+      const uint32_t w0 = (uint32_t)__builtin_fmaf(65536.f, q[2], __builtin_fmaf(256.f, q[1], q[0])) | (uint32_t)q[3] << 24;
+      const uint32_t w1 = (uint32_t)__builtin_fmaf(65536.f, q[6], __builtin_fmaf(256.f, q[5], q[4])) | (uint32_t)q[7] << 24;
+      *reinterpret_cast<u2*>(s_mem + t * (D / 4) + oc * 2) = u2{w0, w1};
     }
     uint16_t* const meta = reinterpret_cast<uint16_t*>(tile + (values ? 36 : 32) * D);
     if (r8 == 0) meta[r * 8 * G + g * 8 + e] = sb;
@@ -190,41 +219,62 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
   }
   if (!values) {
     if (summary == nullptr) return;
+    // over the wave's tokens, then over the waves
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s_min[threadIdx.x / O][oc * 8 + i] = lo8[i];
-      s_max[threadIdx.x / O][oc * 8 + i] = hi8[i];
+#pragma unroll
+      for (int d = O; d < kWave; d <<= 1) {
+        lo8[i] = fminf(lo8[i], __shfl_xor(lo8[i], d));
+        hi8[i] = fmaxf(hi8[i], __shfl_xor(hi8[i], d));
+      }
+    }
+    float* const s_lo = reinterpret_cast<float*>(s_mem);          // [waves][D]
+    float* const s_hi = s_lo + (kAppendThreads / kWave) * D;
+    if ((tid & 63) < O) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s_lo[(tid >> 6) * D + oc * 8 + i] = lo8[i];
+        s_hi[(tid >> 6) * D + oc * 8 + i] = hi8[i];
+      }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * D; c += kAppendThreads) {
+    for (int c = tid; c < 2 * D; c += kAppendThreads) {
       const bool mx = c >= D;
       const int d = c % D;
       uint16_t* const at = summary + ph * (2 * D) + c;
       float m = o > 0 ? h2f(*at) : (mx ? -INFINITY : INFINITY);
-      for (int j = 0; j < TS; ++j) m = mx ? fmaxf(m, s_max[j][d]) : fminf(m, s_min[j][d]);
+#pragma unroll
+      for (int j = 0; j < kAppendThreads / kWave; ++j)
+        m = mx ? fmaxf(m, s_hi[j * D + d]) : fminf(m, s_lo[j * D + d]);
       *at = f2h(m);
     }
     return;
   }
   __syncthreads();
-  // words of 8 tokens: tile, r and channel; bits of other tokens stay
-  for (int c = threadIdx.x; c < 8 * D; c += kAppendThreads) {
-    const int d = c % D, r = (c / D) & 3, tile = c / (4 * D);
-    uint32_t w = 0, mask = 0;
+  // a thread: tile, row r, 64 channels c, 4 channels at d4 and every 16th (j); the
+  // bits of tokens outside the run stay
+  for (int c = tid; c < 2 * D; c += kAppendThreads) {
+    const int j = c & 3, d4 = (c >> 2) & 3, r = (c >> 4) & 3, c64 = (c >> 6) % (D / 64),
+              tile = (c >> 6) / (D / 64);
+    uint32_t mask = 0, A[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int t = tile * 32 + (e >> 2) * 16 + r * 4 + (e & 3);
-      if (t >= o && t < o + rc.y) {
-        const int bit = 4 * ((e >> 1) + 4 * (e & 1));
-        w |= (uint32_t)s_code[t * D + d] << bit;
-        mask |= 15u << bit;
-      }
+      const bool in = t >= o && t < o + rc.y;
+      A[e] = in ? s_mem[t * (D / 4) + c64 * 16 + j * 4 + d4] : 0;
+      mask |= in ? 15u << (4 * ((e >> 1) + 4 * (e & 1))) : 0;
     }
     if (mask == 0) continue;
-    uint32_t* const at = reinterpret_cast<uint32_t*>(page + tile * (40 * D) + 16 * D +
-                                                     (d >> 6) * 1024 +
-                                                     (r * 16 + (d & 15)) * 16 + ((d >> 4) & 3) * 4);
-    *at = mask == 0xFFFFFFFFu ? w : (*at & ~mask) | w;
+    const uint32_t b0 = A[0] | A[2] << 4, b1 = A[4] | A[6] << 4, b2 = A[1] | A[3] << 4,
+                   b3 = A[5] | A[7] << 4;
+    uint32_t* const at = reinterpret_cast<uint32_t*>(page + tile * (40 * D) + 16 * D + c64 * 1024 +
+                                                     (r * 16 + d4 * 4) * 16 + j * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = (b0 >> (8 * i) & 255u) | (b1 >> (8 * i) & 255u) << 8 |
+                         (b2 >> (8 * i) & 255u) << 16 | (b3 >> (8 * i) & 255u) << 24;
+      at[4 * i] = mask == 0xFFFFFFFFu ? w : (at[4 * i] & ~mask) | w;
+    }
   }
 }
 
