@@ -143,23 +143,25 @@ class WQError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+_int32 = None       # torch.int32, once the library is loaded
 
 
 def load() -> ctypes.CDLL:
     """Loads the library (raises if it has not been built)."""
-    global _lib
+    global _lib, _int32
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
         raise ImportError(
             f"{LIB_PATH} is missing: build it with `python -m bit_weight_only_gemv_amd.build` "
             "(there is no fallback implementation)")
-    import torch  # noqa: F401  (see module docstring)
+    import torch  # (first: see module docstring)
     lib = ctypes.CDLL(LIB_PATH)
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    _int32 = torch.int32
     _lib = lib
     return lib
 
@@ -445,7 +447,7 @@ def wq_kv4_max_runs(n_seqs: int, n_rows: int) -> int:
 
 def _i32(t, shape, what):
     """Pointer of a contiguous int32 GPU tensor of the given shape."""
-    if "int32" not in str(t.dtype) or tuple(t.shape) != shape:
+    if t.dtype is not _int32 or t.shape != shape:
         raise ValueError(f"{what} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
     return _dptr(t)
 
@@ -453,9 +455,10 @@ def _i32(t, shape, what):
 def wq_kv4_plan(lens, cu_rows, block_table, free_pages, new_lens, slots, runs, taken, stream=None):
     """Sizes from the tensors: lens [B], cu_rows [B + 1], block_table [B, width],
     free_pages [n_free], new_lens [B], slots [rows], runs [n_runs, 2], taken [1]."""
+    fn = load().wq_kv4_plan
     B, width = block_table.shape
     T, F, n_runs = slots.numel(), free_pages.numel(), runs.shape[0]
-    _check(load().wq_kv4_plan(
+    _check(fn(
         _i32(lens, (B,), "lens"), _i32(cu_rows, (B + 1,), "cu_rows"), B, T,
         _i32(block_table, (B, width), "block_table"), width, _i32(free_pages, (F,), "free_pages"),
         F, _i32(new_lens, (B,), "new_lens"), _i32(slots, (T,), "slots"),

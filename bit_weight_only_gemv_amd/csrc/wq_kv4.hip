@@ -134,61 +134,63 @@ __device__ __forceinline__ void codes_of(const float (&x)[8], float z, float s, 
     for (int i = 0; i < 8; ++i) q[i] = s > 0.f ? rintf((x[i] - z) / s) : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(q[i], 0.f), 15.f);
+  for (int i = 0; i < 8; ++i) q[i] = __builtin_amdgcn_fmed3f(q[i], 0.f, 15.f);
 }
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kAppendThreads)
-append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
-              const uint16_t* __restrict__ v, int64_t v_row, int64_t v_head, int T,
-              const int32_t* __restrict__ slots, const int2* __restrict__ runs,
-              uint8_t* __restrict__ data, uint16_t* __restrict__ summary, int64_t n_pages,
-              int heads) {
+// Whether one of a word's two values is NaN, infinite or past 65504 (its exponent
+// field reaches the highest, for BF16 that of 65536).
+template <int DT>
+__device__ __forceinline__ uint32_t out_of_range(uint32_t w) {
+  return ((w & 0x7FFF7FFFu) + (DT == WQ_DT_F16 ? 0x04000400u : 0x38803880u)) & 0x80008000u;
+}
+
+// d / 15 rounded to nearest: the quotient by the rounded reciprocal, corrected
+// once by its exact remainder.
+__device__ __forceinline__ float fifteenth(float d) {
+  const float c = 1.0f / 15.0f, q = d * c;
+  return __builtin_fmaf(__builtin_fmaf(-15.0f, q, d), c, q);
+}
+
+constexpr int append_lds_words(int D) { return 16 * D > 2048 ? 16 * D : 2048; }
+
+// FULL: the run is a whole page, so nothing is masked.
+template <int DT, int D, bool VALUES, bool FULL>
+__device__ __forceinline__ void append_run(const uint16_t* __restrict__ src, int64_t row, int o,
+                                           int count, uint8_t* __restrict__ page,
+                                           uint16_t* __restrict__ summary, uint32_t* s_mem) {
   constexpr int G = D / 32, W = G < 4 ? G : 4, O = D / 8, TS = kAppendThreads / O, IT = 64 / TS;
-  const bool values = blockIdx.x & 1;
-  const int head = (int)((blockIdx.x >> 1) % (unsigned)heads);
-  const int run = (int)((blockIdx.x >> 1) / (unsigned)heads);
-  const int2 rc = runs[run];
-  if (rc.x < 0 || rc.y <= 0 || rc.y > 64 || rc.x > T - rc.y) return;
-  const uint16_t* const src =
-      values ? v + rc.x * v_row + head * v_head : k + rc.x * k_row + head * k_head;
-  const int64_t row = values ? v_row : k_row;
   const int tid = threadIdx.x, oc = tid % O, g = oc >> 2, r8 = oc & 3;
   u4v raw[IT];
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
     const int n = tid / O + it * TS;
-    if (n < rc.y) raw[it] = *reinterpret_cast<const u4v*>(src + n * row + oc * 8);
+    if (FULL || n < count) raw[it] = *reinterpret_cast<const u4v*>(src + n * row + oc * 8);
   }
-  const int slot = slots[rc.x];
-  const int o = slot & 63;
-  if (slot < 0 || (slot >> 6) >= n_pages || o + rc.y > 64) return;
-  if (slots[rc.x + rc.y - 1] != slot + rc.y - 1) return;
-  const int64_t ph = (int64_t)(slot >> 6) * heads + head;
-  uint8_t* const page = data + ph * (80 * D);
-
-  // values: codes by token and channel; keys: the threads' minima and maxima
-  __shared__ __attribute__((aligned(16))) uint32_t s_mem[16 * D];
   float lo8[8], hi8[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) { lo8[i] = INFINITY; hi8[i] = -INFINITY; }
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
     const int n = tid / O + it * TS;
-    if (n >= rc.y) continue;           // the 4 lanes of a group go together
+    if (!FULL && n >= count) continue;     // the 4 lanes of a group go together
     const int t = o + n, tt = t & 31, u = tt >> 4, r = (tt >> 2) & 3, e = 4 * u + (tt & 3);
     float x[8], q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i)
       x[i] = to_float<DT>((uint16_t)(raw[it][i >> 1] >> (16 * (i & 1))));
-      x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -65504.f), 65504.f);
+    if (__any((out_of_range<DT>(raw[it][0]) | out_of_range<DT>(raw[it][1]) |
+               out_of_range<DT>(raw[it][2]) | out_of_range<DT>(raw[it][3])) != 0)) {
+      asm volatile("");        // stays a branch
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -65504.f), 65504.f);
     }
     float lo = x[0], hi = x[0];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       lo = fminf(lo, x[i]);
       hi = fmaxf(hi, x[i]);
-      if (!values) {
+      if (!VALUES) {
         lo8[i] = fminf(lo8[i], x[i]);
         hi8[i] = fmaxf(hi8[i], x[i]);
       }
@@ -197,10 +199,10 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
     hi = fmaxf(hi, dpp_mov<0xB1>(hi));
     lo = fminf(lo, dpp_mov<0x4E>(lo));   // quad_perm [2,3,0,1]
     hi = fmaxf(hi, dpp_mov<0x4E>(hi));
-    const uint16_t zb = f2h(h2f(f2h(lo)) + 0.0f), sb = f2h((hi - lo) / 15.0f);
+    const uint16_t zb = f2h(h2f(f2h(lo)) + 0.0f), sb = f2h(fifteenth(hi - lo));
     codes_of(x, h2f(zb), h2f(sb), q);
     uint8_t* const tile = page + (t >> 5) * (40 * D);
-    if (!values) {
+    if (!VALUES) {
       // slots 0, 2, 4, 6 are the low half's nibbles, 1, 3, 5, 7 the high half's
       const float a = __builtin_fmaf(4096.f, q[6], __builtin_fmaf(256.f, q[4], __builtin_fmaf(16.f, q[2], q[0])));
       const float b = __builtin_fmaf(4096.f, q[7], __builtin_fmaf(256.f, q[5], __builtin_fmaf(16.f, q[3], q[1])));
@@ -213,40 +215,40 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
       const uint32_t w1 = (uint32_t)__builtin_fmaf(65536.f, q[6], __builtin_fmaf(256.f, q[5], q[4])) | (uint32_t)q[7] << 24;
       *reinterpret_cast<u2*>(s_mem + t * (D / 4) + oc * 2) = u2{w0, w1};
     }
-    uint16_t* const meta = reinterpret_cast<uint16_t*>(tile + (values ? 36 : 32) * D);
-    if (r8 == 0) meta[r * 8 * G + g * 8 + e] = sb;
-    if (r8 == 1) meta[D + (values ? r * 8 * G + g * 8 + e : tt * G + g)] = zb;
+    // lane 0 of the group stores the scale, lane 1 the offset
+    const int at = r * 8 * G + g * 8 + e;
+    uint16_t* const meta = reinterpret_cast<uint16_t*>(tile + (VALUES ? 36 : 32) * D);
+    if (r8 < 2) meta[r8 == 0 ? at : D + (VALUES ? at : tt * G + g)] = r8 == 0 ? sb : zb;
   }
-  if (!values) {
+  if constexpr (!VALUES) {
     if (summary == nullptr) return;
-    // over the wave's tokens, then over the waves
+    // FP16 minima and maxima of the threads' tokens, [2][TS][D], then over those:
+    // rounding is monotonic, so it may come first
+    u4v lv, hv;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int d = O; d < kWave; d <<= 1) {
-        lo8[i] = fminf(lo8[i], __shfl_xor(lo8[i], d));
-        hi8[i] = fmaxf(hi8[i], __shfl_xor(hi8[i], d));
-      }
+    for (int x = 0; x < 4; ++x) {
+      lv[x] = pack2(f2h(lo8[2 * x]), f2h(lo8[2 * x + 1]));
+      hv[x] = pack2(f2h(hi8[2 * x]), f2h(hi8[2 * x + 1]));
     }
-    float* const s_lo = reinterpret_cast<float*>(s_mem);          // [waves][D]
-    float* const s_hi = s_lo + (kAppendThreads / kWave) * D;
-    if ((tid & 63) < O) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s_lo[(tid >> 6) * D + oc * 8 + i] = lo8[i];
-        s_hi[(tid >> 6) * D + oc * 8 + i] = hi8[i];
-      }
-    }
+    u4v* const s4 = reinterpret_cast<u4v*>(s_mem);
+    s4[tid] = lv;
+    s4[kAppendThreads + tid] = hv;
     __syncthreads();
-    for (int c = tid; c < 2 * D; c += kAppendThreads) {
-      const bool mx = c >= D;
-      const int d = c % D;
-      uint16_t* const at = summary + ph * (2 * D) + c;
-      float m = o > 0 ? h2f(*at) : (mx ? -INFINITY : INFINITY);
+    for (int c = tid; c < D; c += kAppendThreads) {      // two channels of one of the two
+      const bool mx = c >= D / 2;
+      const uint32_t* const from = s_mem + (mx ? 4 * kAppendThreads : 0) + c % (D / 2);
+      uint32_t* const at = reinterpret_cast<uint32_t*>(summary) + c;
+      h2 m = as_h2(from[0]);
 #pragma unroll
-      for (int j = 0; j < kAppendThreads / kWave; ++j)
-        m = mx ? fmaxf(m, s_hi[j * D + d]) : fminf(m, s_lo[j * D + d]);
-      *at = f2h(m);
+      for (int j = 1; j < TS; ++j) {
+        const h2 y = as_h2(from[j * (D / 2)]);
+        m = mx ? __builtin_elementwise_max(m, y) : __builtin_elementwise_min(m, y);
+      }
+      if (o > 0) {
+        const h2 y = as_h2(*at);
+        m = mx ? __builtin_elementwise_max(m, y) : __builtin_elementwise_min(m, y);
+      }
+      *at = as_u32(m);
     }
     return;
   }
@@ -260,9 +262,9 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int t = tile * 32 + (e >> 2) * 16 + r * 4 + (e & 3);
-      const bool in = t >= o && t < o + rc.y;
-      A[e] = in ? s_mem[t * (D / 4) + c64 * 16 + j * 4 + d4] : 0;
-      mask |= in ? 15u << (4 * ((e >> 1) + 4 * (e & 1))) : 0;
+      const uint32_t in = FULL || (t >= o && t < o + count) ? 0xFFFFFFFFu : 0u;
+      A[e] = s_mem[t * (D / 4) + c64 * 16 + j * 4 + d4] & in;
+      mask |= in & 15u << (4 * ((e >> 1) + 4 * (e & 1)));
     }
     if (mask == 0) continue;
     const uint32_t b0 = A[0] | A[2] << 4, b1 = A[4] | A[6] << 4, b2 = A[1] | A[3] << 4,
@@ -273,8 +275,37 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = (b0 >> (8 * i) & 255u) | (b1 >> (8 * i) & 255u) << 8 |
                          (b2 >> (8 * i) & 255u) << 16 | (b3 >> (8 * i) & 255u) << 24;
-      at[4 * i] = mask == 0xFFFFFFFFu ? w : (at[4 * i] & ~mask) | w;
+      at[4 * i] = FULL || mask == 0xFFFFFFFFu ? w : (at[4 * i] & ~mask) | w;
     }
+  }
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
+              const uint16_t* __restrict__ v, int64_t v_row, int64_t v_head, int T,
+              const int32_t* __restrict__ slots, const int2* __restrict__ runs,
+              uint8_t* __restrict__ data, uint16_t* __restrict__ summary, int64_t n_pages,
+              int heads) {
+  __shared__ __attribute__((aligned(16))) uint32_t s_mem[append_lds_words(D)];
+  const bool values = blockIdx.x & 1;
+  const int head = (int)((blockIdx.x >> 1) % (unsigned)heads);
+  const int run = (int)((blockIdx.x >> 1) / (unsigned)heads);
+  const int2 rc = runs[run];
+  if (rc.x < 0 || rc.y <= 0 || rc.y > 64 || rc.x > T - rc.y) return;
+  const int slot = slots[rc.x], last = slots[rc.x + rc.y - 1], o = slot & 63;
+  if (slot < 0 || (slot >> 6) >= n_pages || o + rc.y > 64 || last != slot + rc.y - 1) return;
+  const int64_t ph = (int64_t)(slot >> 6) * heads + head;
+  uint8_t* const page = data + ph * (80 * D);
+  uint16_t* const sm = summary == nullptr ? nullptr : summary + ph * (2 * D);
+  if (values) {
+    const uint16_t* const src = v + rc.x * v_row + head * v_head;
+    if (rc.y == 64) append_run<DT, D, true, true>(src, v_row, 0, 64, page, sm, s_mem);
+    else append_run<DT, D, true, false>(src, v_row, o, rc.y, page, sm, s_mem);
+  } else {
+    const uint16_t* const src = k + rc.x * k_row + head * k_head;
+    if (rc.y == 64) append_run<DT, D, false, true>(src, k_row, 0, 64, page, sm, s_mem);
+    else append_run<DT, D, false, false>(src, k_row, o, rc.y, page, sm, s_mem);
   }
 }
 

@@ -31,7 +31,7 @@ def _strided(t, what):
     if not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{what} must be a GPU tensor [rows, heads, D]")
     r, h, c = t.stride()
-    if c != 1:
+    if c != 1 and t.numel():
         raise ValueError(f"{what}: channels must be consecutive")
     return t.data_ptr(), r, h
 
@@ -77,16 +77,15 @@ class KV4Cache:
     def append(self, k, v, slots, runs, stream=None):
         """Writes k, v [rows, n_kv_heads, D] (FP16 or BF16, any row and head
         strides that are multiples of 8) into their slots."""
+        fn = L.load().wq_kv4_append
         T = slots.numel()
         want = (T, self.n_kv_heads, self.head_dim)
-        if tuple(k.shape) != want or tuple(v.shape) != want or k.dtype != v.dtype:
+        if k.shape != want or v.shape != want or k.dtype != v.dtype:
             raise ValueError(f"k and v must be {list(want)} of one type")
         kp, kr, kh = _strided(k, "k")
         vp, vr, vh = _strided(v, "v")
-        L._check(L.load().wq_kv4_append(self._ref, _dtype(k), kp, kr, kh, vp, vr, vh, T,
-                                        L._i32(slots, (T,), "slots"),
-                                        L._i32(runs, (runs.shape[0], 2), "runs"), runs.shape[0],
-                                        L._stream(stream)))
+        L._check(fn(self._ref, _dtype(k), kp, kr, kh, vp, vr, vh, T, L._i32(slots, (T,), "slots"),
+                    L._i32(runs, (runs.shape[0], 2), "runs"), runs.shape[0], L._stream(stream)))
 
     def _rows(self, q, block_table, lens, cu_rows):
         B, width = block_table.shape
@@ -102,9 +101,9 @@ class KV4Cache:
         each row and key/value head: int32 [rows, n_kv_heads, n_sel], rising,
         -1 past the end."""
         import torch
+        lib = L.load()
         a = self._rows(q, block_table, lens, cu_rows)
         shape = (a.n_rows, self.n_kv_heads, n_sel)
-        lib = L.load()
         if sel is None:
             sel = _new(shape, torch.int32, q.device, stream)
         need = lib.wq_kv4_select_workspace(a.n_rows, self.n_kv_heads, a.table_width)
@@ -123,13 +122,13 @@ class KV4Cache:
         given, over the last `window` of each row if that is not 0.  lse float32
         [rows, n_heads] receives the logarithm of the softmax sums."""
         import torch
-        a = self._rows(q, block_table, lens, cu_rows)
         lib = L.load()
+        a = self._rows(q, block_table, lens, cu_rows)
         if out is None:
             out = _new(q.shape, q.dtype, q.device, stream)
         elif out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must have q's shape and type")
-        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2])):
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
             raise ValueError("lse must be float32 [rows, n_heads]")
         n_sel = 0 if sel is None else sel.shape[-1]
         if scale is None:
