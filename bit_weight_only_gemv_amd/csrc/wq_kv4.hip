@@ -312,14 +312,15 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 // ----------------------------------------------------------------- select
 // Scores (float32 in the workspace, [row][head][page]), then the n_sel highest.
 //
-// A page's bound is sum_d max(q min, q max) = sum_d q mid + |q| half with mid =
-// (max + min) / 2 and half = (max - min) / 2.  FP16 values and their products are
+// A page's bound is sum_d max(q min, q max) = sum_d q' (max + min) + |q'| (max -
+// min) with q' = q / 2.  FP16 values and their products are
 // far inside 64 bits, so those sums are exact but for operands that lie 2^20
 // apart, and the choice does not depend on their order: two fused multiply-adds
 // a channel and head, at the rate of 32-bit ones.  A wave takes 512 / D pages at
 // a time, 8 channels a lane, up to 8 heads' queries in registers.
 constexpr int kScoreWaves = 4;
 constexpr int kScoreHeads = 8;       // heads of one pass
+constexpr int kScoreTurns = 8;       // most turns of a wave
 
 __device__ __forceinline__ double lane_add(double v, int d) { return v + __shfl_xor(v, d); }
 
@@ -347,7 +348,23 @@ score_kernel(KvRows a, const uint16_t* __restrict__ summary, int64_t n_pages, in
   const int R = a.heads / kv_heads, c0 = (lane % L) * 8;
   const int32_t* const table = a.table + (int64_t)sr.b * a.width;
   float* const out = scores + ((int64_t)row * kv_heads + head) * a.width;
+  // the pages of this wave's turns: P of each, a lane's own in every turn
+  constexpr int kStep = kScoreWaves * P;
+  int ids[kScoreTurns];
+#pragma unroll
+  for (int t = 0; t < kScoreTurns; ++t) {
+    const int p = p_first + t * kStep;
+    ids[t] = p < p_end ? table[p] : -1;
+    if (ids[t] >= n_pages) ids[t] = -1;
+  }
+  auto load = [&](int id, u4v& lo, u4v& hi) {
+    const uint16_t* sm = summary + ((int64_t)max(id, 0) * kv_heads + head) * (2 * D) + c0;
+    lo = *reinterpret_cast<const u4v*>(sm);
+    hi = *reinterpret_cast<const u4v*>(sm + D);
+  };
   for (int h0 = 0; h0 < R; h0 += kScoreHeads) {
+    u4v lo, hi;
+    load(ids[0], lo, hi);
     double q[kScoreHeads][8];
 #pragma unroll
     for (int h = 0; h < kScoreHeads; ++h) {
@@ -356,25 +373,26 @@ score_kernel(KvRows a, const uint16_t* __restrict__ summary, int64_t n_pages, in
       const u4v v = *reinterpret_cast<const u4v*>(src);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        q[h][i] = (double)to_float<DT>((uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+        q[h][i] = 0.5 * (double)to_float<DT>((uint16_t)(v[i >> 1] >> (16 * (i & 1))));
     }
-    for (int p = p_first; p - lane / L < p_end; p += kScoreWaves * P) {
-      const int page = p < p_end ? table[p] : -1;
-      const bool ok = page >= 0 && page < n_pages;
-      const uint16_t* sm = summary + ((int64_t)(ok ? page : 0) * kv_heads + head) * (2 * D) + c0;
-      const u4v lo = *reinterpret_cast<const u4v*>(sm), hi = *reinterpret_cast<const u4v*>(sm + D);
+#pragma unroll
+    for (int t = 0; t < kScoreTurns; ++t) {
+      const int p = p_first + t * kStep;
+      if (p - lane / L >= p_end) break;     // the same for the wave
+      const u4v lo_now = lo, hi_now = hi;
+      if (t + 1 < kScoreTurns) load(ids[t + 1 < kScoreTurns ? t + 1 : t], lo, hi);
       double s[kScoreHeads];
 #pragma unroll
       for (int h = 0; h < kScoreHeads; ++h) s[h] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const double mn = (double)h2f((uint16_t)(lo[i >> 1] >> (16 * (i & 1))));
-        const double mx = (double)h2f((uint16_t)(hi[i >> 1] >> (16 * (i & 1))));
-        const double mid = (mx + mn) * 0.5, half = (mx - mn) * 0.5;
+        const double mn = (double)h2f((uint16_t)(lo_now[i >> 1] >> (16 * (i & 1))));
+        const double mx = (double)h2f((uint16_t)(hi_now[i >> 1] >> (16 * (i & 1))));
+        const double sum = mx + mn, span = mx - mn;
 #pragma unroll
         for (int h = 0; h < kScoreHeads; ++h) {
-          s[h] = __builtin_fma(q[h][i], mid, s[h]);
-          s[h] = __builtin_fma(__builtin_fabs(q[h][i]), half, s[h]);
+          s[h] = __builtin_fma(q[h][i], sum, s[h]);
+          s[h] = __builtin_fma(__builtin_fabs(q[h][i]), span, s[h]);
         }
       }
       double best = -INFINITY;
@@ -386,10 +404,10 @@ score_kernel(KvRows a, const uint16_t* __restrict__ summary, int64_t n_pages, in
         v = row_add<0x141>(v);                // row_half_mirror
         if constexpr (L >= 16) v = row_add<0x140>(v);   // row_mirror
         if constexpr (L == 32) v = lane_add(v, 16);
-        best = v > best ? v : best;
+        best = fmax(best, v);
       }
       if (lane % L == 0 && p < p_end) {
-        float f = p == 0 || p == pages - 1 ? INFINITY : (ok ? (float)best : -INFINITY);
+        float f = p == 0 || p == pages - 1 ? INFINITY : (ids[t] >= 0 ? (float)best : -INFINITY);
         if (h0 > 0) f = fmaxf(f, out[p]);
         out[p] = f;
       }
@@ -652,9 +670,11 @@ extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
   // compute units idle
   const int64_t turn = kScoreWaves * (512 / cache->head_dim);
   const int64_t pairs = rows->n_rows * cache->n_kv_heads;
-  int64_t turns = pairs * rows->table_width / (turn * 1024);
-  turns = turns < 1 ? 1 : turns > 8 ? 8 : turns;
-  while (rows->table_width > turn * turns * 65535) turns *= 2;   // the grid's limit
+  int64_t turns = pairs * rows->table_width / (turn * 512);
+  turns = turns < 1 ? 1 : turns > kScoreTurns ? kScoreTurns : turns;
+  if (rows->table_width > turn * turns * 65535)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: table of %lld pages", who,
+                    (long long)rows->table_width);
   const int64_t chunk = turn * turns;
   const dim3 grid((unsigned)pairs, (unsigned)((rows->table_width + chunk - 1) / chunk));
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {

@@ -15,12 +15,12 @@
 //
 // Precision.  Queries are scaled by a power of two to [2^14, 2^15) and so are
 // exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  A softmax
-// weight is rounded to FP16 once, and that rounded weight is what every sum
-// uses, the denominator's too: it moves a result by at most 2^-11 of the values'
-// spread, and by 2^-12 / sqrt(n) of it where n tokens count.  A weight times a
-// scale enters the product exactly, as an FP16 head and remainder: the codes'
-// part and the offsets' part nearly cancel where a group lies far from 0, so a
-// rounding there would not stay small.  Weights carry 2^8, and value scales of 2
+// weight is an FP16 number and its FP16 remainder (22 bits); for BF16 outputs the
+// number alone, rounded once (2^-12, against the output's 2^-9), and then that is
+// what every sum uses, the denominator's too.  A weight times a scale enters the
+// product as an FP16 head and remainder as well: the codes' part and the offsets'
+// part nearly cancel where a group lies far from 0, so a rounding there would not
+// stay small.  Weights carry 2^8, and value scales of 2
 // and more lower that by a running power of two, so that neither end of FP16's
 // range is met: a weight 2^-30 of the largest still counts.  The running maximum
 // is only raised when a logit passes it by 2^6, which spares most pages the
@@ -34,7 +34,7 @@
 
 namespace wqd {
 
-constexpr int kAttnWaves = 4;
+constexpr int kAttnWaves = 4, kAttnMoreWaves = 8;
 constexpr int kFoldPages = 8;
 constexpr float kWeightExp = 8.f;    // weights carry 2^8 ...
 constexpr float kRaise = 6.f;        // ... and grow by up to 2^6 before the maximum is raised
@@ -88,7 +88,7 @@ template <int D>
 struct TileShape {
   static constexpr int G = D / 32, W = G < 4 ? G : 4, J = D / 16, M = G == 8 ? 2 : 1, ZN = G / 2;
   // Byte of row r's scales that lane l holds: M dwords (2 slots each) of 4 G.
-  static __device__ __forceinline__ int scale_at(int r, int l) {
+  static __device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t l) {
     return r * (16 * G) + (G == 2 ? (l & 7) * 4 : l * (4 * M));
   }
   // Dword j (slots 2j, 2j + 1) of group g of row r's scales (GJ = 4 g + j), in all lanes.
@@ -105,9 +105,9 @@ struct KeyTile : TileShape<D> {
   uint32_t codes[2][S::G];      // 16-token part, group: 8 codes of token l
   uint32_t scales[S::M];
   uint32_t offsets[2][S::ZN];   // token l's, all groups
-  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int lane) {
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, uint32_t lane) {
     constexpr int G = S::G, W = S::W;
-    const int r = lane >> 4, l = lane & 15;
+    const uint32_t r = lane >> 4, l = lane & 15;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -126,8 +126,8 @@ struct ValueTile : TileShape<D> {
   uint32_t codes[S::J];         // 16 channels: 8 codes of channel l
   uint32_t scales[S::M];
   u4v offsets;                  // group l's, of 8 tokens
-  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, int lane) {
-    const int r = lane >> 4, l = lane & 15;
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ q, uint32_t lane) {
+    const uint32_t r = lane >> 4, l = lane & 15;
 #pragma unroll
     for (int c = 0; c < S::J / 4; ++c)
       __builtin_memcpy(&codes[c * 4], q + 16 * D + c * 1024 + lane * 16, 16);
@@ -170,11 +170,12 @@ struct AttnArgs {
   float* part;            // [row][head][split][D], then [row][head][split][4]: sum, maximum, exact sum
 };
 
-template <int DT, int D, bool SEL>
-__global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p) {
+template <int DT, int D, bool SEL, int NW>
+__global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
   using TS = TileShape<D>;
   constexpr int G = TS::G, J = TS::J;
   constexpr int NT = D <= 128 ? 2 : 1;        // tiles taken together
+  constexpr bool REST = DT == WQ_DT_F16;      // weights with their FP16 remainder
   constexpr int kPart = (4 * J + 3) * 64;     // floats a wave keeps in LDS
   extern __shared__ __attribute__((aligned(16))) float s_merge[];
   const KvRows& a = p.a;
@@ -191,8 +192,13 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
   const int kvh = pair % p.kv_heads, split = rest % p.splits;
   const int tile0 = p.tiles - 1 - rest / p.splits;
   int b, row0, n, len;
+  // The wave's first page numbers (or their places in the row's list), read at
+  // the same time as the lengths: where the hints hold, a split starts here.
+  const int guess_at = split * p.split_pages + wave + NW * lane;
+  int guess = -1;
   if constexpr (SEL) {
     row0 = pair / p.kv_heads;
+    if (guess_at < p.n_sel) guess = p.sel[((int64_t)row0 * p.kv_heads + kvh) * p.n_sel + guess_at];
     const SeqRow sr = find_row(a, row0);
     b = sr.b;
     n = 1;
@@ -200,6 +206,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
     if (row0 >= a.cu[b + 1]) return;
   } else {
     b = pair / p.kv_heads;
+    if (guess_at < a.width) guess = a.table[(int64_t)b * a.width + guess_at];
     row0 = max(a.cu[b], 0);
     n = min(a.cu[b + 1], a.rows) - row0;
     len = a.lens[b];
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
     const int total = SEL ? p.n_sel : max(pages - first, 0);
     const int per = max(p.split_pages, (total + p.splits - 1) / p.splits);
     const int j0 = min(split * per, total), j1 = min(j0 + per, total);
-    const int count = (j1 - j0 - wave + kAttnWaves - 1) / kAttnWaves;
+    const int count = (j1 - j0 - wave + NW - 1) / NW;
 
     // the next step of this wave: a page, or where NT is 1 a tile of it.  Lanes
     // hold the places and numbers of 64 pages at a time.
@@ -240,9 +247,12 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
       part = 0;
       for (at = -1; ++k < count;) {
         if ((k & 63) == 0) {
-          const int j = j0 + wave + kAttnWaves * (k + lane);
-          held_at = j < j1 ? (SEL ? list[j] : first + j) : -1;
-          held_id = held_at >= 0 && held_at < pages ? table[held_at] : -1;
+          const int j = j0 + wave + NW * (k + lane);
+          const bool guessed = k == 0 && per == p.split_pages && first == 0;
+          held_at = j < j1 ? (SEL ? (guessed ? guess : list[j]) : first + j) : -1;
+          held_id = -1;
+          if (held_at >= 0 && held_at < pages)
+            held_id = !SEL && guessed ? guess : table[held_at];
         }
         const int id = __builtin_amdgcn_readlane(held_id, k & 63);
         if (id < 0 || id >= p.n_pages) continue;      // no tokens there
@@ -261,26 +271,30 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
 #pragma unroll
       for (int t = 0; t < NT; ++t) vt[t].load(src + t * (40 * D), lane);
     };
+    // this lane's column, its query's loads ahead of the pages' and its scaling
+    // behind them
+    const int col = tile * 16 + l;
+    const bool on = col < cols;
+    const int row = on ? row0 + col / R : -1, head = kvh * R + col % R;
+    const int pos = on ? (SEL ? len - 1 : len - n + col / R) : -1;
+    u4v qv[G];
+    {
+      const uint16_t* q = a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        qv[g] = on ? *reinterpret_cast<const u4v*>(q + 32 * g) : u4v{0, 0, 0, 0};
+    }
     next();
     if (at >= 0) {
       load_keys();
       load_values();
     }
-
-    // this lane's column, and its scaled query
-    const int col = tile * 16 + l;
-    const bool on = col < cols;
-    const int row = on ? row0 + col / R : -1, head = kvh * R + col % R;
-    const int pos = on ? (SEL ? len - 1 : len - n + col / R) : -1;
     h8 Q[G], SQ;
     float c1, c2;
     {
-      const uint16_t* q = a.q + (on ? row * a.q_row + head * a.q_head : 0);
-      u4v qv[G];
       float top = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        qv[g] = on ? *reinterpret_cast<const u4v*>(q + 32 * g + 8 * r) : u4v{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           top = fmaxf(top, fabsf(to_float<DT>((uint16_t)(qv[g][i >> 1] >> (16 * (i & 1))))));
@@ -468,14 +482,23 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
         __builtin_amdgcn_sched_barrier(0);
         u4v z = vt[t].offsets, wv;
         if (l >= G) z = u4v{fill, fill, fill, fill};
-        h2 ws[4];
+        h2 ws[4], wr[4];
+        u4v rv;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const h2 w = {(_Float16)y[8 * t + 2 * x], (_Float16)y[8 * t + 2 * x + 1]};
+          const float y0 = y[8 * t + 2 * x], y1 = y[8 * t + 2 * x + 1];
+          const h2 w = {(_Float16)y0, (_Float16)y1};
           wv[x] = as_u32(w);
           ws[x] = w * (x & 1 ? down16 : down);
+          if constexpr (REST) {
+            const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
+            rv[x] = as_u32(rest);
+            wr[x] = rest * (x & 1 ? down16 : down);
+          }
         }
-        OZ = mfma(__builtin_bit_cast(h8, z), __builtin_bit_cast(h8, wv), OZ);
+        const h8 za = __builtin_bit_cast(h8, z);
+        OZ = mfma(za, __builtin_bit_cast(h8, wv), OZ);
+        if constexpr (REST) OZ = mfma(za, __builtin_bit_cast(h8, rv), OZ);
         unroll<G>([&](auto g) {
           h2 s[4];
           unroll<4>([&](auto x) { s[x] = TS::template scale2<g * 4 + x>(vt[t].scales); });
@@ -486,7 +509,9 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
           for (int x = 0; x < 4; ++x) {
             const h2 h = ws[x] * s[x];
             hi[x] = as_u32(h);
-            lo[x] = as_u32(__builtin_elementwise_fma(ws[x], s[x], -h));
+            h2 rest = __builtin_elementwise_fma(ws[x], s[x], -h);
+            if constexpr (REST) rest = __builtin_elementwise_fma(wr[x], s[x], rest);
+            lo[x] = as_u32(rest);
           }
           const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
           O[2 * g] = mfma(v0, hb, O[2 * g]);
@@ -508,23 +533,23 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
     // the waves' parts joined in order
     __syncthreads();
     if (on) {
-      float mw[kAttnWaves], mx = -INFINITY, sum = 0.f;
+      float mw[NW], mx = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
+      for (int w = 0; w < NW; ++w) {
         mw[w] = s_merge[w * kPart + (4 * J + 1) * 64 + lane];
         mx = fmaxf(mx, mw[w]);
       }
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
+      for (int w = 0; w < NW; ++w) {
         mw[w] = mw[w] == mx ? 1.f : __builtin_amdgcn_exp2f(mw[w] - mx);
         sum += mw[w] * s_merge[w * kPart + 4 * J * 64 + lane];
       }
       const int64_t out_at = (int64_t)row * a.heads + head;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      for (int j = wave; j < J; j += kAttnWaves) {
+      for (int j = wave; j < J; j += NW) {
         f4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w)
+        for (int w = 0; w < NW; ++w)
           o += mw[w] * reinterpret_cast<const f4*>(s_merge + w * kPart)[j * 64 + lane];
         const int d = 16 * j + 4 * r;
         if (p.splits == 1) {
@@ -540,7 +565,7 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) attn_kernel(AttnArgs p)
         float ex = 0.f;
         if (p.lse != nullptr)
 #pragma unroll
-          for (int w = 0; w < kAttnWaves; ++w)
+          for (int w = 0; w < NW; ++w)
             ex += mw[w] * s_merge[w * kPart + (4 * J + 2) * 64 + lane];
         if (p.splits == 1) {
           if (p.lse != nullptr) p.lse[out_at] = log_sum(ex, mx);
@@ -610,6 +635,7 @@ join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t*
 // How a call is split: column tiles of a sequence (or row) and splits of its pages.
 struct AttnPlan {
   int64_t pairs, tiles, splits, split_pages;
+  int waves;
 };
 static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t max_rows,
                           int64_t max_len, int64_t n_sel, bool sel) {
@@ -621,12 +647,21 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
   int64_t pages = sel ? n_sel : (max_len + 63) / 64;
   if (!sel && pages > a->table_width) pages = a->table_width;
   if (pages < 1) pages = 1;
-  // two workgroups for every compute unit, as many as run at once; a split has
-  // at least two pages a wave
+  // Two workgroups of 4 waves for every compute unit, as many as run at once:
+  // a second round costs more than uneven lengths do (32 sequences of up to 8191
+  // tokens: 56 us, in two rounds 61).  A split has at least two pages a wave, one
+  // while that leaves compute units idle (64 chosen pages: 8.7 us, 10.1 with two).
   const int64_t items = p.pairs * p.tiles;
   int64_t splits = (512 + items - 1) / items;
-  const int64_t most = (pages + 2 * kAttnWaves - 1) / (2 * kAttnWaves);
+  const int64_t waves = items * ((pages + kAttnWaves - 1) / kAttnWaves) <= 256 ? kAttnWaves : 2 * kAttnWaves;
+  const int64_t most = (pages + waves - 1) / waves;
   if (splits > most) splits = most;
+  // few pages for few workgroups: one workgroup of 8 waves, and no second launch
+  p.waves = kAttnWaves;
+  if (items <= 256 && pages <= 2 * kAttnMoreWaves) {
+    splits = 1;
+    if (pages > kAttnWaves) p.waves = kAttnMoreWaves;
+  }
   p.split_pages = (pages + splits - 1) / splits;
   p.splits = (pages + p.split_pages - 1) / p.split_pages;
   return p;
@@ -696,15 +731,20 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
     constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
     auto launch = [&](auto kernel) {
-      const size_t lds = (size_t)kAttnWaves * (D / 4 + 3) * 64 * 4;
+      const size_t lds = (size_t)plan.waves * (D / 4 + 3) * 64 * 4;
       if (!allow_lds((const void*)kernel, lds)) {
         status = wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
         return;
       }
-      kernel<<<dim3((unsigned)grid), kAttnWaves * kWave, lds, (hipStream_t)stream>>>(p);
+      kernel<<<dim3((unsigned)grid), plan.waves * kWave, lds, (hipStream_t)stream>>>(p);
     };
-    if (sel != nullptr) launch(attn_kernel<DT, D, true>);
-    else launch(attn_kernel<DT, D, false>);
+    if (plan.waves == kAttnWaves) {
+      if (sel != nullptr) launch(attn_kernel<DT, D, true, kAttnWaves>);
+      else launch(attn_kernel<DT, D, false, kAttnWaves>);
+    } else {
+      if (sel != nullptr) launch(attn_kernel<DT, D, true, kAttnMoreWaves>);
+      else launch(attn_kernel<DT, D, false, kAttnMoreWaves>);
+    }
     if (status == WQ_OK && plan.splits > 1)
       join_kernel<DT, D><<<dim3((unsigned)items), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
           p.part, items, p.splits, out, lse);
