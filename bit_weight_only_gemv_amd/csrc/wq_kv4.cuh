@@ -23,6 +23,23 @@ struct KvRows {
   int64_t q_row, q_head;
 };
 
+// Division of 0 <= n < 2^31 by a divisor known on the host: one multiplication
+// (the device's own division is some 40 instructions, and a short attention call
+// would spend a tenth of its time on them).  With l = ceil(log2 d) and m =
+// ceil(2^(31 + l) / d) < 2^32, n m / 2^(31 + l) exceeds n / d by less than
+// n / 2^31 / d < 1 / d, so the floors agree.
+struct Divisor {
+  uint32_t d, m, l;
+  Divisor() = default;
+  explicit Divisor(int64_t by) : d((uint32_t)by), l(0) {
+    while ((1ull << l) < (uint64_t)by) ++l;
+    m = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * m) >> (31 + l));
+  }
+};
+
 template <int DT>
 __device__ __forceinline__ float to_float(uint16_t b) {
   if constexpr (DT == WQ_DT_F16) return h2f(b);

@@ -286,11 +286,10 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
               const uint16_t* __restrict__ v, int64_t v_row, int64_t v_head, int T,
               const int32_t* __restrict__ slots, const int2* __restrict__ runs,
               uint8_t* __restrict__ data, uint16_t* __restrict__ summary, int64_t n_pages,
-              int heads) {
+              int heads, Divisor by) {
   __shared__ __attribute__((aligned(16))) uint32_t s_mem[append_lds_words(D)];
   const bool values = blockIdx.x & 1;
-  const int head = (int)((blockIdx.x >> 1) % (unsigned)heads);
-  const int run = (int)((blockIdx.x >> 1) / (unsigned)heads);
+  const int run = by.div(blockIdx.x >> 1), head = (int)(blockIdx.x >> 1) - run * heads;
   const int2 rc = runs[run];
   if (rc.x < 0 || rc.y <= 0 || rc.y > 64 || rc.x > T - rc.y) return;
   const int slot = slots[rc.x], last = slots[rc.x + rc.y - 1], o = slot & 63;
@@ -334,18 +333,18 @@ __device__ __forceinline__ double row_add(double v) {
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kScoreWaves * kWave)
-score_kernel(KvRows a, const uint16_t* __restrict__ summary, int64_t n_pages, int kv_heads,
-             int n_sel, int chunk, float* __restrict__ scores) {
+score_kernel(KvRows a, Divisor by, const uint16_t* __restrict__ summary, int64_t n_pages,
+             int kv_heads, int R, int n_sel, int chunk, float* __restrict__ scores) {
   constexpr int L = D / 8, P = kWave / L;   // lanes a page, pages a wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int head = blockIdx.x % kv_heads, row = blockIdx.x / kv_heads;
+  const int row = by.div(blockIdx.x), head = blockIdx.x - row * kv_heads;
   const SeqRow sr = find_row(a, row);
   const int pages = sr.pos >= 0 ? (int)min((int64_t)(sr.pos / 64 + 1), a.width) : 0;
   if (pages <= n_sel) return;               // all of them are taken
   const int p_end = min((int)(blockIdx.y + 1) * chunk, pages);
   const int p_first = blockIdx.y * chunk + wave * P + lane / L;
   if ((int)blockIdx.y * chunk >= pages) return;
-  const int R = a.heads / kv_heads, c0 = (lane % L) * 8;
+  const int c0 = (lane % L) * 8;
   const int32_t* const table = a.table + (int64_t)sr.b * a.width;
   float* const out = scores + ((int64_t)row * kv_heads + head) * a.width;
   // the pages of this wave's turns: P of each, a lane's own in every turn
@@ -447,12 +446,12 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_wave, u
 }
 
 __global__ void __launch_bounds__(kPickThreads)
-pick_kernel(KvRows a, int kv_heads, const float* __restrict__ scores, int n_sel,
+pick_kernel(KvRows a, Divisor by, const float* __restrict__ scores, int n_sel,
             int32_t* __restrict__ sel) {
   __shared__ uint32_t s_hist[4][256];
   __shared__ uint32_t s_found[2], s_wave[kPickThreads / kWave];
   extern __shared__ uint32_t s_key[];
-  const int tid = threadIdx.x, row = blockIdx.x / kv_heads;
+  const int tid = threadIdx.x, row = by.div(blockIdx.x);
   const SeqRow sr = find_row(a, row);
   const int pages = sr.pos >= 0 ? (int)min((int64_t)(sr.pos / 64 + 1), a.width) : 0;
   const float* sc = scores + (int64_t)blockIdx.x * a.width;
@@ -629,7 +628,7 @@ extern "C" int wq_kv4_append(const wq_kv4_cache* cache, int dtype, const uint16_
         <<<grid, kAppendThreads, 0, (hipStream_t)stream>>>(
             k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, (int)n_rows, slots,
             reinterpret_cast<const int2*>(runs), cache->data, cache->summary, cache->n_pages,
-            (int)cache->n_kv_heads);
+            (int)cache->n_kv_heads, Divisor(cache->n_kv_heads));
   });
   return check_launch(who);
 }
@@ -664,6 +663,7 @@ extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
   if (rows->n_rows * cache->n_kv_heads > 0x7FFFFFFFll)
     return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
   const KvRows a = kv4_rows(rows);
+  const Divisor by(cache->n_kv_heads);
   float* scores = static_cast<float*>(workspace);
   // a workgroup takes `chunk` pages of a (row, head): up to 8 of its waves' turns
   // (the queries' conversion is spread over them), fewer where that would leave
@@ -680,11 +680,11 @@ extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
     score_kernel<decltype(dt)::value, decltype(d)::value>
         <<<grid, kScoreWaves * kWave, 0, (hipStream_t)stream>>>(
-            a, cache->summary, cache->n_pages, (int)cache->n_kv_heads, (int)n_sel, (int)chunk,
-            scores);
+            a, by, cache->summary, cache->n_pages, (int)cache->n_kv_heads,
+            (int)(rows->n_heads / cache->n_kv_heads), (int)n_sel, (int)chunk, scores);
   });
   const int64_t held = rows->table_width < kPickHeld ? rows->table_width : kPickHeld;
   pick_kernel<<<dim3((unsigned)pairs), kPickThreads, (size_t)held * 4, (hipStream_t)stream>>>(
-      a, (int)cache->n_kv_heads, scores, (int)n_sel, sel);
+      a, by, scores, (int)n_sel, sel);
   return check_launch(who);
 }

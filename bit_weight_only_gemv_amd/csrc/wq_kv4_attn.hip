@@ -162,6 +162,7 @@ struct AttnArgs {
   KvRows a;
   const uint8_t* data;
   int64_t n_pages;
+  Divisor kv_heads_by, group_by, pairs_by, splits_by;
   int kv_heads, window, n_sel, tiles, splits, split_pages;
   float scale;
   const int32_t* sel;
@@ -181,23 +182,23 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
   const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane >> 4, l = lane & 15;
-  const int R = a.heads / p.kv_heads;
+  const int R = (int)p.group_by.d;
 
   // pairs (sequence or row, key/value head) vary fastest: workgroups that read
   // the same pages are a multiple of the pairs apart and so, for 8 pairs and
   // their multiples, on the same XCD; the last column tiles, which see the most
   // tokens, come first
-  const unsigned pairs = (SEL ? a.rows : a.seqs) * (unsigned)p.kv_heads;
-  const int pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
-  const int kvh = pair % p.kv_heads, split = rest % p.splits;
-  const int tile0 = p.tiles - 1 - rest / p.splits;
+  const int rest = p.pairs_by.div(blockIdx.x), pair = blockIdx.x - rest * p.pairs_by.d;
+  const int of = p.kv_heads_by.div(pair), kvh = pair - of * p.kv_heads;
+  const int turn = p.splits_by.div(rest), split = rest - turn * p.splits;
+  const int tile0 = p.tiles - 1 - turn;
   int b, row0, n, len;
   // The wave's first page numbers (or their places in the row's list), read at
   // the same time as the lengths: where the hints hold, a split starts here.
   const int guess_at = split * p.split_pages + wave + NW * lane;
   int guess = -1;
   if constexpr (SEL) {
-    row0 = pair / p.kv_heads;
+    row0 = of;
     if (guess_at < p.n_sel) guess = p.sel[((int64_t)row0 * p.kv_heads + kvh) * p.n_sel + guess_at];
     const SeqRow sr = find_row(a, row0);
     b = sr.b;
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     len = sr.pos + 1;
     if (row0 >= a.cu[b + 1]) return;
   } else {
-    b = pair / p.kv_heads;
+    b = of;
     if (guess_at < a.width) guess = a.table[(int64_t)b * a.width + guess_at];
     row0 = max(a.cu[b], 0);
     n = min(a.cu[b + 1], a.rows) - row0;
@@ -224,13 +225,13 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     // positions of the tile's columns, and this workgroup's pages: positions in
     // the block table, or in the row's list; a wave takes every fourth
     const int c_hi = min(tile * 16 + 15, cols - 1);
-    const int pos_lo = SEL ? len - 1 : len - n + tile * 16 / R;
-    const int pos_hi = SEL ? len - 1 : len - n + c_hi / R;
+    const int pos_lo = SEL ? len - 1 : len - n + p.group_by.div(tile * 16);
+    const int pos_hi = SEL ? len - 1 : len - n + p.group_by.div(c_hi);
     const int64_t pages64 = ((int64_t)pos_hi + 64) / 64;
     const int pages = (int)(pages64 < a.width ? pages64 : a.width);
     const int first = !SEL && p.window > 0 ? max(pos_lo - p.window + 1, 0) / 64 : 0;
     const int total = SEL ? p.n_sel : max(pages - first, 0);
-    const int per = max(p.split_pages, (total + p.splits - 1) / p.splits);
+    const int per = max(p.split_pages, p.splits_by.div(total + p.splits - 1));
     const int j0 = min(split * per, total), j1 = min(j0 + per, total);
     const int count = (j1 - j0 - wave + NW - 1) / NW;
 
@@ -275,8 +276,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     // behind them
     const int col = tile * 16 + l;
     const bool on = col < cols;
-    const int row = on ? row0 + col / R : -1, head = kvh * R + col % R;
-    const int pos = on ? (SEL ? len - 1 : len - n + col / R) : -1;
+    const int nth = p.group_by.div(col);
+    const int row = on ? row0 + nth : -1, head = kvh * R + col - nth * R;
+    const int pos = on ? (SEL ? len - 1 : len - n + nth) : -1;
     u4v qv[G];
     {
       const uint16_t* q = a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r;
@@ -717,6 +719,10 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   p.data = cache->data;
   p.n_pages = cache->n_pages;
   p.kv_heads = (int)cache->n_kv_heads;
+  p.kv_heads_by = Divisor(cache->n_kv_heads);
+  p.group_by = Divisor(rows->n_heads / cache->n_kv_heads);
+  p.pairs_by = Divisor(plan.pairs);
+  p.splits_by = Divisor(plan.splits);
   p.window = window > 0x40000000 ? 0 : (int)window;
   p.n_sel = (int)n_sel;
   p.tiles = (int)plan.tiles;
