@@ -171,13 +171,13 @@ struct AttnArgs {
   float* part;            // [row][head][split][D], then [row][head][split][4]: sum, maximum, exact sum
 };
 
-template <int DT, int D, bool SEL, int NW>
+template <int DT, int D, bool SEL, int NW, int CT>
 __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
   using TS = TileShape<D>;
   constexpr int G = TS::G, J = TS::J;
-  constexpr int NT = D <= 128 ? 2 : 1;        // tiles taken together
+  constexpr int NT = D <= 128 && CT == 1 ? 2 : 1;        // tiles taken together
   constexpr bool REST = DT == WQ_DT_F16;      // weights with their FP16 remainder
-  constexpr int kPart = (4 * J + 3) * 64;     // floats a wave keeps in LDS
+  constexpr int kPart = (4 * J + 3) * 64;     // floats a wave keeps in LDS, a column tile
   extern __shared__ __attribute__((aligned(16))) float s_merge[];
   const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -221,11 +221,11 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
   uint32_t magic = 0x64006400u;   // in a VGPR: the mask and it are then one instruction
   asm("" : "+v"(magic));
 
-  for (int tile = tile0; tile * 16 < cols; tile += p.tiles) {
+  for (int tile = tile0; tile * (16 * CT) < cols; tile += p.tiles) {
     // positions of the tile's columns, and this workgroup's pages: positions in
     // the block table, or in the row's list; a wave takes every fourth
-    const int c_hi = min(tile * 16 + 15, cols - 1);
-    const int pos_lo = SEL ? len - 1 : len - n + p.group_by.div(tile * 16);
+    const int c_hi = min(tile * (16 * CT) + 16 * CT - 1, cols - 1);
+    const int pos_lo = SEL ? len - 1 : len - n + p.group_by.div(tile * (16 * CT));
     const int pos_hi = SEL ? len - 1 : len - n + p.group_by.div(c_hi);
     const int64_t pages64 = ((int64_t)pos_hi + 64) / 64;
     const int pages = (int)(pages64 < a.width ? pages64 : a.width);
@@ -274,32 +274,36 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     };
     // this lane's column, its query's loads ahead of the pages' and its scaling
     // behind them
-    const int col = tile * 16 + l;
-    const bool on = col < cols;
-    const int nth = p.group_by.div(col);
-    const int row = on ? row0 + nth : -1, head = kvh * R + col - nth * R;
-    const int pos = on ? (SEL ? len - 1 : len - n + nth) : -1;
-    u4v qv[G];
-    {
-      const uint16_t* q = a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r;
+    int row[CT], head[CT], pos[CT];
+    u4v qv[CT][G];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int col = tile * (16 * CT) + 16 * ct + l;
+      const bool on = col < cols;
+      const int nth = p.group_by.div(col);
+      row[ct] = on ? row0 + nth : -1;
+      head[ct] = kvh * R + col - nth * R;
+      pos[ct] = on ? (SEL ? len - 1 : len - n + nth) : -1;
+      const uint16_t* q = a.q + (on ? row[ct] * a.q_row + head[ct] * a.q_head : 0) + 8 * r;
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        qv[g] = on ? *reinterpret_cast<const u4v*>(q + 32 * g) : u4v{0, 0, 0, 0};
+        qv[ct][g] = on ? *reinterpret_cast<const u4v*>(q + 32 * g) : u4v{0, 0, 0, 0};
     }
     next();
     if (at >= 0) {
       load_keys();
       load_values();
     }
-    h8 Q[G], SQ;
-    float c1, c2;
-    {
+    h8 Q[CT][G], SQ[CT];
+    float c1[CT], c2[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
       float top = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          top = fmaxf(top, fabsf(to_float<DT>((uint16_t)(qv[g][i >> 1] >> (16 * (i & 1))))));
+          top = fmaxf(top, fabsf(to_float<DT>((uint16_t)(qv[ct][g][i >> 1] >> (16 * (i & 1))))));
       }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -312,9 +316,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float y =
-              ldexpf(to_float<DT>((uint16_t)(qv[g][i >> 1] >> (16 * (i & 1)))), 14 - e);
+              ldexpf(to_float<DT>((uint16_t)(qv[ct][g][i >> 1] >> (16 * (i & 1)))), 14 - e);
           sum += y;
-          Q[g][i] = (_Float16)(i & 2 ? y * 0.0625f : y);
+          Q[ct][g][i] = (_Float16)(i & 2 ? y * 0.0625f : y);
         }
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
@@ -324,43 +328,52 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
                                      : r == 1 ? __builtin_bit_cast(uint16_t, lo) : 0u;
         sq[g >> 1] |= bits << (16 * (g & 1));
       }
-      SQ = __builtin_bit_cast(h8, u4v{sq[0], sq[1], sq[2], sq[3]});
+      SQ[ct] = __builtin_bit_cast(h8, u4v{sq[0], sq[1], sq[2], sq[3]});
       const float f = p.scale * 1.44269504f;
-      c1 = ldexpf(f, e - 14 + 24);
-      c2 = ldexpf(f, e - 14 + 6);
+      c1[ct] = ldexpf(f, e - 14 + 24);
+      c2[ct] = ldexpf(f, e - 14 + 6);
     }
 
-    f4 O[J], OZ = {0, 0, 0, 0};
-    float m = -INFINITY, m_kept = -INFINITY;
-    float exact = 0.f;      // this lane's weights before their rounding, for lse
+    f4 O[CT][J], OZ[CT];
+    float m[CT], m_kept[CT];
+    float exact[CT];        // this lane's weights before their rounding, for lse
     int vexp = 0;           // value scales since the last fold are below 2^(vexp + 1)
     bool kept = false;
 #pragma unroll
-    for (int j = 0; j < J; ++j) O[j] = f4{0, 0, 0, 0};
+    for (int ct = 0; ct < CT; ++ct) {
+      m[ct] = m_kept[ct] = -INFINITY;
+      exact[ct] = 0.f;
+      OZ[ct] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < J; ++j) O[ct][j] = f4{0, 0, 0, 0};
+    }
     // Folds code sums and offsets into the wave's values in LDS.  The two nearly
     // cancel, and a matrix-core sum loses a little to every addition: over a long
     // cache what they have in common would swallow the result's last bits.
     auto fold = [&]() {
       const float up = ldexpf(1.f, vexp);
-      float* const s = s_merge + wave * kPart;
-      f4* const s4 = reinterpret_cast<f4*>(s) + lane;
-      const float f = m_kept == m ? 1.f : __builtin_amdgcn_exp2f(m_kept - m);
-      float z[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) z[g] = __shfl(OZ[g & 3], (g >> 2) * 16 + l);
-      float sum = __shfl(OZ[0], 32 + l);
+      for (int ct = 0; ct < CT; ++ct) {
+        float* const s = s_merge + (wave * CT + ct) * kPart;
+        f4* const s4 = reinterpret_cast<f4*>(s) + lane;
+        const float f = m_kept[ct] == m[ct] ? 1.f : __builtin_amdgcn_exp2f(m_kept[ct] - m[ct]);
+        float z[G];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        f4 v = O[j] * up + z[j >> 1];
-        if (kept) v += s4[j * 64] * f;
-        s4[j * 64] = v;
-        O[j] = f4{0, 0, 0, 0};
+        for (int g = 0; g < G; ++g) z[g] = __shfl(OZ[ct][g & 3], (g >> 2) * 16 + l);
+        float sum = __shfl(OZ[ct][0], 32 + l);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          f4 v = O[ct][j] * up + z[j >> 1];
+          if (kept) v += s4[j * 64] * f;
+          s4[j * 64] = v;
+          O[ct][j] = f4{0, 0, 0, 0};
+        }
+        if (kept) sum += s[4 * J * 64 + lane] * f;
+        s[4 * J * 64 + lane] = sum;
+        s[(4 * J + 1) * 64 + lane] = m[ct];
+        OZ[ct] = f4{0, 0, 0, 0};
+        m_kept[ct] = m[ct];
       }
-      if (kept) sum += s[4 * J * 64 + lane] * f;
-      s[4 * J * 64 + lane] = sum;
-      s[(4 * J + 1) * 64 + lane] = m;
-      OZ = f4{0, 0, 0, 0};
-      m_kept = m;
       vexp = 0;
       kept = true;
     };
@@ -374,31 +387,41 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
       ++since;
       const int t0 = at * 64 + part * 32;
       // logits: sums of codes times queries by group, and of offsets
-      f4 sc[2 * NT], zt[2 * NT];
+      f4 sc[CT][2 * NT], zt[CT][2 * NT];
       unroll<2 * NT>([&](auto uu) {
         constexpr int u = uu, t = u / 2, h = u % 2;
         uint32_t zw[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < TS::ZN; ++i) zw[i] = kt[t].offsets[h][i];
         if (u == 2) __builtin_amdgcn_sched_barrier(0);
-        zt[u] = mfma(__builtin_bit_cast(h8, u4v{zw[0], zw[1], zw[2], zw[3]}), SQ, f4{0, 0, 0, 0});
-        f4 s = {0, 0, 0, 0};
+        const h8 za = __builtin_bit_cast(h8, u4v{zw[0], zw[1], zw[2], zw[3]});
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          zt[ct][u] = mfma(za, SQ[ct], f4{0, 0, 0, 0});
+          sc[ct][u] = f4{0, 0, 0, 0};
+        }
         unroll<G>([&](auto g) {
-          const f4 d = mfma(code_operand(kt[t].codes[h][g]), Q[g], f4{0, 0, 0, 0});
+          const h8 ka = code_operand(kt[t].codes[h][g]);
           const h2 s0 = TS::template scale2<g * 4 + 2 * h>(kt[t].scales);
           const h2 s1 = TS::template scale2<g * 4 + 2 * h + 1>(kt[t].scales);
-          s[0] = __builtin_fmaf((float)s0[0], d[0], s[0]);
-          s[1] = __builtin_fmaf((float)s0[1], d[1], s[1]);
-          s[2] = __builtin_fmaf((float)s1[0], d[2], s[2]);
-          s[3] = __builtin_fmaf((float)s1[1], d[3], s[3]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const f4 d = mfma(ka, Q[ct][g], f4{0, 0, 0, 0});
+            f4& s = sc[ct][u];
+            s[0] = __builtin_fmaf((float)s0[0], d[0], s[0]);
+            s[1] = __builtin_fmaf((float)s0[1], d[1], s[1]);
+            s[2] = __builtin_fmaf((float)s1[0], d[2], s[2]);
+            s[3] = __builtin_fmaf((float)s1[1], d[3], s[3]);
+          }
         });
-        sc[u] = s;
       });
       // the keys' registers are free: the next step's keys arrive behind the
       // values' product, its values behind the next logits
 #pragma unroll
-      for (int u = 0; u < 2 * NT; ++u)
-        asm volatile("" : "+v"(sc[u]), "+v"(zt[u]));   // done here, not after the loads
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int u = 0; u < 2 * NT; ++u)
+          asm volatile("" : "+v"(sc[ct][u]), "+v"(zt[ct][u]));   // done here, not after the loads
       __builtin_amdgcn_sched_barrier(0);
       next();
       load_keys();           // past the last step: that step's again, not used
@@ -406,44 +429,59 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 
       // base-2 logits above the running maximum, plus kWeightExp
       constexpr int NY = 8 * NT;
-      const bool none = m == -INFINITY;
-      const float m8 = none ? -kWeightExp : m - kWeightExp;
-      float y[NY], top = -INFINITY;
+      float y[CT][NY], top[CT];
+      bool raise = false;
+      const bool edge = t0 + 32 * NT - 1 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
 #pragma unroll
-      for (int i = 0; i < NY; ++i)
-        y[i] = __builtin_fmaf(sc[i >> 2][i & 3], c1, __builtin_fmaf(zt[i >> 2][i & 3], c2, -m8));
-      if (t0 + 32 * NT - 1 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window)) {
-        asm volatile("");      // stays a branch: few pages have an edge
+      for (int ct = 0; ct < CT; ++ct) {
+        const bool none = m[ct] == -INFINITY;
+        const float m8 = none ? -kWeightExp : m[ct] - kWeightExp;
 #pragma unroll
-        for (int i = 0; i < NY; ++i) {
-          const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
-          if (t > pos || (p.window > 0 && t <= pos - p.window)) y[i] = -INFINITY;
+        for (int i = 0; i < NY; ++i)
+          y[ct][i] = __builtin_fmaf(sc[ct][i >> 2][i & 3], c1[ct],
+                                    __builtin_fmaf(zt[ct][i >> 2][i & 3], c2[ct], -m8));
+        if (edge) {
+          asm volatile("");      // stays a branch: few pages have an edge
+#pragma unroll
+          for (int i = 0; i < NY; ++i) {
+            const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
+            if (t > pos[ct] || (p.window > 0 && t <= pos[ct] - p.window)) y[ct][i] = -INFINITY;
+          }
+        }
+        top[ct] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NY; ++i) top[ct] = fmaxf(top[ct], y[ct][i]);
+        raise |= top[ct] > (none ? -INFINITY : kWeightExp + kRaise);
+      }
+      if (__any(raise)) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const bool none = m[ct] == -INFINITY;
+          float most = fmaxf(top[ct], __shfl_xor(top[ct], 16));
+          most = fmaxf(most, __shfl_xor(most, 32));
+          // the maximum in y's scale stands at kWeightExp
+          const float up = none ? (most == -INFINITY ? 0.f : most - kWeightExp)
+                                : fmaxf(most - kWeightExp, 0.f);
+          const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
+          if (!none) m[ct] += up;
+          else if (most != -INFINITY) m[ct] = up;
+#pragma unroll
+          for (int i = 0; i < NY; ++i) y[ct][i] -= up;
+#pragma unroll
+          for (int j = 0; j < J; ++j) O[ct][j] *= f;
+          OZ[ct] *= f;
+          exact[ct] *= f;
         }
       }
 #pragma unroll
-      for (int i = 0; i < NY; ++i) top = fmaxf(top, y[i]);
-      if (__any(top > (none ? -INFINITY : kWeightExp + kRaise))) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        // the maximum in y's scale stands at kWeightExp
-        const float up = none ? (top == -INFINITY ? 0.f : top - kWeightExp)
-                              : fmaxf(top - kWeightExp, 0.f);
-        const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
-        if (!none) m += up;
-        else if (top != -INFINITY) m = up;
+      for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
-        for (int i = 0; i < NY; ++i) y[i] -= up;
+        for (int i = 0; i < NY; ++i) y[ct][i] = __builtin_amdgcn_exp2f(y[ct][i]);
+        if (p.lse != nullptr) {
+          asm volatile("");      // stays a branch
 #pragma unroll
-        for (int j = 0; j < J; ++j) O[j] *= f;
-        OZ *= f;
-        exact *= f;
-      }
-#pragma unroll
-      for (int i = 0; i < NY; ++i) y[i] = __builtin_amdgcn_exp2f(y[i]);
-      if (p.lse != nullptr) {
-        asm volatile("");      // stays a branch
-#pragma unroll
-        for (int i = 0; i < NY; ++i) exact += y[i];
+          for (int i = 0; i < NY; ++i) exact[ct] += y[ct][i];
+        }
       }
 
       if (t0 + 32 * NT > written) {
@@ -472,7 +510,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
           const float f = ldexpf(1.f, vexp - e);
           vexp = e;
 #pragma unroll
-          for (int j = 0; j < J; ++j) O[j] *= f;
+          for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int j = 0; j < J; ++j) O[ct][j] *= f;
         }
       }
       const _Float16 d1 = (_Float16)ldexpf(1.f, -vexp), d16 = (_Float16)ldexpf(0.0625f, -vexp);
@@ -482,44 +522,50 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         __builtin_amdgcn_sched_barrier(0);
-        u4v z = vt[t].offsets, wv;
+        u4v z = vt[t].offsets;
         if (l >= G) z = u4v{fill, fill, fill, fill};
-        h2 ws[4], wr[4];
-        u4v rv;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float y0 = y[8 * t + 2 * x], y1 = y[8 * t + 2 * x + 1];
-          const h2 w = {(_Float16)y0, (_Float16)y1};
-          wv[x] = as_u32(w);
-          ws[x] = w * (x & 1 ? down16 : down);
-          if constexpr (REST) {
-            const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
-            rv[x] = as_u32(rest);
-            wr[x] = rest * (x & 1 ? down16 : down);
-          }
-        }
         const h8 za = __builtin_bit_cast(h8, z);
-        OZ = mfma(za, __builtin_bit_cast(h8, wv), OZ);
-        if constexpr (REST) OZ = mfma(za, __builtin_bit_cast(h8, rv), OZ);
+        h2 ws[CT][4], wr[CT][4];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          u4v wv, rv;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float y0 = y[ct][8 * t + 2 * x], y1 = y[ct][8 * t + 2 * x + 1];
+            const h2 w = {(_Float16)y0, (_Float16)y1};
+            wv[x] = as_u32(w);
+            ws[ct][x] = w * (x & 1 ? down16 : down);
+            if constexpr (REST) {
+              const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
+              rv[x] = as_u32(rest);
+              wr[ct][x] = rest * (x & 1 ? down16 : down);
+            }
+          }
+          OZ[ct] = mfma(za, __builtin_bit_cast(h8, wv), OZ[ct]);
+          if constexpr (REST) OZ[ct] = mfma(za, __builtin_bit_cast(h8, rv), OZ[ct]);
+        }
         unroll<G>([&](auto g) {
           h2 s[4];
           unroll<4>([&](auto x) { s[x] = TS::template scale2<g * 4 + x>(vt[t].scales); });
           const h8 v0 = normal_operand(vt[t].codes[2 * g], magic);
           const h8 v1 = normal_operand(vt[t].codes[2 * g + 1], magic);
-          u4v hi, lo;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const h2 h = ws[x] * s[x];
-            hi[x] = as_u32(h);
-            h2 rest = __builtin_elementwise_fma(ws[x], s[x], -h);
-            if constexpr (REST) rest = __builtin_elementwise_fma(wr[x], s[x], rest);
-            lo[x] = as_u32(rest);
+          for (int ct = 0; ct < CT; ++ct) {
+            u4v hi, lo;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const h2 h = ws[ct][x] * s[x];
+              hi[x] = as_u32(h);
+              h2 rest = __builtin_elementwise_fma(ws[ct][x], s[x], -h);
+              if constexpr (REST) rest = __builtin_elementwise_fma(wr[ct][x], s[x], rest);
+              lo[x] = as_u32(rest);
+            }
+            const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
+            O[ct][2 * g] = mfma(v0, hb, O[ct][2 * g]);
+            O[ct][2 * g + 1] = mfma(v1, hb, O[ct][2 * g + 1]);
+            O[ct][2 * g] = mfma(v0, lb, O[ct][2 * g]);
+            O[ct][2 * g + 1] = mfma(v1, lb, O[ct][2 * g + 1]);
           }
-          const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
-          O[2 * g] = mfma(v0, hb, O[2 * g]);
-          O[2 * g + 1] = mfma(v1, hb, O[2 * g + 1]);
-          O[2 * g] = mfma(v0, lb, O[2 * g]);
-          O[2 * g + 1] = mfma(v1, lb, O[2 * g + 1]);
         });
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -528,31 +574,36 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 
     fold();
     if (p.lse != nullptr) {
-      exact += __shfl_xor(exact, 16);
-      exact += __shfl_xor(exact, 32);
-      s_merge[wave * kPart + (4 * J + 2) * 64 + lane] = exact;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        exact[ct] += __shfl_xor(exact[ct], 16);
+        exact[ct] += __shfl_xor(exact[ct], 32);
+        s_merge[(wave * CT + ct) * kPart + (4 * J + 2) * 64 + lane] = exact[ct];
+      }
     }
     // the waves' parts joined in order
     __syncthreads();
-    if (on) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      if (row[ct] < 0) continue;
+      auto part_of = [&](int w) { return s_merge + (w * CT + ct) * kPart; };
       float mw[NW], mx = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        mw[w] = s_merge[w * kPart + (4 * J + 1) * 64 + lane];
+        mw[w] = part_of(w)[(4 * J + 1) * 64 + lane];
         mx = fmaxf(mx, mw[w]);
       }
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
         mw[w] = mw[w] == mx ? 1.f : __builtin_amdgcn_exp2f(mw[w] - mx);
-        sum += mw[w] * s_merge[w * kPart + 4 * J * 64 + lane];
+        sum += mw[w] * part_of(w)[4 * J * 64 + lane];
       }
-      const int64_t out_at = (int64_t)row * a.heads + head;
+      const int64_t out_at = (int64_t)row[ct] * a.heads + head[ct];
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       for (int j = wave; j < J; j += NW) {
         f4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-          o += mw[w] * reinterpret_cast<const f4*>(s_merge + w * kPart)[j * 64 + lane];
+        for (int w = 0; w < NW; ++w) o += mw[w] * reinterpret_cast<const f4*>(part_of(w))[j * 64 + lane];
         const int d = 16 * j + 4 * r;
         if (p.splits == 1) {
           uint16_t h[4];
@@ -567,8 +618,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
         float ex = 0.f;
         if (p.lse != nullptr)
 #pragma unroll
-          for (int w = 0; w < NW; ++w)
-            ex += mw[w] * s_merge[w * kPart + (4 * J + 2) * 64 + lane];
+          for (int w = 0; w < NW; ++w) ex += mw[w] * part_of(w)[(4 * J + 2) * 64 + lane];
         if (p.splits == 1) {
           if (p.lse != nullptr) p.lse[out_at] = log_sum(ex, mx);
         } else {
@@ -637,14 +687,18 @@ join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t*
 // How a call is split: column tiles of a sequence (or row) and splits of its pages.
 struct AttnPlan {
   int64_t pairs, tiles, splits, split_pages;
-  int waves;
+  int waves, ct;            // waves a workgroup, column tiles a wave
 };
 static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t max_rows,
                           int64_t max_len, int64_t n_sel, bool sel) {
   AttnPlan p{};
   const int64_t R = a->n_heads / c->n_kv_heads;
   const int64_t cols = (sel || max_rows < 1 ? 1 : max_rows) * R;
-  p.tiles = (cols + 15) / 16;
+  // Two column tiles share the codes' unpacking where there are enough of them: a
+  // 512-token piece of two prompts over 6000 tokens takes 218 us with two, 265 with
+  // one.  Heads of 256 channels would not fit their registers.
+  p.ct = !sel && c->head_dim <= 128 && cols >= 64 ? 2 : 1;
+  p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
   p.pairs = (sel ? a->n_rows : a->n_seqs) * c->n_kv_heads;
   int64_t pages = sel ? n_sel : (max_len + 63) / 64;
   if (!sel && pages > a->table_width) pages = a->table_width;
@@ -662,7 +716,7 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
   p.waves = kAttnWaves;
   if (items <= 256 && pages <= 2 * kAttnMoreWaves) {
     splits = 1;
-    if (pages > kAttnWaves) p.waves = kAttnMoreWaves;
+    if (pages > kAttnWaves && p.ct == 1) p.waves = kAttnMoreWaves;
   }
   p.split_pages = (pages + splits - 1) / splits;
   p.splits = (pages + p.split_pages - 1) / p.split_pages;
@@ -737,19 +791,21 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
     constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
     auto launch = [&](auto kernel) {
-      const size_t lds = (size_t)plan.waves * (D / 4 + 3) * 64 * 4;
+      const size_t lds = (size_t)plan.waves * plan.ct * (D / 4 + 3) * 64 * 4;
       if (!allow_lds((const void*)kernel, lds)) {
         status = wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
         return;
       }
       kernel<<<dim3((unsigned)grid), plan.waves * kWave, lds, (hipStream_t)stream>>>(p);
     };
-    if (plan.waves == kAttnWaves) {
-      if (sel != nullptr) launch(attn_kernel<DT, D, true, kAttnWaves>);
-      else launch(attn_kernel<DT, D, false, kAttnWaves>);
+    if (plan.ct == 2) {
+      if constexpr (D <= 128) launch(attn_kernel<DT, D, false, kAttnWaves, 2>);
+    } else if (plan.waves == kAttnWaves) {
+      if (sel != nullptr) launch(attn_kernel<DT, D, true, kAttnWaves, 1>);
+      else launch(attn_kernel<DT, D, false, kAttnWaves, 1>);
     } else {
-      if (sel != nullptr) launch(attn_kernel<DT, D, true, kAttnMoreWaves>);
-      else launch(attn_kernel<DT, D, false, kAttnMoreWaves>);
+      if (sel != nullptr) launch(attn_kernel<DT, D, true, kAttnMoreWaves, 1>);
+      else launch(attn_kernel<DT, D, false, kAttnMoreWaves, 1>);
     }
     if (status == WQ_OK && plan.splits > 1)
       join_kernel<DT, D><<<dim3((unsigned)items), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(

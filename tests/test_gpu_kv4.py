@@ -509,3 +509,95 @@ def test_long_cache_addresses_past_32_bits():
     for s, w in ((None, None), (sel, want)):
         out = cache.attention(q, *args, 2, 150, sel=s)
         check_attention(out, None, made, q, np.array([0, 2]), D ** -0.5, 0, w, "far pages")
+
+
+# --------------------------------------------- many rows, memory, example
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 1, 70])
+def test_attention_two_column_tiles(D, window):
+    """Rows enough for two column tiles a wave, ending inside the second or the
+    first, windows, large value scales and rows before the first token."""
+    for lens, rows, heads in (([300, 40], [75, 40], 2), ([130, 0], [33, 3], 4), ([90], [130], 1)):
+        made = Made(lens, 1, D, seed=11, v_scale=2.0)
+        for dtype in TYPES.values():
+            attend(made, made.gpu(), rows, heads, dtype, window=window, label=f"{D} {rows} {heads} {window}")
+
+
+def test_bad_row_tables_stay_in_bounds():
+    """cu_rows that does not rise, runs past the rows or is negative, and lengths
+    out of step with the table: nothing outside the given rows is written."""
+    made = Made([100, 50, 200], 2, 64, seed=2)
+    cache = made.gpu()
+    q = torch.randn(6, 4, 64, generator=torch.Generator().manual_seed(3)).half().cuda()
+    room = torch.full((10, 4, 64), 5.0, dtype=torch.float16, device="cuda")
+    for cu in ([0, 4, 2, 6], [0, 9, 12, 50], [-3, 1, 2, 6], [5, 5, 5, 5], [0, 2, 4, 6]):
+        for lens in (made.lens, [1 << 30, -5, 0]):
+            cache.attention(q, ints(made.table), ints(lens), ints(cu), 2, 200, out=room[2:8])
+            sel = cache.select(q, ints(made.table), ints(lens), ints(cu), 2)
+            cache.attention(q, ints(made.table), ints(lens), ints(cu), 2, 200, sel=sel, out=room[2:8])
+            slots, runs = ints(np.zeros(6)), ints(np.zeros((6, 2)))
+            B.wq_kv4_plan(ints(lens), ints(cu), ints(made.table), ints([1, 2]), ints([0, 0, 0]), slots, runs, ints([0]))
+    torch.cuda.synchronize()
+    assert (room[:2] == 5).all() and (room[8:] == 5).all()
+
+
+def test_launch_loop_keeps_device_memory_flat():
+    """The library allocates nothing: the caller's workspaces are all there is."""
+    made = Made([3000, 100], 2, 128, seed=1)
+    cache = made.gpu()
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(3)).half().cuda()
+    args = (ints(made.table), ints(made.lens), ints([0, 1, 2]))
+    out, sel = torch.empty_like(q), ints(np.zeros((2, 2, 5)))
+    work = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+
+    def once():
+        cache.select(q, *args, 5, sel=sel, workspace=work)
+        cache.attention(q, *args, 1, 3000, out=out, workspace=work)
+        cache.attention(q, *args, 1, 3000, sel=sel, out=out, workspace=work)
+
+    for _ in range(500):
+        once()
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    for _ in range(2000):
+        once()
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free
+
+
+@pytest.mark.parametrize("pages", [0, 3])
+def test_example_block(pages):
+    """The example's decode steps, small, against the oracle: the cache's bytes, the
+    attention's output from the step's own queries, and the growing lengths."""
+    import os
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import kv4_decode
+    block = kv4_decode.Block(3, 400, hidden=512, heads=8, kv_heads=2, dim=64)
+    prompt = [62, 200, 1]
+    kv = block.fill(prompt)
+    made = Made([0], 2, 64, extra=0)
+    made.data, made.summary = np.zeros(block.cache.data.shape, np.uint8), np.zeros(block.cache.summary.shape, np.float16)
+    made.n_pages = len(made.data)
+    free = torch.randperm(made.n_pages, generator=torch.Generator().manual_seed(0)).numpy()
+    made.table, made.lens, slots, _, taken = K4.plan(np.zeros(3, np.int64), np.concatenate([[0], np.cumsum(prompt)]),
+                                                     np.full(block.table.shape, -1), free)
+    free = np.roll(free, -taken)
+    K4.append(made.data, made.summary, f32(kv[0]), f32(kv[1]), slots)
+    step, x, proj, att, y = block.stepper(pages)
+    cu = np.arange(4)
+    g = torch.Generator().manual_seed(1)
+    for i in range(4):
+        x.copy_(torch.randn(x.shape, generator=g).half().view(torch.int16))
+        step()
+        torch.cuda.synchronize()
+        q, k, v = block.split(proj)
+        made.table, made.lens, slots, _, taken = K4.plan(made.lens, cu, made.table, free)
+        free = np.roll(free, -taken)
+        K4.append(made.data, made.summary, f32(k), f32(v), slots)
+        assert np.array_equal(block.cache.data.cpu().numpy(), made.data), i
+        assert np.array_equal(host(block.lens), made.lens) and np.array_equal(host(block.table), made.table)
+        sel = K4.select(made.summary, f32(q), made.table, made.lens, cu, pages) if pages else None
+        check_attention(att, None, made, q, cu, 64 ** -0.5, 0, sel, f"example step {i}")
+        assert torch.isfinite(y.view(torch.float16).float()).all() and (y != 0).any()
