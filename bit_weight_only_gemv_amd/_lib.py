@@ -144,12 +144,12 @@ class WQError(RuntimeError):
 
 _lib: Optional[ctypes.CDLL] = None
 _int32 = None       # torch.int32, once the library is loaded
-_raw_stream = None  # torch's current stream of a device as a handle, where it has that call
+_raw_stream = _current_device = None  # torch's current stream of a device as a handle, where it has that call
 
 
 def load() -> ctypes.CDLL:
     """Loads the library (raises if it has not been built)."""
-    global _lib, _int32, _raw_stream
+    global _lib, _int32, _raw_stream, _current_device
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -164,6 +164,7 @@ def load() -> ctypes.CDLL:
         fn.argtypes = args
     _int32 = torch.int32
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = torch.cuda.current_device
     _lib = lib
     return lib
 
@@ -323,9 +324,9 @@ def _dptr(t) -> int:
 
 def _stream(stream):
     if stream is None:
-        import torch
         if _raw_stream is not None:     # a tenth of current_stream()'s time
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
+        import torch
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -451,9 +452,9 @@ def wq_kv4_max_runs(n_seqs: int, n_rows: int) -> int:
 
 def _i32(t, shape, what):
     """Pointer of a contiguous int32 GPU tensor of the given shape."""
-    if t.dtype is not _int32 or t.shape != shape:
-        raise ValueError(f"{what} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return _dptr(t)
+    if t.dtype is _int32 and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous GPU tensor, int32 {list(shape)}: got {t.dtype} {list(t.shape)}")
 
 
 def wq_kv4_plan(lens, cu_rows, block_table, free_pages, new_lens, slots, runs, taken, stream=None):

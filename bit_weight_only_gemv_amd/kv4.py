@@ -17,13 +17,17 @@ import ctypes
 from . import _lib as L
 
 
+_TYPES = {"torch.float16": L.WQ_DT_F16, "torch.bfloat16": L.WQ_DT_BF16}
+
+
 def _dtype(t):
-    import torch
-    if t.dtype == torch.float16:
-        return L.WQ_DT_F16
-    if t.dtype == torch.bfloat16:
-        return L.WQ_DT_BF16
-    raise ValueError(f"float16 or bfloat16 expected, got {t.dtype}")
+    d = _TYPES.get(t.dtype)
+    if d is None:                       # by name the first time, then by type
+        d = _TYPES.get(str(t.dtype))
+        if d is None:
+            raise ValueError(f"float16 or bfloat16 expected, got {t.dtype}")
+        _TYPES[t.dtype] = d
+    return d
 
 
 def _strided(t, what):
