@@ -15,9 +15,8 @@
 //
 // Precision.  Queries are scaled by a power of two to [2^14, 2^15) and so are
 // exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  A softmax
-// weight is an FP16 number and its FP16 remainder (22 bits); for BF16 outputs the
-// number alone, rounded once (2^-12, against the output's 2^-9), and then that is
-// what every sum uses, the denominator's too.  A weight times a scale enters the
+// weight is an FP16 number and its FP16 remainder (22 bits), for BF16 outputs too:
+// rounded to 11 bits it shows where values of both signs nearly cancel.  A weight times a scale enters the
 // product as an FP16 head and remainder as well: the codes' part and the offsets'
 // part nearly cancel where a group lies far from 0, so a rounding there would not
 // stay small.  Weights carry 2^8, and value scales of 2
@@ -187,7 +186,6 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
   using TS = TileShape<D>;
   constexpr int G = TS::G, J = TS::J;
   constexpr int NT = D <= 128 && CT == 1 ? 2 : 1;        // tiles taken together
-  constexpr bool REST = DT == WQ_DT_F16;      // weights with their FP16 remainder
   constexpr int kPart = (4 * J + 3) * 64;     // floats a wave keeps in LDS, a column tile
   extern __shared__ __attribute__((aligned(16))) float s_merge[];
   const KvRows& a = p.a;
@@ -546,14 +544,12 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
             const h2 w = {(_Float16)y0, (_Float16)y1};
             wv[x] = as_u32(w);
             ws[ct][x] = w * (x & 1 ? down16 : down);
-            if constexpr (REST) {
-              const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
-              rv[x] = as_u32(rest);
-              wr[ct][x] = rest * (x & 1 ? down16 : down);
-            }
+            const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
+            rv[x] = as_u32(rest);
+            wr[ct][x] = rest * (x & 1 ? down16 : down);
           }
           OZ[ct] = mfma(za, __builtin_bit_cast(h8, wv), OZ[ct]);
-          if constexpr (REST) OZ[ct] = mfma(za, __builtin_bit_cast(h8, rv), OZ[ct]);
+          OZ[ct] = mfma(za, __builtin_bit_cast(h8, rv), OZ[ct]);
         }
         unroll<G>([&](auto g) {
           h2 s[4];
@@ -568,7 +564,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
               const h2 h = ws[ct][x] * s[x];
               hi[x] = as_u32(h);
               h2 rest = __builtin_elementwise_fma(ws[ct][x], s[x], -h);
-              if constexpr (REST) rest = __builtin_elementwise_fma(wr[ct][x], s[x], rest);
+              rest = __builtin_elementwise_fma(wr[ct][x], s[x], rest);
               lo[x] = as_u32(rest);
             }
             const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);

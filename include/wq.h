@@ -480,7 +480,8 @@ int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t n_
  * in the row's pages.  A row that sees none gives zeros.  out is n_rows x
  * n_heads x D, contiguous; lse float32 [n_rows][n_heads] (NULL if not wanted)
  * receives log(sum_t exp(logit)), -inf where a row sees none.  Logits, softmax and
- * sums are held in float32; out is rounded once.
+ * sums are held in float32; a softmax weight enters its product with the values in
+ * 22 bits; out is rounded once.
  * max_rows and max_len are the largest n_b and lens the caller expects: they
  * choose how the work is split, and results hold for others as well.
  * workspace: wq_kv4_attention_workspace bytes for the same arguments, 16-byte

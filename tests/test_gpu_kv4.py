@@ -601,3 +601,31 @@ def test_example_block(pages):
         sel = K4.select(made.summary, f32(q), made.table, made.lens, cu, pages) if pages else None
         check_attention(att, None, made, q, cu, 64 ** -0.5, 0, sel, f"example step {i}")
         assert torch.isfinite(y.view(torch.float16).float()).all() and (y != 0).any()
+
+
+# ------------------------------------------ softmax weights and their range
+
+
+def check_held(out, made, q, cu, scale, label, sinks=0.0):
+    """check_attention's bound with nothing for the weights' own rounding, in either
+    type: weights are held in 22 bits or more, which 2^-17 covers with room.  sinks:
+    absolute error allowed, as the caller derives it."""
+    ref, _, size, top = K4.attention(made.data, f32(q), made.table, made.lens, cu, scale)
+    e_p = 2 * (64 * 2.0 ** -24 * top[..., None] + 2.0 ** -18) + 2.0 ** -17
+    tol = torch.finfo(q.dtype).eps / 2 * np.abs(ref) + e_p * (size + np.abs(ref)) + 2.0 ** -25 + sinks
+    worst = float((np.abs(host(out) - ref) / tol).max())
+    say(f"  {label}: worst |err|/bound = {worst:.4f}")
+    assert worst <= 1, label
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [[2, 3, 5], [64, 70], [1000]])
+def test_attention_weights_keep_their_bits(D, dtype, lens):
+    """Few values of both signs nearly cancel, and what a weight lost by a rounding
+    to 11 bits would show beside the small result."""
+    made = Made(lens, 2, D, seed=21, v_scale=1.0)
+    n = len(lens)
+    q = torch.randn(n, 16, D, generator=torch.Generator().manual_seed(4)).to(TYPES[dtype]).cuda()
+    out = made.gpu().attention(q, ints(made.table), ints(made.lens), ints(np.arange(n + 1)), 1, max(lens), scale=0.02)
+    check_held(out, made, q, np.arange(n + 1), 0.02, f"{D} {dtype} {lens}")
