@@ -6,24 +6,26 @@
 // group g, and the group's part of the query Q_g,
 //   logit = scale (sum_g S_g (c_g . Q_g) + sum_g Z_g sum(Q_g)),
 // and with the softmax weights p,
-//   out_d = sum_t (p_t S_{t,g(d)}) c_{t,d} + sum_t p_t Z_{t,g(d)}.
-// Both sums over codes are 16x16x32 products whose A operand is the codes: one
-// mask per two codes makes FP16 subnormals c 2^-24 (or 16 c 2^-24; B carries the
-// 1/16).  Tokens are the rows of the first product, so a lane ends with 4 tokens
+//   out_d = sum_t p_t (S_{t,g(d)} c_{t,d}) + sum_t p_t Z_{t,g(d)}.
+// Both are 16x16x32 products.  The first one's A operand is the codes: one mask per
+// two codes makes FP16 subnormals c 2^-24 (or 16 c 2^-24; B carries the 1/16).  The
+// second one's is S c.  Tokens are the rows of the first product, so a lane ends with 4 tokens
 // of one column per 16, and two such tiles are just its 8 k of the second
 // product's B operand: the weights never leave their registers.
 //
 // Precision.  Queries are scaled by a power of two to [2^14, 2^15) and so are
 // exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  A softmax
 // weight is an FP16 number and its FP16 remainder (22 bits), for BF16 outputs too:
-// rounded to 11 bits it shows where values of both signs nearly cancel.  A weight times a scale enters the
-// product as an FP16 head and remainder as well: the codes' part and the offsets'
-// part nearly cancel where a group lies far from 0, so a rounding there would not
-// stay small.  Weights carry 2^8, and value scales of 2
-// and more lower that by a running power of two, so that neither end of FP16's
-// range is met: a weight 2^-30 of the largest still counts.  The running maximum
-// is only raised when a logit passes it by 2^6, which spares most pages the
-// cross-lane maximum and the rescale of the sums.
+// rounded to 11 bits it shows where values of both signs nearly cancel.  S c is an
+// FP16 number and its remainder, which is exact.  Scales stay off the weights: a
+// small weight times a small scale would fall below FP16, and its token would count
+// as its group's minimum.  For the same reason the weights are relative to a
+// reference that follows the logits both ways: a page whose largest weight would
+// pass 2^14 or stay below 2^2 sets it to that logit, where weights carry 2^10.  So
+// 22 bits hold for what counts in a page, however small the page's share is
+// (behind a strong first token, say), and most pages are spared the cross-lane
+// maximum and the rescale of the sums.  The reference stays within 2^64 of the
+// highest, so that FP32 holds the sums.
 //
 // What bounds it.  One token a sequence over a long cache: the cache's bytes.
 // Four sequences of 131072 tokens, 8 heads of 128 channels, 671 MB: 131 us, where
@@ -46,8 +48,10 @@ namespace wqd {
 
 constexpr int kAttnWaves = 4, kAttnMoreWaves = 8;
 constexpr int kFoldPages = 8;        // 5% of the time at 2, and no closer
-constexpr float kWeightExp = 8.f;    // weights carry 2^8 ...
-constexpr float kRaise = 6.f;        // ... and grow by up to 2^6 before the maximum is raised
+constexpr float kWeightExp = 10.f;   // a page's largest weight at the reference is 2^10;
+constexpr float kRaise = 4.f;        // one of over 2^14 raises the reference,
+constexpr float kLower = 8.f;        // one of less than 2^2 lowers it,
+constexpr float kBelow = 64.f;       // by no more than 2^64 below the highest
 
 // f(0), ..., f(N - 1) with the index as a compile-time constant.
 template <typename F, int... I>
@@ -73,19 +77,15 @@ __device__ __forceinline__ h8 code_operand(uint32_t w) {
   return __builtin_bit_cast(h8, u4v{lo0, hi0, lo1, hi1});
 }
 
-// The same with the codes as normal numbers: c and 16 c.  A sum on the matrix
-// cores drops what lies below its largest operand's exponent, which subnormals
-// make 2^10 too large: here that would be a bias of 2^-19, and it matters where
-// many values average out.
-__device__ __forceinline__ h8 normal_operand(uint32_t w, uint32_t magic) {
-  const uint32_t w8 = w >> 8;
-  const uint32_t v[4] = {(w & 0x000F000Fu) | magic, (w & 0x00F000F0u) | magic,
-                         (w8 & 0x000F000Fu) | magic, (w8 & 0x00F000F0u) | magic};
-  u4v o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = as_u32(as_h2(v[i]) - h2{(_Float16)1024.f, (_Float16)1024.f});
-  return __builtin_bit_cast(h8, o);
+// Codes of a word's slots 2 x and 2 x + 1 as FP16 numbers (a subnormal S c would not
+// be exact), from numbers of which they are the last bits: 1024 + c, and 64 + c
+// where they stand 4 bits higher.
+template <int X>
+__device__ __forceinline__ h2 code_pair(uint32_t w, uint32_t magic, uint32_t magic16) {
+  if constexpr (X >= 2) w >>= 8;
+  if constexpr (X & 1)
+    return as_h2((w & 0x00F000F0u) | magic16) - h2{(_Float16)64.f, (_Float16)64.f};
+  return as_h2((w & 0x000F000Fu) | magic) - h2{(_Float16)1024.f, (_Float16)1024.f};
 }
 
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
   const int32_t* const list = SEL ? p.sel + ((int64_t)row0 * p.kv_heads + kvh) * p.n_sel : nullptr;
   const int64_t stride = (int64_t)p.kv_heads * (80 * D);
   const uint8_t* const base = p.data + (int64_t)kvh * (80 * D);
-  uint32_t magic = 0x64006400u;   // in a VGPR: the mask and it are then one instruction
-  asm("" : "+v"(magic));
+  uint32_t magic = 0x64006400u, magic16 = 0x54005400u;   // in VGPRs: a mask and one are then one instruction
+  asm("" : "+v"(magic), "+v"(magic16));
 
   for (int tile = tile0; tile * (16 * CT) < cols; tile += p.tiles) {
     // positions of the tile's columns, and this workgroup's pages: positions in
@@ -344,13 +344,13 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     }
 
     f4 O[CT][J], OZ[CT];
-    float m[CT], m_kept[CT];
+    float m[CT], m_kept[CT];      // the reference, now and at the last fold
+    float least[CT];        // the lowest that it may be
     float exact[CT];        // this lane's weights before their rounding, for lse
-    int vexp = 0;           // value scales since the last fold are below 2^(vexp + 1)
     bool kept = false;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      m[ct] = m_kept[ct] = -INFINITY;
+      m[ct] = m_kept[ct] = least[ct] = -INFINITY;
       exact[ct] = 0.f;
       OZ[ct] = f4{0, 0, 0, 0};
 #pragma unroll
@@ -360,7 +360,6 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     // cancel, and a matrix-core sum loses a little to every addition: over a long
     // cache what they have in common would swallow the result's last bits.
     auto fold = [&]() {
-      const float up = ldexpf(1.f, vexp);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         float* const s = s_merge + (wave * CT + ct) * kPart;
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
         float sum = __shfl(OZ[ct][0], 32 + l);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          f4 v = O[ct][j] * up + z[j >> 1];
+          f4 v = O[ct][j] + z[j >> 1];
           if (kept) v += s4[j * 64] * f;
           s4[j * 64] = v;
           O[ct][j] = f4{0, 0, 0, 0};
@@ -383,7 +382,6 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
         OZ[ct] = f4{0, 0, 0, 0};
         m_kept[ct] = m[ct];
       }
-      vexp = 0;
       kept = true;
     };
 
@@ -436,10 +434,11 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
       load_keys();           // past the last step: that step's again, not used
       __builtin_amdgcn_sched_barrier(0);
 
-      // base-2 logits above the running maximum, plus kWeightExp
+      // base-2 logits above the reference, plus kWeightExp
       constexpr int NY = 8 * NT;
       float y[CT][NY], top[CT];
       bool raise = false;
+      uint64_t lower = 0;     // bit l: column l's four lanes
       const bool edge = t0 + 32 * NT - 1 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
@@ -461,19 +460,22 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 #pragma unroll
         for (int i = 0; i < NY; ++i) top[ct] = fmaxf(top[ct], y[ct][i]);
         raise |= top[ct] > (none ? -INFINITY : kWeightExp + kRaise);
+        const uint64_t low = __ballot(top[ct] < kWeightExp - kLower && m[ct] > least[ct]);
+        lower |= low & low >> 16 & low >> 32 & low >> 48;
       }
-      if (__any(raise)) {
+      if (__any(raise) || (lower & 0xFFFFu) != 0) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           const bool none = m[ct] == -INFINITY;
           float most = fmaxf(top[ct], __shfl_xor(top[ct], 16));
           most = fmaxf(most, __shfl_xor(most, 32));
-          // the maximum in y's scale stands at kWeightExp
-          const float up = none ? (most == -INFINITY ? 0.f : most - kWeightExp)
-                                : fmaxf(most - kWeightExp, 0.f);
+          // the reference in y's scale stands at kWeightExp
+          float up = most == -INFINITY ? 0.f : most - kWeightExp;
+          if (!none && up < 0.f) up = up < -kLower ? fmaxf(up, least[ct] - m[ct]) : 0.f;
           const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
           if (!none) m[ct] += up;
           else if (most != -INFINITY) m[ct] = up;
+          least[ct] = fmaxf(least[ct], m[ct] - kBelow);
 #pragma unroll
           for (int i = 0; i < NY; ++i) y[ct][i] -= up;
 #pragma unroll
@@ -498,35 +500,6 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) vt[t].cut(written - t0 - 32 * t, lane);
       }
-      // value scales of 2 and more: lower the weights' power of two
-      uint32_t big = 0;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int x = 0; x < TS::M; ++x) big |= vt[t].scales[x];
-      if (__any((big & 0x40004000u) != 0)) {
-        uint32_t most = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int x = 0; x < TS::M; ++x)
-            most = max(most, max(vt[t].scales[x] >> 16, vt[t].scales[x] & 0xFFFFu));
-        int e = (int)(most >> 10) - 15;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) e = max(e, __shfl_xor(e, d));
-        e = __builtin_amdgcn_readfirstlane(e);
-        if (e > vexp) {
-          const float f = ldexpf(1.f, vexp - e);
-          vexp = e;
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int j = 0; j < J; ++j) O[ct][j] *= f;
-        }
-      }
-      const _Float16 d1 = (_Float16)ldexpf(1.f, -vexp), d16 = (_Float16)ldexpf(0.0625f, -vexp);
-      const h2 down = {d1, d1}, down16 = {d16, d16};
-
       const uint32_t fill = l == 8 ? 0x3C003C00u : 0u;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -534,7 +507,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
         u4v z = vt[t].offsets;
         if (l >= G) z = u4v{fill, fill, fill, fill};
         const h8 za = __builtin_bit_cast(h8, z);
-        h2 ws[CT][4], wr[CT][4];
+        h8 wh[CT], wl[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           u4v wv, rv;
@@ -542,38 +515,55 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
           for (int x = 0; x < 4; ++x) {
             const float y0 = y[ct][8 * t + 2 * x], y1 = y[ct][8 * t + 2 * x + 1];
             const h2 w = {(_Float16)y0, (_Float16)y1};
-            wv[x] = as_u32(w);
-            ws[ct][x] = w * (x & 1 ? down16 : down);
             const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
+            wv[x] = as_u32(w);
             rv[x] = as_u32(rest);
-            wr[ct][x] = rest * (x & 1 ? down16 : down);
           }
-          OZ[ct] = mfma(za, __builtin_bit_cast(h8, wv), OZ[ct]);
-          OZ[ct] = mfma(za, __builtin_bit_cast(h8, rv), OZ[ct]);
+          wh[ct] = __builtin_bit_cast(h8, wv);
+          wl[ct] = __builtin_bit_cast(h8, rv);
+          OZ[ct] = mfma(za, wh[ct], OZ[ct]);
+          OZ[ct] = mfma(za, wl[ct], OZ[ct]);
         }
-        unroll<G>([&](auto g) {
-          h2 s[4];
-          unroll<4>([&](auto x) { s[x] = TS::template scale2<g * 4 + x>(vt[t].scales); });
-          const h8 v0 = normal_operand(vt[t].codes[2 * g], magic);
-          const h8 v1 = normal_operand(vt[t].codes[2 * g + 1], magic);
+        // 15 S passes FP16's range from 4096 on: such scales enter as four quarters
+        uint32_t wide = 0, quarters[TS::M];
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            u4v hi, lo;
+        for (int x = 0; x < TS::M; ++x) wide |= (vt[t].scales[x] + 0x14001400u) & 0x80008000u;
+        int times = 1;
+        if (__any(wide != 0)) {
+          times = 4;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const h2 h = ws[ct][x] * s[x];
-              hi[x] = as_u32(h);
-              h2 rest = __builtin_elementwise_fma(ws[ct][x], s[x], -h);
-              rest = __builtin_elementwise_fma(wr[ct][x], s[x], rest);
-              lo[x] = as_u32(rest);
-            }
-            const h8 hb = __builtin_bit_cast(h8, hi), lb = __builtin_bit_cast(h8, lo);
-            O[ct][2 * g] = mfma(v0, hb, O[ct][2 * g]);
-            O[ct][2 * g + 1] = mfma(v1, hb, O[ct][2 * g + 1]);
-            O[ct][2 * g] = mfma(v0, lb, O[ct][2 * g]);
-            O[ct][2 * g + 1] = mfma(v1, lb, O[ct][2 * g + 1]);
+          for (int x = 0; x < TS::M; ++x) {
+            quarters[x] = ((vt[t].scales[x] + 0x14001400u) >> 15 & 0x00010001u) * 0xFFFFu;
+            vt[t].scales[x] -= quarters[x] & 0x08000800u;
           }
-        });
+        }
+        for (;;) {
+          unroll<G>([&](auto g) {
+            uint32_t (&codes)[TS::J] = vt[t].codes;
+            asm volatile("" : "+v"(codes[2 * g]), "+v"(codes[2 * g + 1]));   // unpacked here, not ahead of the loop
+            u4v hi[2], lo[2];
+            unroll<4>([&](auto x) {
+              const h2 s = TS::template scale2<g * 4 + x>(vt[t].scales);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const h2 c = code_pair<x>(codes[2 * g + i], magic, magic16), h = c * s;
+                hi[i][(int)x] = as_u32(h);
+                lo[i][(int)x] = as_u32(__builtin_elementwise_fma(c, s, -h));
+              }
+            });
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  O[ct][2 * g + i] = mfma(__builtin_bit_cast(h8, k == 1 ? lo[i] : hi[i]),
+                                          k == 2 ? wl[ct] : wh[ct], O[ct][2 * g + i]);
+          });
+          if (--times == 0) break;
+#pragma unroll
+          for (int x = 0; x < TS::M; ++x) vt[t].scales[x] &= quarters[x];
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
       load_values();

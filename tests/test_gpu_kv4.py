@@ -629,3 +629,73 @@ def test_attention_weights_keep_their_bits(D, dtype, lens):
     q = torch.randn(n, 16, D, generator=torch.Generator().manual_seed(4)).to(TYPES[dtype]).cuda()
     out = made.gpu().attention(q, ints(made.table), ints(made.lens), ints(np.arange(n + 1)), 1, max(lens), scale=0.02)
     check_held(out, made, q, np.arange(n + 1), 0.02, f"{D} {dtype} {lens}")
+
+
+class Tail(Made):
+    """Flat logits and values of one sign, behind one strong token of zero values in
+    each of the first `sinks` pages: the small weights make up the whole result."""
+
+    def __init__(self, n, D, nats, big=0.0, sinks=8, seed=7):
+        self.big = big
+        super().__init__([n], 1, D, seed=seed, spread=0.01, v_scale=0.02)
+        k, v = np.full((1, 1, D), 2.0, np.float16), np.zeros((1, 1, D), np.float16)
+        for p in range(sinks):
+            K4.append(self.data, self.summary, k, v, [64 * self.table[0, p] + 5 * p])
+        self.scale = nats / (2.0 * D)
+
+    def _append(self, k, v, slots):
+        v = v + np.float16(0.05)
+        if self.big:
+            v[..., :32] = v[..., :32].astype(np.float32) * (self.big / 0.05)
+        super()._append(k, v, slots)
+
+    def check(self, dtype, max_len, label):
+        D = self.data.shape[2] // 80
+        q = torch.ones(1, 2, D, dtype=dtype, device="cuda")
+        out = self.gpu().attention(q, ints(self.table), ints(self.lens), ints([0, 1]), 1, max_len, scale=self.scale)
+        # a weight loses at most 2^-25 of what stands for 2^8 or more at the sinks: 64
+        # tokens of their pages, values below 0.14 (or big's)
+        sinks = np.full(D, 64 * 2.0 ** -33 * 0.14)
+        sinks[:32] *= max(1.0, self.big / 0.05)
+        check_held(out, self, q, np.array([0, 1]), self.scale, label, sinks)
+
+
+@pytest.mark.parametrize("D,n", [(64, 20000), (128, 9000), (256, 5000)])
+@pytest.mark.parametrize("nats", [11, 13, 15, 17])
+def test_attention_keeps_small_weights(D, n, nats):
+    """The whole cache in one workgroup, and split as for its length."""
+    made = Tail(n, D, nats)
+    for dtype in TYPES.values():
+        for max_len in (1, n):
+            made.check(dtype, max_len, f"{D} {n} {nats} {dtype} {max_len}")
+
+
+@pytest.mark.parametrize("D,n", [(64, 6000), (256, 3000)])
+@pytest.mark.parametrize("nats,big", [(0, 2.0), (0, 20000.0), (12, 600.0), (12, 9000.0)])
+def test_attention_large_group_beside_small_ones(D, n, nats, big):
+    made = Tail(n, D, nats, big=big)
+    for dtype in TYPES.values():
+        for max_len in (1, n):
+            made.check(dtype, max_len, f"{D} {n} {nats} {big} {dtype} {max_len}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("step", [-4.0, -0.5, 0.5, 4.0])
+def test_attention_logits_that_fall_or_rise_with_every_page(D, step):
+    """The weights' reference follows the pages down and up, by up to 160 nats; every
+    eighth token has values over the whole of FP16's range."""
+    n, H = 64 * 40 - 9, 1
+    made = Made([n], H, D, seed=3, spread=0.0, v_scale=1.0)
+    rng = np.random.default_rng(1)
+    k = np.repeat(step * np.arange(n)[:, None] // 64, D, 1)[:, None].astype(np.float16)
+    v = rng.standard_normal((n, H, D)).astype(np.float16)
+    v[::8] = np.sign(v[::8]) * np.float16(65504)
+    K4.append(made.data, made.summary, k, v, made.table[0, np.arange(n) // 64] * 64 + np.arange(n) % 64)
+    cache = made.gpu()
+    for dtype in TYPES.values():
+        q = torch.ones(1, 2, D, dtype=dtype, device="cuda")
+        for max_len in (1, n):
+            lse = torch.empty(1, 2, device="cuda")
+            out = cache.attention(q, ints(made.table), ints(made.lens), ints([0, 1]), 1, max_len, scale=1 / D, lse=lse)
+            check_attention(out, lse, made, q, np.array([0, 1]), 1 / D, label=f"{D} {step} {dtype} {max_len}")
+            check_held(out, made, q, np.array([0, 1]), 1 / D, f"{D} {step} {dtype} {max_len}")
