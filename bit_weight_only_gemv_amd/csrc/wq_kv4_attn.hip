@@ -682,6 +682,8 @@ join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t*
 }
 
 // How a call is split: column tiles of a sequence (or row) and splits of its pages.
+// Hints past what the call can have count as that, so that nothing overflows; there
+// is at least one row and one sequence.
 struct AttnPlan {
   int64_t pairs, tiles, splits, split_pages;
   int waves, ct;            // waves a workgroup, column tiles a wave
@@ -690,6 +692,8 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
                           int64_t max_len, int64_t n_sel, bool sel) {
   AttnPlan p{};
   const int64_t R = a->n_heads / c->n_kv_heads;
+  if (max_rows > a->n_rows) max_rows = a->n_rows;
+  if (max_len > 64 * a->table_width) max_len = 64 * a->table_width;
   const int64_t cols = (sel || max_rows < 1 ? 1 : max_rows) * R;
   // Two column tiles share the codes' unpacking where there are enough of them: a
   // 512-token piece of two prompts over 6000 tokens takes 218 us with two, 265 with
@@ -698,7 +702,6 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
   p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
   p.pairs = (sel ? a->n_rows : a->n_seqs) * c->n_kv_heads;
   int64_t pages = sel ? n_sel : (max_len + 63) / 64;
-  if (!sel && pages > a->table_width) pages = a->table_width;
   if (pages < 1) pages = 1;
   // Two workgroups of 4 waves for every compute unit, as many as run at once:
   // a second round costs more than uneven lengths do (32 sequences of up to 8191
@@ -741,6 +744,7 @@ extern "C" int64_t wq_kv4_attention_workspace(const wq_kv4_cache* cache, const w
   if (int e = check_attention(cache, rows, max_rows, max_len, n_sel, "wq_kv4_attention_workspace"))
     return e;
   wq::ok();
+  if (rows->n_rows == 0 || rows->n_seqs == 0) return 0;
   const AttnPlan p = attn_plan(cache, rows, max_rows, max_len, n_sel, n_sel > 0);
   if (p.splits == 1) return 0;
   return (rows->n_rows * rows->n_heads * p.splits * (cache->head_dim + 4) * 4 + 15) / 16 * 16;
@@ -753,9 +757,10 @@ extern "C" int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* ro
   const char* who = "wq_kv4_attention";
   if (int e = check_attention(cache, rows, max_rows, max_len, n_sel, who)) return e;
   if (window < 0) return wq::fail(WQ_ERR_INVALID_ARG, "%s: window must be at least 0", who);
-  if ((sel != nullptr) != (n_sel > 0))
+  const bool empty = rows->n_rows == 0 || rows->n_seqs == 0;   // its sel may be NULL
+  if (sel != nullptr ? n_sel == 0 : n_sel > 0 && !empty)
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: sel and n_sel go together", who);
-  if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
+  if (empty) return wq::ok();
   const int64_t need = wq_kv4_attention_workspace(cache, rows, max_rows, max_len, n_sel);
   if (!out || (need && !workspace)) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (workspace_bytes < need)

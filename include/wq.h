@@ -483,7 +483,8 @@ int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t n_
  * sums are held in float32; a softmax weight enters its product with the values in
  * 22 bits; out is rounded once.
  * max_rows and max_len are the largest n_b and lens the caller expects: they
- * choose how the work is split, and results hold for others as well.
+ * choose how the work is split, and results hold for others as well (hints past
+ * n_rows and 64 table_width count as these).
  * workspace: wq_kv4_attention_workspace bytes for the same arguments, 16-byte
  * aligned (NULL where that is 0).  out must not overlap q. */
 int64_t wq_kv4_attention_workspace(const wq_kv4_cache* cache, const wq_kv4_rows* rows,

@@ -699,3 +699,19 @@ def test_attention_logits_that_fall_or_rise_with_every_page(D, step):
             out = cache.attention(q, ints(made.table), ints(made.lens), ints([0, 1]), 1, max_len, scale=1 / D, lse=lse)
             check_attention(out, lse, made, q, np.array([0, 1]), 1 / D, label=f"{D} {step} {dtype} {max_len}")
             check_held(out, made, q, np.array([0, 1]), 1 / D, f"{D} {step} {dtype} {max_len}")
+
+
+# ---------------------------------------------------------- empty batches
+
+
+@pytest.mark.parametrize("n_seqs", [0, 3])
+def test_batches_without_rows(n_seqs):
+    """Attention, selection and sparse attention of no rows return empty outputs."""
+    made = Made([5, 70, 0], 2, 64)
+    cache = made.gpu()
+    q = torch.empty(0, 4, 64, dtype=torch.float16, device="cuda")
+    args = (ints(made.table[:n_seqs]), ints(made.lens[:n_seqs]), ints(np.zeros(n_seqs + 1)))
+    assert cache.attention(q, *args, 0, 70).shape == q.shape
+    sel = cache.select(q, *args, 4)
+    assert sel.shape == (0, 2, 4)
+    assert cache.attention(q, *args, 1 << 60, 1 << 60, sel=sel).shape == q.shape

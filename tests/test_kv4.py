@@ -191,3 +191,27 @@ def test_wrapper_checks():
         B.KV4Cache(torch.zeros(2, 2, 80 * 64, dtype=torch.uint8))     # not on the GPU
     with pytest.raises(ValueError):
         B.KV4Cache(torch.zeros(2, 2, 80 * 64, dtype=torch.uint8), torch.zeros(2, 2, 2, 32, dtype=torch.float16))
+
+
+def space(c=None, a=None, max_rows=1, max_len=64, n_sel=0):
+    c, a = c or cache(), a or rows()
+    return L.load().wq_kv4_attention_workspace(ref(c), ref(a), max_rows, max_len, n_sel)
+
+
+@pytest.mark.parametrize("n_rows,n_seqs,n_sel", [(0, 0, 0), (0, 2, 0), (0, 2, 4), (2, 0, 0), (2, 0, 4)])
+def test_empty_batches_need_no_workspace(n_rows, n_seqs, n_sel):
+    assert space(a=rows(n_rows=n_rows, n_seqs=n_seqs), n_sel=n_sel) == 0
+
+
+def test_an_empty_batch_may_have_an_empty_list():
+    assert attend(a=rows(n_rows=0), sel=None, n_sel=4) == 0
+    assert attend(sel=None, n_sel=4) == attend(sel=P, n_sel=0) == L.WQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("n_heads", [8, 32, 64])
+@pytest.mark.parametrize("big", [1 << 31, 1 << 58, 1 << 62, (1 << 63) - 1])
+def test_hints_beyond_the_call_count_as_its_size(n_heads, big):
+    """Rows and lengths that the call cannot have: n_rows and 64 table_width of them."""
+    a = rows(n_rows=50, n_heads=n_heads, table_width=900)
+    assert space(a=a, max_rows=big, max_len=big) == space(a=a, max_rows=50, max_len=64 * 900) > 0
+    assert space(a=a, max_rows=1, max_len=big) == space(a=a, max_rows=1, max_len=64 * 900) > 0
