@@ -41,15 +41,33 @@ def _strided(t, what):
 
 
 def _new(shape, dtype, device, stream):
-    """A tensor of the current stream that a call on `stream` uses: its memory
-    is not handed out again before that call's work is done."""
+    """A tensor that a call on `stream` writes and the current stream's work uses.
+    It is memory of `stream`, not of the current one, whose last user there may not
+    be done; and it is not handed out again before the current stream's work that
+    is queued when it is dropped."""
     import torch
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.numel():
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        t.record_stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    t = _of_stream(shape, dtype, device, stream)
+    if t.numel():
+        t.record_stream(torch.cuda.current_stream(device))
     return t
+
+
+def _workspace(nbytes, device, stream):
+    """Memory that only a call on `stream` uses."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _of_stream(nbytes, torch.uint8, device, stream)
+
+
+def _of_stream(shape, dtype, device, stream):
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class KV4Cache:
@@ -114,7 +132,7 @@ class KV4Cache:
         if need < 0:
             L._check(need)
         if workspace is None:
-            workspace = _new(need, torch.uint8, q.device, stream)
+            workspace = _workspace(need, q.device, stream)
         L._check(lib.wq_kv4_select(self._ref, ctypes.addressof(a), n_sel, L._i32(sel, shape, "sel"),
                                    L._dptr(workspace), workspace.numel(), L._stream(stream)))
         return sel
@@ -142,7 +160,7 @@ class KV4Cache:
         if need < 0:
             L._check(need)
         if workspace is None and need:
-            workspace = _new(need, torch.uint8, q.device, stream)
+            workspace = _workspace(need, q.device, stream)
         L._check(lib.wq_kv4_attention(
             self._ref, ar, max_rows, max_len, scale, window,
             None if sel is None else L._i32(sel, (a.n_rows, self.n_kv_heads, n_sel), "sel"), n_sel,

@@ -715,3 +715,34 @@ def test_batches_without_rows(n_seqs):
     sel = cache.select(q, *args, 4)
     assert sel.shape == (0, 2, 4)
     assert cache.attention(q, *args, 1 << 60, 1 << 60, sel=sel).shape == q.shape
+
+
+# ---------------------------------------------------- memory and streams
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_on_another_stream_are_not_memory_in_use(handle):
+    """The current stream still works on memory that it has given back: a call on
+    another stream takes none of it for its output, its choice and its workspace."""
+    made = Made([3000], 2, 64, seed=3)
+    cache = made.gpu()
+    q = torch.randn(1, 4, 64, generator=torch.Generator().manual_seed(0)).half().cuda()
+    args = (ints(made.table), ints(made.lens), ints([0, 1]))
+    want, chosen = cache.attention(q, *args, 1, 3000), cache.select(q, *args, 5)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    for _ in range(4):
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(20_000_000)
+        used = [torch.full((n,), 3.0, device="cuda") for n in (16, 64, 1024, 4096, 65536)]
+        held = [(t.data_ptr(), 4 * t.numel()) for t in used]
+        sums = [t.sum() for t in used]
+        del used
+        out = cache.attention(q, *args, 1, 3000, stream=stream)
+        sel = cache.select(q, *args, 5, stream=stream)
+        for t in (out, sel):
+            assert all(t.data_ptr() >= p + n or t.data_ptr() + t.numel() * t.element_size() <= p for p, n in held)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, want) and torch.equal(sel, chosen)
+        assert [float(s) for s in sums] == [48.0, 192.0, 3072.0, 12288.0, 196608.0]

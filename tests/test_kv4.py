@@ -215,3 +215,52 @@ def test_hints_beyond_the_call_count_as_its_size(n_heads, big):
     a = rows(n_rows=50, n_heads=n_heads, table_width=900)
     assert space(a=a, max_rows=big, max_len=big) == space(a=a, max_rows=50, max_len=64 * 900) > 0
     assert space(a=a, max_rows=1, max_len=big) == space(a=a, max_rows=1, max_len=64 * 900) > 0
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_made_for_a_stream_comes_from_that_stream(monkeypatch, handle):
+    """A block that the current stream has just given back may still be in use there,
+    and a call on another stream does not wait for it: what such a call writes has
+    to be memory of its own stream.  What it returns is also held for the current
+    one, where the caller uses and drops it; its workspace is not."""
+    import contextlib
+
+    torch = pytest.importorskip("torch")
+    from bit_weight_only_gemv_amd import kv4
+
+    class Stream:
+        def __init__(self, handle=7, device=None):
+            self.cuda_stream = handle
+
+    current, made = Stream(1), []
+    now = [current]
+
+    @contextlib.contextmanager
+    def use(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    class Tensor:
+        def __init__(self, *a, **kw):
+            self.of, self.held = now[-1].cuda_stream, []
+            made.append(self)
+
+        def numel(self):
+            return 4
+
+        def record_stream(self, s):
+            self.held.append(s.cuda_stream)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now[-1])
+    monkeypatch.setattr(torch, "empty", Tensor)
+    t = kv4._new((4,), torch.uint8, "cuda", 9 if handle else Stream(9))
+    assert t.of == 9 and t.held == [1]
+    t = kv4._new((4,), torch.uint8, "cuda", None)
+    assert t.of == 1 and t.held == []
+    t = kv4._workspace(4, "cuda", 9 if handle else Stream(9))
+    assert t.of == 9 and t.held == []
+    assert now == [current] and len(made) == 3
