@@ -463,6 +463,8 @@ def wq_kv4_plan(lens, cu_rows, block_table, free_pages, new_lens, slots, runs, t
     fn = load().wq_kv4_plan
     B, width = block_table.shape
     T, F, n_runs = slots.numel(), free_pages.numel(), runs.shape[0]
+    if T and not B:
+        raise ValueError(f"{T} rows of no sequences")
     _check(fn(
         _i32(lens, (B,), "lens"), _i32(cu_rows, (B + 1,), "cu_rows"), B, T,
         _i32(block_table, (B, width), "block_table"), width, _i32(free_pages, (F,), "free_pages"),

@@ -585,14 +585,14 @@ extern "C" int wq_kv4_plan(const int32_t* lens, const int32_t* cu_rows, int64_t 
   if (n_seqs < 0 || n_rows < 0 || n_rows > (1 << 24) || table_width < 1 ||
       table_width > (1 << 24) || n_free < 0 || n_free > kMaxPage + 1)
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
-  if (n_seqs == 0) return wq::ok();
+  if (n_seqs == 0 && n_rows > 0) return wq::ok();
   const int64_t want = wq_kv4_max_runs(n_seqs, n_rows);
   if (n_runs < want)
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: runs holds %lld, %lld needed", who, (long long)n_runs,
                     (long long)want);
   if (n_runs > (1 << 25)) return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
-  if (!lens || !cu_rows || !block_table || !new_lens || !taken || (n_rows && !slots) ||
-      (n_runs && !runs) || (n_free && !free_pages))
+  if ((n_seqs && (!lens || !cu_rows || !block_table || !new_lens)) || !taken ||
+      (n_rows && !slots) || (n_runs && !runs) || (n_free && !free_pages))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned4(lens) || !aligned4(cu_rows) || !aligned4(block_table) || !aligned4(new_lens) ||
       !aligned4(taken) || !aligned4(slots) || ((uintptr_t)runs & 7u) || !aligned4(free_pages))
@@ -602,8 +602,8 @@ extern "C" int wq_kv4_plan(const int32_t* lens, const int32_t* cu_rows, int64_t 
     return wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
   int64_t most = n_rows > n_runs ? n_rows : n_runs;
   if (n_seqs > most) most = n_seqs;
-  int64_t wgs = (most + kPlanThreads - 1) / kPlanThreads;
-  if (wgs > 256) wgs = 256;
+  int64_t wgs = (most + kPlanThreads - 1) / kPlanThreads;   // one at least, for `taken`
+  wgs = wgs > 256 ? 256 : wgs < 1 ? 1 : wgs;
   plan_kernel<<<dim3((unsigned)wgs), kPlanThreads, lds, (hipStream_t)stream>>>(
       lens, cu_rows, (int)n_seqs, (int)n_rows, block_table, table_width, free_pages, (int)n_free,
       new_lens, slots, runs, (int)n_runs, taken);

@@ -114,6 +114,8 @@ class KV4Cache:
         T, H, D = q.shape
         if D != self.head_dim:
             raise ValueError(f"q has {D} channels, the cache {self.head_dim}")
+        if T and not B:
+            raise ValueError(f"{T} rows of no sequences")
         p, r, h = _strided(q, "q")
         return L.Kv4Rows(L._i32(block_table, (B, width), "block_table"), L._i32(lens, (B,), "lens"),
                          L._i32(cu_rows, (B + 1,), "cu_rows"), width, B, T, H, _dtype(q), p, r, h)

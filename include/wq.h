@@ -443,7 +443,10 @@ int64_t wq_kv4_max_runs(int64_t n_seqs, int64_t n_rows);
  *   runs[j]      {first row, count}: the rows that share a page, in row order,
  *                n_runs = wq_kv4_max_runs(...) of them; unused ones are {-1, 0}
  *   taken[0]     pages needed; more than n_free means that some were missing
- * lens is only read, so a call may be repeated. */
+ * lens is only read, so a call may be repeated.  A table too narrow shows in new_lens
+ * (more than 64 table_width) and in the slots.  Without sequences there are no
+ * rows: taken and the runs are written, and a call that names rows all the same
+ * does nothing, here and below. */
 int wq_kv4_plan(const int32_t* lens, const int32_t* cu_rows, int64_t n_seqs, int64_t n_rows,
                 int32_t* block_table, int64_t table_width, const int32_t* free_pages,
                 int64_t n_free, int32_t* new_lens, int32_t* slots, int32_t* runs, int64_t n_runs,

@@ -746,3 +746,13 @@ def test_outputs_on_another_stream_are_not_memory_in_use(handle):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(out, want) and torch.equal(sel, chosen)
         assert [float(s) for s in sums] == [48.0, 192.0, 3072.0, 12288.0, 196608.0]
+
+
+@pytest.mark.parametrize("n_runs", [0, 5, 3000])
+def test_plan_of_no_sequences(n_runs):
+    """Fixed buffers of a step that has no sequences left: the last step's pages and
+    runs are not taken again."""
+    none, runs, taken = ints(np.zeros(0)), ints(np.full((n_runs, 2), 7)), ints([7])
+    for cu in (none[:0].new_zeros(1), ints([0])):
+        B.wq_kv4_plan(none, cu, ints(np.zeros((0, 4))), ints([3, 4]), none, none, runs, taken)
+        assert int(taken) == 0 and (runs == ints([-1, 0])).all()

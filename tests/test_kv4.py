@@ -264,3 +264,24 @@ def test_memory_made_for_a_stream_comes_from_that_stream(monkeypatch, handle):
     t = kv4._workspace(4, "cuda", 9 if handle else Stream(9))
     assert t.of == 9 and t.held == []
     assert now == [current] and len(made) == 3
+
+
+def test_wrappers_refuse_rows_of_no_sequences():
+    torch = pytest.importorskip("torch")
+    i32 = dict(dtype=torch.int32)
+    none, cu, table = torch.zeros(0, **i32), torch.zeros(1, **i32), torch.zeros(0, 4, **i32)
+    with pytest.raises(ValueError, match="no sequences"):
+        B.wq_kv4_plan(none, cu, table, none, none, torch.zeros(3, **i32), torch.zeros(3, 2, **i32), cu)
+    c = object.__new__(B.KV4Cache)
+    c.n_kv_heads, c.head_dim = 2, 64
+    q = torch.zeros(3, 4, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="no sequences"):
+        c.select(q, table, none, cu, 4)
+    with pytest.raises(ValueError, match="no sequences"):
+        c.attention(q, table, none, cu, 1, 64)
+
+
+def test_plan_of_no_sequences_needs_no_tables_but_taken():
+    none = dict(B_=0, T=0, lens=None, cu=None, table=None, new=None, slots=None, free=None, n_free=0)
+    assert plan(**none, taken=None) == L.WQ_ERR_INVALID_ARG
+    assert plan(**none, n_runs=4, runs=None) == L.WQ_ERR_INVALID_ARG
