@@ -31,6 +31,12 @@ __device__ __forceinline__ int upper_index(const int* sums, int n, int x) {
   return lo;
 }
 
+// New tokens of a sequence, 0 .. T for any cu_rows: the difference of two int32 need
+// not be one, and of a signed one that overflows the compiler assumes that it does not.
+__device__ __forceinline__ int new_tokens(int from, int to, int T) {
+  return to > from ? (int)min((uint32_t)to - (uint32_t)from, (uint32_t)T) : 0;
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ cu, int B, int T,
             int32_t* __restrict__ table, int64_t width, const int32_t* __restrict__ free_pages,
@@ -41,55 +47,60 @@ plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ cu, in
   int* s_cu = s_len + B;               // [B + 1]
   int* s_need = s_cu + B + 1;          // [B + 1] exclusive sums of pages needed
   int* s_runs = s_need + B + 1;        // [B + 1] exclusive sums of runs
-  __shared__ int s_wave[2][kPlanThreads / kWave];
+  __shared__ uint32_t s_wave[2][kPlanThreads / kWave];
   const int tid = threadIdx.x;
   const int per = (B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  int need = 0, nruns = 0;
+  uint32_t need = 0, nruns = 0;        // sums of bad cu_rows may wrap, so unsigned
   for (int b = b0; b < b1; ++b) {
     const int len = min(max(lens[b], 0), kMaxLen);
-    const int c = cu[b], n = min(max(cu[b + 1] - c, 0), T);
+    const int c = cu[b], n = new_tokens(c, cu[b + 1], T);
     s_len[b] = len;
     s_cu[b] = c;
     if (b == B - 1) s_cu[B] = cu[B];
-    s_need[b] = need;
-    s_runs[b] = nruns;
+    s_need[b] = (int)need;
+    s_runs[b] = (int)nruns;
     need += (len + n + 63) / 64 - (len + 63) / 64;
     nruns += n > 0 ? (len + n - 1) / 64 - len / 64 + 1 : 0;
   }
-  int ni = need, ri = nruns;           // inclusive sums over the wave's lanes
+  uint32_t ni = need, ri = nruns;      // inclusive sums over the wave's lanes
   for (int d = 1; d < kWave; d <<= 1) {
-    const int a = __shfl_up(ni, d), b = __shfl_up(ri, d);
+    const uint32_t a = __shfl_up(ni, d), b = __shfl_up(ri, d);
     if ((tid & 63) >= d) { ni += a; ri += b; }
   }
   if ((tid & 63) == 63) { s_wave[0][tid >> 6] = ni; s_wave[1][tid >> 6] = ri; }
   __syncthreads();
-  int nbase = ni - need, rbase = ri - nruns;
+  uint32_t nbase = ni - need, rbase = ri - nruns;
   for (int w = 0; w < tid >> 6; ++w) { nbase += s_wave[0][w]; rbase += s_wave[1][w]; }
-  for (int b = b0; b < b1; ++b) { s_need[b] += nbase; s_runs[b] += rbase; }
-  if (tid == kPlanThreads - 1) { s_need[B] = nbase + need; s_runs[B] = rbase + nruns; }
+  for (int b = b0; b < b1; ++b) {
+    s_need[b] = (int)((uint32_t)s_need[b] + nbase);
+    s_runs[b] = (int)((uint32_t)s_runs[b] + rbase);
+  }
+  if (tid == kPlanThreads - 1) { s_need[B] = (int)(nbase + need); s_runs[B] = (int)(rbase + nruns); }
   __syncthreads();
   const int total = s_need[B], total_runs = s_runs[B];
   const int g0 = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
 
   if (g0 == 0) taken[0] = total;
-  for (int b = g0; b < B; b += step) new_lens[b] = s_len[b] + max(s_cu[b + 1] - s_cu[b], 0);
-  for (int i = g0; i < total; i += step) {
+  for (int b = g0; b < B; b += step) new_lens[b] = s_len[b] + new_tokens(s_cu[b], s_cu[b + 1], T);
+  for (int i = g0; i < min(total, T / 64 + B); i += step) {    // rising cu_rows need no more
     const int b = upper_index(s_need, B, i);
-    const int p = (s_len[b] + 63) / 64 + i - s_need[b];
+    const uint32_t p = (uint32_t)((s_len[b] + 63) / 64) + ((uint32_t)i - (uint32_t)s_need[b]);
     if (p < width) table[b * width + p] = i < n_free ? free_pages[i] : -1;
   }
   for (int row = g0; row < T; row += step) {
     int slot = -1;
     const int b = upper_index(s_cu, B, row);
-    const int off = row - s_cu[b];
-    if (off >= 0 && off < s_cu[b + 1] - s_cu[b]) {
-      const int pos = s_len[b] + off, p = pos / 64;
+    // any cu_rows: no position past kMaxLen + T, no page outside the list
+    const uint32_t off = (uint32_t)row - (uint32_t)s_cu[b];
+    if (row >= s_cu[b] && row < s_cu[b + 1] && off < (uint32_t)T) {
+      const int pos = s_len[b] + (int)off, p = pos / 64;
       const int fresh = p - (s_len[b] + 63) / 64;   // pages this call adds start at 0
+      const uint32_t at = (uint32_t)s_need[b] + (uint32_t)fresh;
       int page = -1;
       if (p < width) {
         if (fresh < 0) page = table[b * width + p];
-        else if (s_need[b] + fresh < n_free) page = free_pages[s_need[b] + fresh];
+        else if (at < (uint32_t)n_free) page = free_pages[at];
       }
       if (page >= 0 && page <= kMaxPage) slot = page * 64 + (pos & 63);
     }
@@ -99,11 +110,11 @@ plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ cu, in
     int first = -1, count = 0;
     if (j < total_runs) {
       const int b = upper_index(s_runs, B, j);
-      const int len = s_len[b], end = len + s_cu[b + 1] - s_cu[b];
-      const int page = len / 64 + j - s_runs[b];
-      const int lo = max(page * 64, len), hi = min(page * 64 + 64, end);
-      first = s_cu[b] + lo - len;
-      count = hi - lo;
+      const int len = s_len[b], end = len + new_tokens(s_cu[b], s_cu[b + 1], T);
+      const int64_t start = 64 * (int64_t)(len / 64 + ((int64_t)j - s_runs[b]));
+      const int lo = (int)max(start, (int64_t)len), hi = (int)min(start + 64, (int64_t)end);
+      first = (int)((uint32_t)s_cu[b] + (uint32_t)lo - (uint32_t)len);
+      count = (int)((uint32_t)hi - (uint32_t)lo);
     }
     reinterpret_cast<int2*>(runs)[j] = make_int2(first, count);
   }

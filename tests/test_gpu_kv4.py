@@ -756,3 +756,24 @@ def test_plan_of_no_sequences(n_runs):
     for cu in (none[:0].new_zeros(1), ints([0])):
         B.wq_kv4_plan(none, cu, ints(np.zeros((0, 4))), ints([3, 4]), none, none, runs, taken)
         assert int(taken) == 0 and (runs == ints([-1, 0])).all()
+
+
+def test_plan_stays_in_bounds_for_any_rows():
+    """cu_rows that fall, repeat and lie far outside the rows, over the longest
+    lengths: every slot is of a page that the call was given, or none."""
+    far = -(1 << 31)
+    for cu, lens in (([far, 100, 200], [1 << 30, 5]), ([-(1 << 30) - 7, 100, 200], [1 << 30, 5]),
+                     ([0, (1 << 31) - 1, 200], [70, 1 << 30]), ([5, far, (1 << 31) - 1], [70, 70])):
+        slots, runs, taken = ints(np.zeros(300)), ints(np.zeros((8, 2))), ints([0])
+        B.wq_kv4_plan(ints(lens), ints(cu), ints(np.full((2, 3), 50)), ints([60, 61]), ints([0, 0]), slots, runs, taken)
+        assert set(np.unique(host(slots) // 64)) <= {-1, 50, 60, 61}, cu
+
+
+def test_plan_stays_in_bounds_where_the_pages_overflow():
+    """8192 sequences that claim all of 2^24 rows each: their pages pass 2^31."""
+    n, T = 8192, 1 << 24
+    cu = (np.arange(n + 1, dtype=np.int64) * T + (1 << 31)) % (1 << 32) - (1 << 31)
+    slots, runs = ints(np.zeros(T)), ints(np.zeros((B.wq_kv4_max_runs(n, T), 2)))
+    B.wq_kv4_plan(ints(np.ones(n)), ints(cu), ints(np.full((n, 2), 50)), ints([60, 61]), ints(np.zeros(n)), slots, runs,
+                  ints([0]))
+    assert set(torch.unique(slots.div(64, rounding_mode="floor")).tolist()) <= {-1, 50, 60, 61}
