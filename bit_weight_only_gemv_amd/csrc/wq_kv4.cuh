@@ -51,20 +51,21 @@ __device__ __forceinline__ uint16_t from_float(float f) {   // round to nearest 
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-// The sequence of a row and the row's position in it (-1: it sees no token).
+// The sequence of a row and the row's position in it (-1: it sees no token).  No
+// difference overflows for any lens and cu_rows.
 struct SeqRow {
   int b, pos;
 };
 __device__ __forceinline__ SeqRow find_row(const KvRows& a, int row) {
   int lo = 0, hi = a.seqs;
   if (row < hi && a.cu[row] == row && a.cu[row + 1] == row + 1)   // one row each: no search
-    return {row, max(a.lens[row] - 1, -1)};
+    return {row, max(a.lens[row], 0) - 1};
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
     if (a.cu[m] <= row) lo = m; else hi = m;
   }
   const int end = a.cu[lo + 1];
-  return {lo, row < end ? max(a.lens[lo] - (end - row), -1) : -1};
+  return {lo, row < end ? max(max(a.lens[lo], 0) - (end - row), -1) : -1};
 }
 
 // Index arrays (int32) need their own alignment only: a caller's free list or

@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
     b = of;
     if (guess_at < a.width) guess = a.table[(int64_t)b * a.width + guess_at];
     row0 = max(a.cu[b], 0);
-    n = min(a.cu[b + 1], a.rows) - row0;
-    len = a.lens[b];
+    n = max(min(max(a.cu[b + 1], 0), a.rows) - row0, 0);     // rows of the call for any cu_rows
+    len = max(a.lens[b], 0);
   }
   const int cols = n * R;
   const int written = SEL ? a.lens[b] : len;      // tokens that the cache holds

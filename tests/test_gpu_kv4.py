@@ -777,3 +777,29 @@ def test_plan_stays_in_bounds_where_the_pages_overflow():
     B.wq_kv4_plan(ints(np.ones(n)), ints(cu), ints(np.full((n, 2), 50)), ints([60, 61]), ints(np.zeros(n)), slots, runs,
                   ints([0]))
     assert set(torch.unique(slots.div(64, rounding_mode="floor")).tolist()) <= {-1, 50, 60, 61}
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_stays_in_bounds_for_any_rows(D):
+    """cu_rows and lengths at the ends of int32: nothing outside the given rows is
+    written, and sequences that are in order keep their results."""
+    made = Made([100, 50, 200], 2, D, seed=2)
+    cache = made.gpu()
+    q = torch.randn(70, 4, D, generator=torch.Generator().manual_seed(3)).half().cuda()
+    low, high = -(1 << 31), (1 << 31) - 1
+    room = torch.empty(90, 4, D, dtype=torch.float16, device="cuda")
+    table = ints(made.table)
+    for max_rows in (1, 70):
+        want = cache.attention(q, table, ints(made.lens), ints([0, 6, 6, 70]), max_rows, 200)
+        for cu in ([0, 6, low, 70], [0, 6, high, low], [low, 6, low, high], [high, high, low, low], [0, 6, 70, low]):
+            for lens in ([100, 50, 200], [100, low, high]):
+                room.fill_(5.0)
+                cache.attention(q, table, ints(lens), ints(cu), max_rows, 200, out=room[10:80])
+                assert (room[:10] == 5).all() and (room[80:] == 5).all(), (cu, lens)
+                if cu[:2] == [0, 6] and cu[2] >= 70:            # no sequence shares rows 0 .. 5
+                    assert torch.equal(room[10:16], want[:6]), (cu, lens)
+                sel = cache.select(q, table, ints(lens), ints(cu), 2)
+                assert int(sel.min()) >= -1 and int(sel.max()) < made.table.shape[1]
+                room.fill_(5.0)
+                cache.attention(q, table, ints(lens), ints(cu), max_rows, 200, sel=sel, out=room[10:80])
+                assert (room[:10] == 5).all() and (room[80:] == 5).all(), (cu, lens)
