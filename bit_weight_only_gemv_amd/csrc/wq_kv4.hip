@@ -337,6 +337,7 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 constexpr int kScoreWaves = 4;
 constexpr int kScoreHeads = 8;       // heads of one pass
 constexpr int kScoreTurns = 8;       // most turns of a wave
+constexpr float kMostScore = 0x1.fffffep127f;
 
 __device__ __forceinline__ double lane_add(double v, int d) { return v + __shfl_xor(v, d); }
 
@@ -423,7 +424,9 @@ score_kernel(KvRows a, Divisor by, const uint16_t* __restrict__ summary, int64_t
         best = fmax(best, v);
       }
       if (lane % L == 0 && p < p_end) {
-        float f = p == 0 || p == pages - 1 ? INFINITY : (ids[t] >= 0 ? (float)best : -INFINITY);
+        // infinite for the two that are always taken, and for no other
+        float f = p == 0 || p == pages - 1 ? INFINITY
+                                           : (ids[t] >= 0 ? fminf((float)best, kMostScore) : -INFINITY);
         if (h0 > 0) f = fmaxf(f, out[p]);
         out[p] = f;
       }

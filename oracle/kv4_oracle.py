@@ -147,6 +147,11 @@ def rows_of(lens, cu):
 
 def select(summary, q, table, lens, cu, n_sel):
     """int64 [rows, H, n_sel]."""
+    with np.errstate(over="ignore"):      # huge queries
+        return _select(summary, q, table, lens, cu, n_sel)
+
+
+def _select(summary, q, table, lens, cu, n_sel):
     n_pages, H = summary.shape[:2]
     T, heads, D = q.shape
     q = np.asarray(q, np.float64)
@@ -161,9 +166,8 @@ def select(summary, q, table, lens, cu, n_sel):
                 if 0 <= page < n_pages:
                     s = summary[page, h].astype(np.float64)
                     score[p] = np.maximum(x * s[0], x * s[1]).sum(-1).max()
-            if m:
-                score[0] = score[m - 1] = np.inf
-            pick = np.sort(np.lexsort((np.arange(m), -score))[:n_sel])
+            always = np.isin(np.arange(m), (0, m - 1))
+            pick = np.sort(np.lexsort((np.arange(m), -score, ~always))[:n_sel])
             sel[row, h, :len(pick)] = pick
     return sel
 

@@ -803,3 +803,20 @@ def test_attention_stays_in_bounds_for_any_rows(D):
                 room.fill_(5.0)
                 cache.attention(q, table, ints(lens), ints(cu), max_rows, 200, sel=sel, out=room[10:80])
                 assert (room[:10] == 5).all() and (room[80:] == 5).all(), (cu, lens)
+
+
+# ------------------------------------------------- bounds of any query
+
+
+def choose(made, q, n_sel, label):
+    cu = [0, len(q)]
+    sel = made.gpu().select(q, ints(made.table), ints(made.lens), ints(cu), n_sel)
+    assert np.array_equal(host(sel), K4.select(made.summary, f32(q), made.table, made.lens, cu, n_sel)), label
+
+
+def test_select_keeps_the_last_page_beside_bounds_past_float32():
+    made = Made([64 * 30 + 1], 1, 128, seed=4, spread=3.0)
+    for size in (1e37, 3e38):
+        q = (size * torch.sign(torch.randn(2, 4, 128, generator=torch.Generator().manual_seed(5)))).to(torch.bfloat16)
+        for n in (2, 5, 20):
+            choose(made, q.cuda(), n, f"{size} {n}")
