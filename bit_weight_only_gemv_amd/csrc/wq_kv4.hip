@@ -330,7 +330,8 @@ append_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 // min) with q' = q / 2.  FP16 values and their products are
 // far inside 64 bits, so those sums are exact but for operands that lie 2^20
 // apart, and the choice does not depend on their order: two fused multiply-adds
-// a channel and head, at the rate of 32-bit ones.  A wave takes 512 / D pages at
+// a channel and head, at the rate of 32-bit ones.  They are finite unless the head's
+// query is not (0 times infinity included), and such a head takes no part.  A wave takes 512 / D pages at
 // a time, 8 channels a lane, up to 8 heads' queries in registers.  16 sequences of
 // up to 65001 tokens, 64 heads over 8 (43 MB of summaries, 8 us as a read): 25 us,
 // half of it the multiply-adds, the rest conversions and sums across lanes.
@@ -421,7 +422,7 @@ score_kernel(KvRows a, Divisor by, const uint16_t* __restrict__ summary, int64_t
         v = row_add<0x141>(v);                // row_half_mirror
         if constexpr (L >= 16) v = row_add<0x140>(v);   // row_mirror
         if constexpr (L == 32) v = lane_add(v, 16);
-        best = fmax(best, v);
+        best = fmax(best, __builtin_fma(v, 0.0, v));   // NaN unless finite, and then passed over
       }
       if (lane % L == 0 && p < p_end) {
         // infinite for the two that are always taken, and for no other

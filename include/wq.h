@@ -469,7 +469,8 @@ int wq_kv4_append(const wq_kv4_cache* cache, int dtype, const uint16_t* k, int64
  *   max over the group's heads h of  sum_d max(q[h][d] min[d], q[h][d] max[d])
  * (an upper bound of the page's logits), the first and the last page always.
  * Sums are made in 64 bits and rounded once to float32; ties go to the lower
- * page, NaN counts as lowest.  sel int32 [n_rows][n_kv_heads][n_sel]: page
+ * page.  A head whose query holds an infinity or NaN takes no part; without one
+ * that does, all pages tie.  sel int32 [n_rows][n_kv_heads][n_sel]: page
  * positions in the block table, rising, -1 where there are fewer.
  * workspace: wq_kv4_select_workspace bytes, 16-byte aligned. */
 int64_t wq_kv4_select_workspace(int64_t n_rows, int64_t n_kv_heads, int64_t table_width);

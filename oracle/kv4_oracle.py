@@ -147,7 +147,7 @@ def rows_of(lens, cu):
 
 def select(summary, q, table, lens, cu, n_sel):
     """int64 [rows, H, n_sel]."""
-    with np.errstate(over="ignore"):      # huge queries
+    with np.errstate(invalid="ignore", over="ignore"):      # infinite and huge queries
         return _select(summary, q, table, lens, cu, n_sel)
 
 
@@ -160,12 +160,14 @@ def _select(summary, q, table, lens, cu, n_sel):
         m = min(max(pos // PAGE + 1, 0), table.shape[1]) if pos >= 0 else 0
         for h in range(H):
             x = q[row, h * (heads // H):(h + 1) * (heads // H)]
+            takes_part = np.isfinite(x).all(-1)
             score = np.full(m, -np.inf, np.float32)
             for p in range(m):
                 page = table[b, p]
                 if 0 <= page < n_pages:
                     s = summary[page, h].astype(np.float64)
-                    score[p] = np.maximum(x * s[0], x * s[1]).sum(-1).max()
+                    s = np.maximum(x * s[0], x * s[1]).sum(-1)[takes_part]
+                    score[p] = np.where(np.isnan(s), -np.inf, s).max(initial=-np.inf)
             always = np.isin(np.arange(m), (0, m - 1))
             pick = np.sort(np.lexsort((np.arange(m), -score, ~always))[:n_sel])
             sel[row, h, :len(pick)] = pick

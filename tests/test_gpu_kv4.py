@@ -820,3 +820,22 @@ def test_select_keeps_the_last_page_beside_bounds_past_float32():
         q = (size * torch.sign(torch.randn(2, 4, 128, generator=torch.Generator().manual_seed(5)))).to(torch.bfloat16)
         for n in (2, 5, 20):
             choose(made, q.cuda(), n, f"{size} {n}")
+
+
+@pytest.mark.parametrize("heads", [2, 6, 20])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_select_with_queries_that_are_not_finite(dtype, heads):
+    """A head whose query holds an infinity or NaN does not decide for its group,
+    also where a channel's minimum and maximum are equal, 0 or of two signs."""
+    made = Made([64 * 40 + 9], 2, 64, seed=4)
+    made.summary[made.table[0, 3], :, :, 5] = 0
+    made.summary[made.table[0, 4], :, 0, 5] = made.summary[made.table[0, 4], :, 1, 5]
+    q = torch.randn(2, heads, 64, generator=torch.Generator().manual_seed(5)).to(TYPES[dtype])
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        one, two, whole = q.clone(), q.clone(), q.clone()
+        one[1, heads // 2, 5] = bad
+        two[0, 0, 5], two[0, heads - 1, 60] = bad, -bad
+        whole[0, :, 7] = bad
+        for n in (2, 7):
+            for x in (one, two, whole):
+                choose(made, x.cuda(), n, f"{dtype} {heads} {bad} {n}")
