@@ -147,6 +147,9 @@ class KV4Cache:
         [rows, n_heads] receives the logarithm of the softmax sums."""
         import torch
         lib = L.load()
+        n_sel = 0 if sel is None else sel.shape[-1]
+        if sel is not None and n_sel == 0:      # its NULL pointer would mean all tokens
+            raise ValueError("sel has no places")
         a = self._rows(q, block_table, lens, cu_rows)
         if out is None:
             out = _new(q.shape, q.dtype, q.device, stream)
@@ -154,7 +157,6 @@ class KV4Cache:
             raise ValueError("out must have q's shape and type")
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
             raise ValueError("lse must be float32 [rows, n_heads]")
-        n_sel = 0 if sel is None else sel.shape[-1]
         if scale is None:
             scale = self.head_dim ** -0.5
         ar = ctypes.addressof(a)

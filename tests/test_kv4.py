@@ -285,3 +285,15 @@ def test_plan_of_no_sequences_needs_no_tables_but_taken():
     none = dict(B_=0, T=0, lens=None, cu=None, table=None, new=None, slots=None, free=None, n_free=0)
     assert plan(**none, taken=None) == L.WQ_ERR_INVALID_ARG
     assert plan(**none, n_runs=4, runs=None) == L.WQ_ERR_INVALID_ARG
+
+
+def test_attention_refuses_a_list_without_places():
+    """Its pointer is NULL, which would mean all tokens."""
+    torch = pytest.importorskip("torch")
+    i32 = dict(dtype=torch.int32)
+    c = object.__new__(B.KV4Cache)
+    c.n_kv_heads, c.head_dim = 2, 64
+    q = torch.zeros(1, 4, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="sel"):
+        c.attention(q, torch.zeros(1, 4, **i32), torch.zeros(1, **i32), torch.zeros(2, **i32), 1, 64,
+                    sel=torch.zeros(1, 2, 0, **i32))
