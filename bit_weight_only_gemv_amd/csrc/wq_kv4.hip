@@ -660,6 +660,8 @@ extern "C" int64_t wq_kv4_select_workspace(int64_t n_rows, int64_t n_kv_heads,
   if (n_rows < 0 || n_rows > (1 << 24) || n_kv_heads < 1 || n_kv_heads > 65535 ||
       table_width < 1 || table_width > (1 << 24))
     return wq::fail(WQ_ERR_INVALID_ARG, "wq_kv4_select_workspace: bad sizes");
+  if (n_rows * n_kv_heads > 0x7FFFFFFFll)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "wq_kv4_select_workspace: too many rows");
   wq::ok();
   return (n_rows * n_kv_heads * table_width * 4 + 15) / 16 * 16;
 }
@@ -675,6 +677,8 @@ extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
   if (n_sel < 2 || n_sel > (1 << 20))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: n_sel must be at least 2 (the first and last page)", who);
   if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
+  if (rows->n_rows * cache->n_kv_heads > 0x7FFFFFFFll)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
   const int64_t need = wq_kv4_select_workspace(rows->n_rows, cache->n_kv_heads, rows->table_width);
   if (!sel || !workspace) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (workspace_bytes < need)
@@ -682,8 +686,6 @@ extern "C" int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
                     (long long)workspace_bytes, (long long)need);
   if (!aligned4(sel) || !aligned16(workspace))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
-  if (rows->n_rows * cache->n_kv_heads > 0x7FFFFFFFll)
-    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
   const KvRows a = kv4_rows(rows);
   const Divisor by(cache->n_kv_heads);
   float* scores = static_cast<float*>(workspace);

@@ -297,3 +297,10 @@ def test_attention_refuses_a_list_without_places():
     with pytest.raises(ValueError, match="sel"):
         c.attention(q, torch.zeros(1, 4, **i32), torch.zeros(1, **i32), torch.zeros(2, **i32), 1, 64,
                     sel=torch.zeros(1, 2, 0, **i32))
+
+
+@pytest.mark.parametrize("n_rows,heads,width", [(1 << 24, 65535, 1 << 24), (1 << 24, 128, 1)])
+def test_select_workspace_refuses_what_select_does(n_rows, heads, width):
+    """Sizes whose bytes would wrap, or that the call itself does not take."""
+    assert L.load().wq_kv4_select_workspace(n_rows, heads, width) == L.WQ_ERR_UNSUPPORTED
+    assert L.load().wq_last_error()
