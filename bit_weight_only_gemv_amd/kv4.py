@@ -37,7 +37,8 @@ def _strided(t, what):
     r, h, c = t.stride()
     if c != 1 and t.numel():
         raise ValueError(f"{what}: channels must be consecutive")
-    return t.data_ptr(), r, h
+    rows, heads, _ = t.shape
+    return t.data_ptr(), r if rows > 1 else 0, h if heads > 1 else 0    # of one, it is never used
 
 
 def _new(shape, dtype, device, stream):

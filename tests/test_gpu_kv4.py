@@ -839,3 +839,22 @@ def test_select_with_queries_that_are_not_finite(dtype, heads):
         for n in (2, 7):
             for x in (one, two, whole):
                 choose(made, x.cuda(), n, f"{dtype} {heads} {bad} {n}")
+
+
+def test_strides_of_single_rows_and_heads_do_not_count():
+    """One row of a buffer whose rows are no multiple of 8 long, one head likewise."""
+    D = 64
+    made = Made([70], 1, D, seed=6)
+    cache = made.gpu()
+    wide = torch.randn(1, 5 * D + 3, generator=torch.Generator().manual_seed(3)).half().cuda()
+    q = wide[:, :4 * D].view(1, 4, D)
+    out = cache.attention(q, ints(made.table), ints(made.lens), ints([0, 1]), 1, 70)
+    check_attention(out, None, made, q, np.array([0, 1]), D ** -0.5, label="one row")
+    sel = cache.select(q, ints(made.table), ints(made.lens), ints([0, 1]), 2)
+    assert np.array_equal(host(sel), K4.select(made.summary, f32(q), made.table, made.lens, [0, 1], 2))
+    k = torch.randn(2, 80, D, generator=torch.Generator().manual_seed(4)).half().cuda()
+    k, v = (x.as_strided((80, 1, D), (D, 3, 1)) for x in k)
+    slots = np.arange(80)[:50] + 64 * made.table[0, 0]
+    cache.append(k[:50], v[:50], ints(slots), ints([[0, 50]]))
+    K4.append(made.data, made.summary, f32(k[:50]), f32(v[:50]), slots)
+    assert np.array_equal(made.d.cpu().numpy(), made.data)
