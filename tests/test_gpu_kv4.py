@@ -858,3 +858,65 @@ def test_strides_of_single_rows_and_heads_do_not_count():
     cache.append(k[:50], v[:50], ints(slots), ints([[0, 50]]))
     K4.append(made.data, made.summary, f32(k[:50]), f32(v[:50]), slots)
     assert np.array_equal(made.d.cpu().numpy(), made.data)
+
+
+# ------------------------------------------- splits, turns and long tables
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [63, 300, 1000, 4000])
+def test_attention_window_over_several_splits(D, window):
+    """Windows that begin inside a late page of a long cache, whole call and one workgroup."""
+    made = Made([5000, 1700], 1, D, seed=13)
+    cache = made.gpu()
+    for dtype in TYPES.values():
+        for rows in ([1, 1], [3, 40]):
+            for max_len in (1, 5000, 1 << 20):
+                attend(made, cache, rows, 2, dtype, window=window, max_len=max_len,
+                       label=f"{D} window {window} {rows} {max_len}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 900])
+def test_attention_two_column_tiles_over_several_splits(D, window):
+    """Rows enough for two column tiles a wave, over splits, and over so many pages a
+    wave that it folds its sums on the way."""
+    made = Made([2611, 700], 1, D, seed=14, v_scale=2.0)
+    cache = made.gpu()
+    for dtype in TYPES.values():
+        for max_len in (1, 2611):
+            attend(made, cache, [40, 33], 2, dtype, window=window, max_len=max_len,
+                   label=f"{D} two tiles {window} {max_len}")
+
+
+class Pages:
+    """Summaries of many pages alone, for selection."""
+
+    def __init__(self, lens, H, D, seed=0):
+        rng = np.random.default_rng(seed)
+        self.lens = np.asarray(lens)
+        need = -(-self.lens // 64)
+        self.table = np.full((len(lens), int(need.max()) + 3), -1)
+        order = rng.permutation(int(need.sum()) + 2)
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[need[:b].sum():][:n]
+        centre = rng.standard_normal((len(order), H, D))
+        half = np.abs(rng.standard_normal((len(order), H, D)))
+        self.summary = np.stack([centre - half, centre + half], 2).astype(np.float16)
+        self.cache = B.KV4Cache(torch.zeros(len(order), H, 80 * D, dtype=torch.uint8, device="cuda"),
+                                torch.from_numpy(self.summary).cuda())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,rows,heads,n_sel", [([64 * 1100 - 5, 64 * 500], [12, 8], 2, 33), ([64 * 600], [16], 24, 9),
+                                                   ([64 * 9001, 70], [1, 1], 2, 40)])
+def test_select_over_many_pages(D, dtype, lens, rows, heads, n_sel):
+    """Several turns of a wave, more than 8 heads a group, and a table whose keys do
+    not fit the workgroup's memory."""
+    H = 1 if len(lens) == 2 and lens[1] == 70 else 2
+    made = Pages(lens, H, D, seed=D + heads)
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    q = torch.randn(int(cu[-1]), heads, D, generator=torch.Generator().manual_seed(2)).to(TYPES[dtype]).cuda()
+    sel = made.cache.select(q, ints(made.table), ints(made.lens), ints(cu), n_sel)
+    assert np.array_equal(host(sel), K4.select(made.summary, f32(q), made.table, made.lens, cu, n_sel))
