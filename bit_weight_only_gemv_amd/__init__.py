@@ -4,9 +4,10 @@ FP16 outlier columns, behind the C ABI of ``include/wq.h``.
 
 ``_lib`` is the ctypes binding of ``libwq.so`` (same names as the C ABI);
 ``layer`` packs a float32 weight matrix with the library's host encoder and
-moves the packed arrays to the GPU; ``kv4`` is the paged 4-bit key/value cache.  Nothing here computes on the CPU except
-the library's own host encoder, and nothing falls back to another
-implementation: calls fail if ``libwq.so`` has not been built.
+moves the packed arrays to the GPU; ``kv4`` is the paged 4-bit key/value
+cache.  Nothing here computes on the CPU except the library's own host encoder,
+and nothing falls back to another implementation: calls fail if ``libwq.so`` has
+not been built.
 """
 
 from ._lib import (  # noqa: F401

@@ -127,7 +127,8 @@ plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ cu, in
 // Values go through LDS as bytes, 4 channels of 8 tokens to a thread, and come
 // out as 4 words by a byte transpose.  Vector instructions bound it: 23300 tokens of
 // 8 heads of 128 channels (126 MB) take 30 us, 22 as a plain read and write of
-// these bytes; the arithmetic is some 10 instructions a value.  One token: 3.8 us.
+// these bytes; a lane issues 20 instructions a value, which at four cycles each take
+// 24 us, and LDS bank conflicts are below 1 us.  One token: 3.8 us.
 constexpr int kAppendThreads = 256;
 
 // Codes as floats of 8 channels, in the header's arithmetic.  (w - Z) / S is

@@ -9,17 +9,19 @@
 //   out_d = sum_t p_t (S_{t,g(d)} c_{t,d}) + sum_t p_t Z_{t,g(d)}.
 // Both are 16x16x32 products.  The first one's A operand is the codes: one mask per
 // two codes makes FP16 subnormals c 2^-24 (or 16 c 2^-24; B carries the 1/16).  The
-// second one's is S c.  Tokens are the rows of the first product, so a lane ends with 4 tokens
-// of one column per 16, and two such tiles are just its 8 k of the second
+// second one's is S c.  Tokens are the rows of the first product, so a lane ends with
+// 4 tokens of one column per 16, and two such tiles are just its 8 k of the second
 // product's B operand: the weights never leave their registers.
 //
-// Precision.  Queries are scaled by a power of two to [2^14, 2^15) and so are
-// exact in FP16 (BF16 ones too); logits, maxima and sums are FP32.  A softmax
-// weight is an FP16 number and its FP16 remainder (22 bits), for BF16 outputs too:
-// rounded to 11 bits it shows where values of both signs nearly cancel.  S c is an
-// FP16 number and its remainder, which is exact.  Scales stay off the weights: a
-// small weight times a small scale would fall below FP16, and its token would count
-// as its group's minimum.  For the same reason the weights are relative to a
+// Precision.  Queries are scaled by a power of two, the largest channel to [2^14,
+// 2^15), and so are exact in FP16, of either type, down to 2^-24 of the largest;
+// smaller ones are off by 2^-35 of it at most.  Logits, maxima and sums are FP32.
+// A softmax weight is an FP16 number and its FP16 remainder (22 bits), for BF16
+// outputs too: rounded to 11 bits it shows where values of both signs nearly cancel.
+// S c is an FP16 number and its remainder, which is exact; the product of the two
+// remainders, 2^-22 of the whole, is left out.  Scales stay off the weights: a small
+// weight times a small scale would fall below FP16, and its token would count as its
+// group's minimum.  For the same reason the weights are relative to a
 // reference that follows the logits both ways: a page whose largest weight would
 // pass 2^14 or stay below 2^2 sets it to that logit, where weights carry 2^10.  So
 // 22 bits hold for what counts in a page, however small the page's share is
@@ -27,15 +29,16 @@
 // maximum and the rescale of the sums.  The reference stays within 2^64 of the
 // highest, so that FP32 holds the sums.
 //
-// What bounds it.  One token a sequence over a long cache: the cache's bytes.
-// Four sequences of 131072 tokens, 8 heads of 128 channels, 671 MB: 131 us, where
-// a plain read of as many bytes takes 119; a page costs a wave 734 vector and 56
-// matrix instructions, 60% of the time at two waves a SIMD, and a page's loads are
+// What bounds it (traced times).  One token a sequence over a long cache: the
+// cache's bytes and the instructions nearly alike.  Four sequences of 131072 tokens,
+// 8 heads of 128 channels, 671 MB: 137 us, where a plain read of as many bytes takes
+// 119; a page costs a wave 775 vector and 72 matrix instructions, which issue in 60%
+// and keep the matrix cores for 22% of the time at two waves a SIMD, and its loads are
 // under way while the one before is computed (keys are loaded into the registers
 // that the logits have just freed, values into those of the values' product).
-// Many rows: the vector instructions, 217 us for 54 GFLOP of a 512-token piece of
-// two prompts over 6000 tokens.  Short caches: latency, 8 us for one page a wave
-// (lengths and page numbers, then the page, the dependent steps of its
+// Many rows: the vector instructions (1197 a page and wave with two column tiles, 422
+// of them for each tile alone), 251 us for 54 GFLOP of a 512-token piece of two
+// prompts over 6000 tokens.  Short caches: latency, 8 us for one page a wave (lengths and page numbers, then the page, the dependent steps of its
 // computation, the join).
 
 #include "wq_common.cuh"
@@ -47,7 +50,7 @@
 namespace wqd {
 
 constexpr int kAttnWaves = 4, kAttnMoreWaves = 8;
-constexpr int kFoldPages = 8;        // 5% of the time at 2, and no closer
+constexpr int kFoldPages = 8;        // at 2 the long case takes 158 us instead of 137, and is no closer
 constexpr float kWeightExp = 10.f;   // a page's largest weight at the reference is 2^10;
 constexpr float kRaise = 4.f;        // one of over 2^14 raises the reference,
 constexpr float kLower = 8.f;        // one of less than 2^2 lowers it,
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) attn_kernel(AttnArgs p) {
 
   for (int tile = tile0; tile * (16 * CT) < cols; tile += p.tiles) {
     // positions of the tile's columns, and this workgroup's pages: positions in
-    // the block table, or in the row's list; a wave takes every fourth
+    // the block table, or in the row's list; a wave takes every NW-th
     const int c_hi = min(tile * (16 * CT) + 16 * CT - 1, cols - 1);
     const int pos_lo = SEL ? len - 1 : len - n + p.group_by.div(tile * (16 * CT));
     const int pos_hi = SEL ? len - 1 : len - n + p.group_by.div(c_hi);
@@ -696,7 +699,7 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
   if (max_len > 64 * a->table_width) max_len = 64 * a->table_width;
   const int64_t cols = (sel || max_rows < 1 ? 1 : max_rows) * R;
   // Two column tiles share the codes' unpacking where there are enough of them: a
-  // 512-token piece of two prompts over 6000 tokens takes 218 us with two, 265 with
+  // 512-token piece of two prompts over 6000 tokens takes 251 us with two, 298 with
   // one.  Heads of 256 channels would not fit their registers.
   p.ct = !sel && c->head_dim <= 128 && cols >= 64 ? 2 : 1;
   p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
@@ -705,17 +708,17 @@ static AttnPlan attn_plan(const wq_kv4_cache* c, const wq_kv4_rows* a, int64_t m
   if (pages < 1) pages = 1;
   // Two workgroups of 4 waves for every compute unit, as many as run at once:
   // a second round costs more than uneven lengths do (32 sequences of up to 8191
-  // tokens: 56 us, in two rounds 61).  A split has at least two pages a wave, one
-  // while that leaves compute units idle (64 chosen pages: 8.7 us, 10.1 with two).
+  // tokens: 67 us, in two rounds 72).  A split has at least two pages a wave, one
+  // while that leaves compute units idle (64 chosen pages: 8.6 us, 11.8 with two).
   const int64_t items = p.pairs * p.tiles;
   int64_t splits = (512 + items - 1) / items;
   const int64_t waves = items * ((pages + kAttnWaves - 1) / kAttnWaves) <= 256 ? kAttnWaves : 2 * kAttnWaves;
   const int64_t most = (pages + waves - 1) / waves;
   if (splits > most) splits = most;
   // Few pages for few workgroups: one workgroup of up to 8 waves, and no second
-  // launch.  500 tokens of one sequence: 9.5 us with 8 waves, 10.3 with 4, 8.4 and
-  // 2.8 in two launches; 1000 tokens: 12.2, 14.5, 8.4 and 2.7; 2000 tokens: 8.5 and
-  // 2.9 in two.
+  // launch.  500 tokens of one sequence: 9.9 us with 8 waves, 11.0 with 4, 8.6 and
+  // 2.7 in two launches; 1000 tokens: 13.2, 14.8, 8.4 and 2.6, where the second launch's
+  // own 2 to 3 us make up for it; 2000 tokens: 8.7 and 2.9 in two.
   p.waves = kAttnWaves;
   if (items <= 256 && pages <= 2 * kAttnMoreWaves) {
     splits = 1;

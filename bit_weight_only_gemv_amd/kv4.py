@@ -7,7 +7,9 @@ it (include/wq.h, "4-bit key/value cache").  A decode step is
 
 or, for long sequences, with ``sel = cache.select(q, block_table, new_lens,
 cu_rows, n_sel)`` passed to ``attention``.  Everything but the sizes is device
-data, so a captured graph of the step serves other lengths too.
+data, so a captured graph of the step serves other lengths too; it is fastest near
+the max_len that it was captured with.  A call with ``stream`` runs there: what it
+reads has to be ready on that stream, and its result is to be awaited there.
 """
 
 from __future__ import annotations
@@ -37,8 +39,10 @@ def _strided(t, what):
     r, h, c = t.stride()
     if c != 1 and t.numel():
         raise ValueError(f"{what}: channels must be consecutive")
-    rows, heads, _ = t.shape
-    return t.data_ptr(), r if rows > 1 else 0, h if heads > 1 else 0    # of one, it is never used
+    if (r | h) & 7:                     # the stride of a single row or head is never used
+        rows, heads, _ = t.shape
+        r, h = r if rows > 1 else 0, h if heads > 1 else 0
+    return t.data_ptr(), r, h
 
 
 def _new(shape, dtype, device, stream):

@@ -467,7 +467,7 @@ int wq_kv4_append(const wq_kv4_cache* cache, int dtype, const uint16_t* k, int64
 /* Pages for sparse attention.  For each row and key/value head, of the pages
  * that hold tokens up to the row's position, the n_sel of highest
  *   max over the group's heads h of  sum_d max(q[h][d] min[d], q[h][d] max[d])
- * (an upper bound of the page's logits), the first and the last page always.
+ * (an upper bound of the page's logits, the published query-aware choice of pages), the first and the last page always.
  * Sums are made in 64 bits and rounded once to float32; ties go to the lower
  * page.  A head whose query holds an infinity or NaN takes no part; without one
  * that does, all pages tie.  sel int32 [n_rows][n_kv_heads][n_sel]: page
@@ -488,7 +488,8 @@ int wq_kv4_select(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t n_
  * 22 bits; out is rounded once.
  * max_rows and max_len are the largest n_b and lens the caller expects: they
  * choose how the work is split, and results hold for others as well (hints past
- * n_rows and 64 table_width count as these).
+ * n_rows and 64 table_width count as these).  A max_len far above the lengths, or a
+ * window far below it, leaves compute units idle.
  * workspace: wq_kv4_attention_workspace bytes for the same arguments, 16-byte
  * aligned (NULL where that is 0).  out must not overlap q. */
 int64_t wq_kv4_attention_workspace(const wq_kv4_cache* cache, const wq_kv4_rows* rows,
