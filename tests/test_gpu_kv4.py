@@ -735,7 +735,7 @@ def test_outputs_on_another_stream_are_not_memory_in_use(handle):
     for _ in range(4):
         side.wait_stream(torch.cuda.current_stream())
         torch.cuda._sleep(20_000_000)
-        used = [torch.full((n,), 3.0, device="cuda") for n in (16, 64, 1024, 4096, 65536)]
+        used = [torch.full((n,), 2.0, device="cuda") for n in (16, 64, 1024, 4096, 65536)]
         held = [(t.data_ptr(), 4 * t.numel()) for t in used]
         sums = [t.sum() for t in used]
         del used
@@ -745,7 +745,7 @@ def test_outputs_on_another_stream_are_not_memory_in_use(handle):
             assert all(t.data_ptr() >= p + n or t.data_ptr() + t.numel() * t.element_size() <= p for p, n in held)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(out, want) and torch.equal(sel, chosen)
-        assert [float(s) for s in sums] == [48.0, 192.0, 3072.0, 12288.0, 196608.0]
+        assert [float(s) for s in sums] == [32.0, 128.0, 2048.0, 8192.0, 131072.0]
 
 
 @pytest.mark.parametrize("n_runs", [0, 5, 3000])
