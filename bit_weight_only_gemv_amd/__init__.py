@@ -5,7 +5,9 @@ FP16 outlier columns, behind the C ABI of ``include/wq.h``.
 ``_lib`` is the ctypes binding of ``libwq.so`` (same names as the C ABI);
 ``layer`` packs a float32 weight matrix with the library's host encoder and
 moves the packed arrays to the GPU; ``kv4`` is the paged 4-bit key/value
-cache.  Nothing here computes on the CPU except the library's own host encoder,
+cache, ``kv8`` the 8-bit one with the eviction of tokens by their attention
+weights, and ``rope`` the norm and rotation of queries and keys before them.
+Nothing here computes on the CPU except the library's own host encoder,
 and nothing falls back to another implementation: calls fail if ``libwq.so`` has
 not been built.
 """
@@ -23,3 +25,5 @@ from ._lib import (  # noqa: F401
     wq_read_probe, wq_read_probe_sink_words, wq_read_probe_geom, wq_copy_probe,
 )
 from .kv4 import KV4Cache  # noqa: F401
+from .kv8 import KV8Cache  # noqa: F401
+from .rope import wq_qk_norm_rope  # noqa: F401

@@ -89,6 +89,15 @@ SIGNATURES = {
     "wq_kv4_attention_workspace": (_I64, [_P, _P, _I64, _I64, _I64]),
     "wq_kv4_attention": (_INT, [_P, _P, _I64, _I64, ctypes.c_float, _I64, _P, _I64, _P, _P, _P,
                                 _I64, _P]),
+    "wq_kv8_append": (_INT, [_P, _INT, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    "wq_kv8_attention_workspace": (_I64, [_P, _P, _I64, _I64]),
+    "wq_kv8_attention": (_INT, [_P, _P, _I64, _I64, ctypes.c_float, _I64, _P, _P, _P, _I64, _P]),
+    "wq_kv8_accumulate_workspace": (_I64, [_P, _P, _I64, _I64]),
+    "wq_kv8_accumulate": (_INT, [_P, _P, _I64, _I64, _P, ctypes.c_float, _I64, _P, _P, _I64, _P,
+                                 _I64, _P]),
+    "wq_kv8_evict": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P,
+                            _I64, _P, _P, _P]),
+    "wq_qk_norm_rope": (_INT, [_INT, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _I64, _INT, _P]),
     "wq_read_probe": (_INT, [_P, _I64, _P, _P]),
     "wq_read_probe_sink_words": (_I64, [_I64]),
     "wq_read_probe_geom": (_INT, [_P, _I64, _P, _INT, _INT, _INT, _P]),
@@ -134,6 +143,18 @@ class Kv4Rows(ctypes.Structure):
     _fields_ = [("block_table", _P), ("lens", _P), ("cu_rows", _P), ("table_width", _I64),
                 ("n_seqs", _I64), ("n_rows", _I64), ("n_heads", _I64), ("dtype", ctypes.c_int32),
                 ("q", _P), ("q_row_stride", _I64), ("q_head_stride", _I64)]
+
+
+class Kv8Cache(ctypes.Structure):
+    """wq_kv8_cache."""
+    _fields_ = [("data", _P), ("exponents", _P), ("n_pages", _I64), ("n_kv_heads", _I64),
+                ("head_dim", _I64)]
+
+
+class Heads(ctypes.Structure):
+    """wq_heads."""
+    _fields_ = [("x", _P), ("out", _P), ("weight", _P), ("n_heads", _I64), ("row_stride", _I64),
+                ("head_stride", _I64), ("out_row_stride", _I64), ("out_head_stride", _I64)]
 
 
 class WQError(RuntimeError):

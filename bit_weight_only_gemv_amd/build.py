@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libwq.so")
 ARCH = "gfx950"
 HOST_SOURCES = ["wq_host.cpp"]
 HIP_SOURCES = ["wq_gemv.hip", "wq_mma.hip", "wq_gemm.hip", "wq_misc.hip", "wq_refine.hip",
-               "wq_kv4.hip", "wq_kv4_attn.hip"]
+               "wq_kv4.hip", "wq_kv4_attn.hip", "wq_kv8.hip", "wq_kv8_attn.hip", "wq_rope.hip"]
 
 
 def _hipcc() -> str:

@@ -1,0 +1,651 @@
+// Attention over the paged 8-bit key/value cache and the softmax weights that its
+// tokens get (wq.h, "8-bit key/value cache"), on the matrix cores.
+//
+// A workgroup takes 16 columns, (row, head) pairs of one key/value head, and its
+// waves pages of 64 tokens in turn.  With a block's exponents e (keys) and f (values),
+//   logit = scale 2^e (code . Q),   out_d = sum_t (p_t 2^f) code_{t,d},
+// both 16x16x32 products of FP16 operands.  A code is an FP16 number (one byte
+// permute makes 1024 + 128 + q of two, one packed subtraction q), so its products
+// are exact; the powers of two go into the exponential's argument.  Tokens are the
+// rows of the first product, so a lane ends with 4 tokens of one column per block,
+// and two blocks are just its 8 k of the second product's B operand: the weights
+// never leave their registers.
+//
+// Precision.  Queries are scaled by a power of two, the largest channel to [2^14,
+// 2^15), and so are exact in FP16, of either type, down to 2^-24 of the largest;
+// smaller ones are off by 2^-35 of it at most.  Logits, maxima and sums are FP32.
+// A weight p 2^f is an FP16 number and its FP16 remainder (22 bits): rounded to 11
+// bits it shows where values of both signs nearly cancel.  Weights are relative to a
+// reference that follows logit + f both ways: a page whose largest weight would
+// pass 2^14 or stay below 2^2 sets it to that, where weights carry 2^10.  So 22
+// bits hold for what counts in a page, however small the page's share is, and most
+// pages are spared the cross-lane maximum and the rescale of the sums.  The
+// reference stays within 2^64 of the highest and f within [-24, 10], so that FP32
+// holds the sums.
+
+#include "wq_attn.cuh"
+#include "wq_common.cuh"
+#include "wq_device.h"
+#include "wq_kv4.cuh"
+#include "wq_kv8.cuh"
+
+namespace wqd {
+
+// 8 codes (bytes q + 128) as a matrix-core operand.
+__device__ __forceinline__ h8 codes8(uint32_t w0, uint32_t w1) {
+  const h2 bias = {(_Float16)1152.f, (_Float16)1152.f};
+  const uint32_t magic = 0x64646464u;
+  const h2 a = as_h2(__builtin_amdgcn_perm(magic, w0, 0x04010400u)) - bias;
+  const h2 b = as_h2(__builtin_amdgcn_perm(magic, w0, 0x04030402u)) - bias;
+  const h2 c = as_h2(__builtin_amdgcn_perm(magic, w1, 0x04010400u)) - bias;
+  const h2 d = as_h2(__builtin_amdgcn_perm(magic, w1, 0x04030402u)) - bias;
+  return __builtin_bit_cast(h8, u4v{as_u32(a), as_u32(b), as_u32(c), as_u32(d)});
+}
+
+// A column's query: raw as loaded (8 channels 32 g + 8 r of group g), then scaled, and
+// its factor: logits to base 2 are factor 2^e (code . Q).
+template <int G>
+struct Query {
+  u4v raw[G];
+  h8 q[G];
+  float factor;
+  __device__ __forceinline__ void load(const uint16_t* __restrict__ src, bool on) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      raw[g] = on ? *reinterpret_cast<const u4v*>(src + 32 * g) : u4v{0, 0, 0, 0};
+  }
+  template <int DT>
+  __device__ __forceinline__ void scale(float by) {
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = fmaxf(top, fabsf(to_float<DT>((uint16_t)(raw[g][i >> 1] >> (16 * (i & 1))))));
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+    e = top == 0.f || e > 127 ? 14 : max(e, -100);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[g][i] = (_Float16)ldexpf(to_float<DT>((uint16_t)(raw[g][i >> 1] >> (16 * (i & 1)))), 14 - e);
+    factor = ldexpf(by * 1.44269504f, e - 14);
+  }
+};
+
+// A page's keys of one head: block u, channels 64 c + 32 (0, 1) + 8 r of token l.
+template <int D>
+struct Keys8 {
+  static constexpr int C = D / 64;
+  u4v codes[4][C];
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ page, uint32_t lane) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        codes[u][c] = *reinterpret_cast<const u4v*>(page + u * (16 * D) + c * 1024 + lane * 16);
+  }
+};
+
+struct Attn8Args {
+  KvRows a;
+  const uint8_t* data;
+  const uint32_t* exps;   // [page][head][2]
+  int64_t n_pages;
+  Divisor kv_heads_by, group_by, pairs_by, splits_by;
+  int kv_heads, window, tiles, splits, split_pages;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* part;            // [row][head][split][D], then [row][head][split][4]: sum, reference, sum
+};
+
+template <int DT, int D, int NW, int CT>
+__global__ void __launch_bounds__(NW * kWave, D == 256 ? 1 : 2) attn8_kernel(Attn8Args p) {
+  constexpr int G = D / 32, J = D / 16;
+  constexpr int kPart = (4 * J + 2) * 64;     // floats a wave leaves in LDS, a column tile
+  extern __shared__ __attribute__((aligned(16))) float s_merge[];
+  const KvRows& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane >> 4, l = lane & 15;
+  const int R = (int)p.group_by.d;
+
+  // pairs (sequence, key/value head) vary fastest: workgroups that read the same
+  // pages are a multiple of the pairs apart and so, for 8 pairs and their multiples,
+  // on the same XCD; the last column tiles, which see the most tokens, come first
+  const int rest = p.pairs_by.div(blockIdx.x), pair = blockIdx.x - rest * p.pairs_by.d;
+  const int b = p.kv_heads_by.div(pair), kvh = pair - b * p.kv_heads;
+  const int turn = p.splits_by.div(rest), split = rest - turn * p.splits;
+  const int tile0 = p.tiles - 1 - turn;
+  const int32_t* const table = a.table + (int64_t)b * a.width;
+  // the wave's first page numbers, read at the same time as the lengths: where the
+  // hints hold, a split starts here
+  const int guess_at = split * p.split_pages + wave + NW * lane;
+  const int guess = guess_at < a.width ? table[guess_at] : -1;
+  const int row0 = max(a.cu[b], 0);
+  const int n = max(min(max(a.cu[b + 1], 0), a.rows) - row0, 0);   // rows of the call for any cu_rows
+  const int len = max(a.lens[b], 0);
+  const int cols = n * R;
+  const int64_t stride = (int64_t)p.kv_heads * (128 * D);
+  const uint8_t* const base = p.data + (int64_t)kvh * (128 * D);
+  const uint32_t* const exps = p.exps + 2 * kvh;
+
+  for (int tile = tile0; tile * (16 * CT) < cols; tile += p.tiles) {
+    const int c_hi = min(tile * (16 * CT) + 16 * CT - 1, cols - 1);
+    const int pos_lo = len - n + p.group_by.div(tile * (16 * CT));
+    const int pos_hi = len - n + p.group_by.div(c_hi);
+    const int64_t pages64 = ((int64_t)pos_hi + 64) / 64;
+    const int pages = (int)(pages64 < a.width ? pages64 : a.width);
+    const int first = p.window > 0 ? max(pos_lo - p.window + 1, 0) / 64 : 0;
+    const int total = max(pages - first, 0);
+    const int per = max(p.split_pages, p.splits_by.div(total + p.splits - 1));
+    const int j0 = min(split * per, total), j1 = min(j0 + per, total);
+    const int count = (j1 - j0 - wave + NW - 1) / NW;
+
+    // the wave's next page.  Lanes hold the places, numbers and exponents of 64 pages
+    // at a time.
+    int k = -1, held_at = 0, held_id = 0, at = -1;
+    u2 held_exp = {0, 0};
+    uint32_t exp_k = 0, exp_v = 0;
+    const uint8_t* src = base;
+    auto next = [&]() {
+      for (at = -1; ++k < count;) {
+        if ((k & 63) == 0) {
+          const int j = j0 + wave + NW * (k + lane);
+          held_at = j < j1 ? first + j : -1;
+          held_id = -1;
+          if (held_at >= 0 && held_at < pages)
+            held_id = k == 0 && per == p.split_pages && first == 0 ? guess : table[held_at];
+          if (held_id < 0 || held_id >= p.n_pages) held_id = -1;
+          if (held_id >= 0)
+            held_exp = *reinterpret_cast<const u2*>(exps + (int64_t)held_id * (2 * p.kv_heads));
+        }
+        const int id = __builtin_amdgcn_readlane(held_id, k & 63);
+        if (id < 0) continue;      // no tokens there
+        at = __builtin_amdgcn_readlane(held_at, k & 63);
+        src = base + id * stride;
+        break;
+      }
+    };
+    Keys8<D> kt;
+    u4v vt[J];
+    auto load_values = [&]() {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        vt[j] = *reinterpret_cast<const u4v*>(src + 64 * D + j * 1024 + lane * 16);
+    };
+    auto load_exponents = [&]() {
+      exp_k = __builtin_amdgcn_readlane(held_exp[0], k & 63);
+      exp_v = __builtin_amdgcn_readlane(held_exp[1], k & 63);
+    };
+    // this lane's column, its query's loads ahead of the pages' and its scaling behind
+    int row[CT], head[CT], pos[CT];
+    Query<G> Q[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int col = tile * (16 * CT) + 16 * ct + l;
+      const bool on = col < cols;
+      const int nth = p.group_by.div(col);
+      row[ct] = on ? row0 + nth : -1;
+      head[ct] = kvh * R + col - nth * R;
+      pos[ct] = on ? len - n + nth : -1;
+      Q[ct].load(a.q + (on ? row[ct] * a.q_row + head[ct] * a.q_head : 0) + 8 * r, on);
+    }
+    next();
+    if (at >= 0) {
+      kt.load(src, lane);
+      load_values();
+      load_exponents();
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) Q[ct].template scale<DT>(p.scale);
+
+    f4 O[CT][J];
+    float m[CT];            // the reference
+    float least[CT];        // the lowest that it may be
+    float sum[CT];          // this lane's weights without 2^f
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      m[ct] = least[ct] = -INFINITY;
+      sum[ct] = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) O[ct][j] = f4{0, 0, 0, 0};
+    }
+
+    while (at >= 0) {
+      const int t0 = at * 64;
+      f4 sc[CT][4];
+      unroll<4>([&](auto u) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) sc[ct][u] = f4{0, 0, 0, 0};
+        unroll<G>([&](auto g) {
+          const u4v w = kt.codes[u][g / 2];
+          const h8 ka = codes8(w[2 * (g % 2)], w[2 * (g % 2) + 1]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) sc[ct][u] = mfma(ka, Q[ct].q[g], sc[ct][u]);
+        });
+      });
+      int ek[4], ev[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        ek[u] = exponent8(exp_k, u);
+        ev[u] = exponent8(exp_v, u);
+      }
+      // the keys' registers are free: the next page's keys arrive behind the values'
+      // product, its values behind the next logits
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) asm volatile("" : "+v"(sc[ct][u]));   // done here, not after the loads
+      __builtin_amdgcn_sched_barrier(0);
+      next();
+      kt.load(src, lane);          // past the last page: that page's again, not used
+      load_exponents();
+      __builtin_amdgcn_sched_barrier(0);
+
+      // base-2 logits and the values' exponent above the reference, plus kWeightExp
+      float y[CT][16], top[CT];
+      bool raise = false;
+      uint64_t lower = 0;     // bit l: column l's four lanes
+      const bool edge = t0 + 63 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const bool none = m[ct] == -INFINITY;
+        const float m8 = none ? -kWeightExp : m[ct] - kWeightExp;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float c = ldexpf(Q[ct].factor, ek[u]), d = (float)ev[u] - m8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[ct][4 * u + i] = __builtin_fmaf(sc[ct][u][i], c, d);
+        }
+        if (edge) {
+          asm volatile("");      // stays a branch: few pages have an edge
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
+            if (t > pos[ct] || (p.window > 0 && t <= pos[ct] - p.window)) y[ct][i] = -INFINITY;
+          }
+        }
+        top[ct] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top[ct] = fmaxf(top[ct], y[ct][i]);
+        raise |= top[ct] > (none ? -INFINITY : kWeightExp + kRaise);
+        const uint64_t low = __ballot(top[ct] < kWeightExp - kLower && m[ct] > least[ct]);
+        lower |= low & low >> 16 & low >> 32 & low >> 48;
+      }
+      if (__any(raise) || (lower & 0xFFFFu) != 0) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const bool none = m[ct] == -INFINITY;
+          float most = fmaxf(top[ct], __shfl_xor(top[ct], 16));
+          most = fmaxf(most, __shfl_xor(most, 32));
+          // the reference in y's scale stands at kWeightExp
+          float up = most == -INFINITY ? 0.f : most - kWeightExp;
+          if (!none && up < 0.f) up = up < -kLower ? fmaxf(up, least[ct] - m[ct]) : 0.f;
+          const float f = none ? 0.f : __builtin_amdgcn_exp2f(-up);
+          if (!none) m[ct] += up;
+          else if (most != -INFINITY) m[ct] = up;
+          least[ct] = fmaxf(least[ct], m[ct] - kBelow);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[ct][i] -= up;
+#pragma unroll
+          for (int j = 0; j < J; ++j) O[ct][j] *= f;
+          sum[ct] *= f;
+        }
+      }
+      h8 wh[CT][2], wl[CT][2];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[ct][i] = __builtin_amdgcn_exp2f(y[ct][i]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          sum[ct] = __builtin_fmaf((y[ct][4 * u] + y[ct][4 * u + 1]) + (y[ct][4 * u + 2] + y[ct][4 * u + 3]),
+                                   pow2(-ev[u]), sum[ct]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u4v wv, rv;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float y0 = y[ct][8 * h + 2 * x], y1 = y[ct][8 * h + 2 * x + 1];
+            const h2 w = {(_Float16)y0, (_Float16)y1};
+            const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
+            wv[x] = as_u32(w);
+            rv[x] = as_u32(rest);
+          }
+          wh[ct][h] = __builtin_bit_cast(h8, wv);
+          wl[ct][h] = __builtin_bit_cast(h8, rv);
+        }
+      }
+      unroll<J>([&](auto j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const h8 va = codes8(vt[j][2 * h], vt[j][2 * h + 1]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            O[ct][j] = mfma(va, wh[ct][h], O[ct][j]);
+            O[ct][j] = mfma(va, wl[ct][h], O[ct][j]);
+          }
+        }
+      });
+      __builtin_amdgcn_sched_barrier(0);
+      load_values();
+    }
+
+    // the waves' parts joined in order
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float* const s = s_merge + (wave * CT + ct) * kPart;
+      sum[ct] += __shfl_xor(sum[ct], 16);
+      sum[ct] += __shfl_xor(sum[ct], 32);
+#pragma unroll
+      for (int j = 0; j < J; ++j) reinterpret_cast<f4*>(s)[j * 64 + lane] = O[ct][j];
+      s[4 * J * 64 + lane] = sum[ct];
+      s[(4 * J + 1) * 64 + lane] = m[ct];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      if (row[ct] < 0) continue;
+      auto part_of = [&](int w) { return s_merge + (w * CT + ct) * kPart; };
+      float mw[NW], mx = -INFINITY, all = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        mw[w] = part_of(w)[(4 * J + 1) * 64 + lane];
+        mx = fmaxf(mx, mw[w]);
+      }
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        mw[w] = mw[w] == mx ? 1.f : __builtin_amdgcn_exp2f(mw[w] - mx);
+        all += mw[w] * part_of(w)[4 * J * 64 + lane];
+      }
+      const int64_t out_at = (int64_t)row[ct] * a.heads + head[ct];
+      const float inv = all == 0.f ? 0.f : 1.f / all;
+      for (int j = wave; j < J; j += NW) {
+        f4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) o += mw[w] * reinterpret_cast<const f4*>(part_of(w))[j * 64 + lane];
+        const int d = 16 * j + 4 * r;
+        if (p.splits == 1) {
+          uint16_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = from_float<DT>(all == 0.f ? 0.f : o[i] * inv);
+          *reinterpret_cast<u2*>(p.out + out_at * D + d) = u2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+        } else {
+          *reinterpret_cast<f4*>(p.part + (out_at * p.splits + split) * D + d) = o;
+        }
+      }
+      if (wave == 0 && r == 0) {
+        if (p.splits == 1) {
+          if (p.lse != nullptr) p.lse[out_at] = log_sum(all, mx);
+        } else {
+          reinterpret_cast<f4*>(p.part + (int64_t)a.rows * a.heads * p.splits *
+                                             D)[out_at * p.splits + split] = f4{all, mx, all, 0.f};
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// How a call is split: column tiles of a sequence and splits of its pages.  Hints
+// past what the call can have count as that, so that nothing overflows; there is at
+// least one row and one sequence.
+struct Attn8Plan {
+  int64_t pairs, tiles, splits, split_pages;
+  int waves, ct;            // waves a workgroup, column tiles a wave
+};
+static Attn8Plan attn8_plan(const wq_kv8_cache* c, const wq_kv4_rows* a, int64_t max_rows,
+                            int64_t max_len) {
+  Attn8Plan p{};
+  const int64_t R = a->n_heads / c->n_kv_heads;
+  if (max_rows > a->n_rows) max_rows = a->n_rows;
+  if (max_len > 64 * a->table_width) max_len = 64 * a->table_width;
+  const int64_t cols = (max_rows < 1 ? 1 : max_rows) * R;
+  p.ct = c->head_dim <= 128 && cols >= 64 ? 2 : 1;
+  p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
+  p.pairs = a->n_seqs * c->n_kv_heads;
+  int64_t pages = (max_len + 63) / 64;
+  if (pages < 1) pages = 1;
+  const int64_t items = p.pairs * p.tiles, at_once = c->head_dim == 256 ? 256 : 512;
+  int64_t splits = (at_once + items - 1) / items;
+  const int64_t waves = items * ((pages + kAttnWaves - 1) / kAttnWaves) <= 256 ? kAttnWaves : 2 * kAttnWaves;
+  const int64_t most = (pages + waves - 1) / waves;
+  if (splits > most) splits = most;
+  p.waves = kAttnWaves;
+  if (items <= 256 && pages <= 2 * kAttnMoreWaves) {
+    splits = 1;
+    if (pages > kAttnWaves && p.ct == 1 && c->head_dim <= 128) p.waves = kAttnMoreWaves;
+  }
+  p.split_pages = (pages + splits - 1) / splits;
+  p.splits = (pages + p.split_pages - 1) / p.split_pages;
+  return p;
+}
+
+// ------------------------------------------------------------- accumulate
+// mass[b][kvh][t] += sum over the rows' heads of the group of exp(logit - lse).  A
+// workgroup owns pages, so no sum crosses workgroups and the order is fixed.
+struct Mass8Args {
+  KvRows a;
+  const uint8_t* data;
+  const uint32_t* exps;
+  int64_t n_pages;
+  Divisor kv_heads_by, group_by, pairs_by;
+  int kv_heads, window;
+  float scale;
+  const float* lse;
+  const int32_t* held;
+  float* mass;
+  int64_t mass_tokens;
+};
+
+// Sums of v[0..15] over the 16 lanes of a row: lane l ends with that of v[l].
+__device__ __forceinline__ float row16_transposed(const float (&v)[16], int l) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = row16_sum(v[i]);
+    s = l == i ? x : s;
+  }
+  return s;
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kAttnWaves * kWave, 2) mass8_kernel(Mass8Args p) {
+  constexpr int G = D / 32;
+  const KvRows& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane >> 4, l = lane & 15;
+  const int R = (int)p.group_by.d;
+  const int rest = p.pairs_by.div(blockIdx.x), pair = blockIdx.x - rest * p.pairs_by.d;
+  const int b = p.kv_heads_by.div(pair), kvh = pair - b * p.kv_heads;
+  const int row0 = max(a.cu[b], 0);
+  const int n = max(min(max(a.cu[b + 1], 0), a.rows) - row0, 0);
+  const int len = max(a.lens[b], 0), held = p.held[b];
+  const int cols = n * R;
+  const int64_t tokens = min((int64_t)len, p.mass_tokens);
+  const int pages = (int)min((tokens + 63) / 64, a.width);
+  const int32_t* const table = a.table + (int64_t)b * a.width;
+  float* const mass = p.mass + ((int64_t)b * p.kv_heads + kvh) * p.mass_tokens;
+  const int step = (gridDim.x / p.pairs_by.d) * kAttnWaves;
+
+  for (int at = rest * kAttnWaves + wave; at < pages; at += step) {
+    const int t0 = at * 64;
+    const int id = __builtin_amdgcn_readfirstlane(table[at]);
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    if (id >= 0 && id < p.n_pages) {
+      const int64_t ph = (int64_t)id * p.kv_heads + kvh;
+      Keys8<D> kt;
+      kt.load(p.data + ph * (128 * D), lane);
+      const uint32_t exp_k = p.exps[2 * ph];
+      for (int tile = 0; tile * 16 < cols; ++tile) {
+        const int col = tile * 16 + l;
+        const int nth = p.group_by.div(col), row = row0 + nth, head = kvh * R + col - nth * R;
+        const bool in = col < cols;
+        float lse = in ? p.lse[(int64_t)row * a.heads + head] : INFINITY;
+        const bool on = in && fabsf(lse) < INFINITY;
+        lse = on ? lse * 1.44269504f : INFINITY;
+        const int pos = on ? len - n + nth : -1;
+        Query<G> Q;
+        Q.load(a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r, on);
+        Q.template scale<DT>(p.scale);
+        unroll<4>([&](auto u) {
+          f4 sc = {0, 0, 0, 0};
+          unroll<G>([&](auto g) {
+            const u4v w = kt.codes[u][g / 2];
+            sc = mfma(codes8(w[2 * (g % 2)], w[2 * (g % 2) + 1]), Q.q[g], sc);
+          });
+          const float c = ldexpf(Q.factor, exponent8(exp_k, u));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 16 * u + 4 * r + i;
+            float y = __builtin_fmaf(sc[i], c, -lse);
+            if (t > pos || (p.window > 0 && t <= pos - p.window)) y = -INFINITY;
+            acc[4 * u + i] += __builtin_amdgcn_exp2f(y);
+          }
+        });
+      }
+    }
+    const int t = t0 + 16 * (l >> 2) + 4 * r + (l & 3);
+    const float s = row16_transposed(acc, l);
+    if (t < tokens) mass[t] = t < held ? mass[t] + s : s;
+  }
+}
+
+}  // namespace wqd
+
+using namespace wqd;
+
+static int check_attention8(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_t max_rows,
+                            int64_t max_len, const char* who) {
+  if (int e = kv8_check_cache(cache, who)) return e;
+  const wq_kv4_cache shape = kv8_shape(cache);
+  if (int e = kv4_check_rows(&shape, rows, who)) return e;
+  if (max_rows < 0 || max_len < 0) return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
+  return WQ_OK;
+}
+
+extern "C" int64_t wq_kv8_attention_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
+                                              int64_t max_rows, int64_t max_len) {
+  if (int e = check_attention8(cache, rows, max_rows, max_len, "wq_kv8_attention_workspace")) return e;
+  wq::ok();
+  if (rows->n_rows == 0 || rows->n_seqs == 0) return 0;
+  const Attn8Plan p = attn8_plan(cache, rows, max_rows, max_len);
+  if (p.splits == 1) return 0;
+  return (rows->n_rows * rows->n_heads * p.splits * (cache->head_dim + 4) * 4 + 15) / 16 * 16;
+}
+
+extern "C" int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
+                                int64_t max_rows, int64_t max_len, float scale, int64_t window,
+                                uint16_t* out, float* lse, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+  const char* who = "wq_kv8_attention";
+  if (int e = check_attention8(cache, rows, max_rows, max_len, who)) return e;
+  if (window < 0) return wq::fail(WQ_ERR_INVALID_ARG, "%s: window must be at least 0", who);
+  if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
+  const int64_t need = wq_kv8_attention_workspace(cache, rows, max_rows, max_len);
+  if (!out || (need && !workspace)) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (workspace_bytes < need)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                    (long long)workspace_bytes, (long long)need);
+  if (!aligned16(out) || !aligned4(lse) || !aligned16(workspace))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
+  const Attn8Plan plan = attn8_plan(cache, rows, max_rows, max_len);
+  const int64_t grid = plan.pairs * plan.tiles * plan.splits;
+  const int64_t items = rows->n_rows * rows->n_heads;
+  if (grid > 0x7FFFFFFFll || items > 0x7FFFFF00ll)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
+  Attn8Args p{};
+  p.a = kv4_rows(rows);
+  p.data = cache->data;
+  p.exps = reinterpret_cast<const uint32_t*>(cache->exponents);
+  p.n_pages = cache->n_pages;
+  p.kv_heads = (int)cache->n_kv_heads;
+  p.kv_heads_by = Divisor(cache->n_kv_heads);
+  p.group_by = Divisor(rows->n_heads / cache->n_kv_heads);
+  p.pairs_by = Divisor(plan.pairs);
+  p.splits_by = Divisor(plan.splits);
+  p.window = window > 0x40000000 ? 0 : (int)window;
+  p.tiles = (int)plan.tiles;
+  p.splits = (int)plan.splits;
+  p.split_pages = (int)plan.split_pages;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  p.part = static_cast<float*>(workspace);
+  int status = WQ_OK;
+  kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
+    constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
+    auto launch = [&](auto kernel) {
+      const size_t lds = (size_t)plan.waves * plan.ct * (D / 4 + 2) * 64 * 4;
+      if (!allow_lds((const void*)kernel, lds)) {
+        status = wq::fail(WQ_ERR_HIP, "%s: cannot use %zu bytes of LDS", who, lds);
+        return;
+      }
+      kernel<<<dim3((unsigned)grid), plan.waves * kWave, lds, (hipStream_t)stream>>>(p);
+    };
+    if (plan.ct == 2) {
+      if constexpr (D <= 128) launch(attn8_kernel<DT, D, kAttnWaves, 2>);
+    } else if (plan.waves == kAttnWaves) {
+      launch(attn8_kernel<DT, D, kAttnWaves, 1>);
+    } else {
+      if constexpr (D <= 128) launch(attn8_kernel<DT, D, kAttnMoreWaves, 1>);
+    }
+    if (status == WQ_OK && plan.splits > 1)
+      join_kernel<DT, D><<<dim3((unsigned)items), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
+          p.part, items, p.splits, out, lse);
+  });
+  return status == WQ_OK ? check_launch(who) : status;
+}
+
+extern "C" int64_t wq_kv8_accumulate_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
+                                               int64_t max_rows, int64_t max_len) {
+  if (int e = check_attention8(cache, rows, max_rows, max_len, "wq_kv8_accumulate_workspace")) return e;
+  wq::ok();
+  return 0;
+}
+
+extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
+                                 int64_t max_rows, int64_t max_len, const float* lse, float scale,
+                                 int64_t window, const int32_t* held, float* mass,
+                                 int64_t mass_tokens, void* workspace, int64_t workspace_bytes,
+                                 void* stream) {
+  const char* who = "wq_kv8_accumulate";
+  if (int e = check_attention8(cache, rows, max_rows, max_len, who)) return e;
+  if (window < 0 || mass_tokens < 1)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad window or mass size", who);
+  if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
+  if (!lse || !held || !mass) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned4(lse) || !aligned4(held) || !aligned4(mass))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
+  if (max_len > 64 * rows->table_width) max_len = 64 * rows->table_width;
+  const int64_t pairs = rows->n_seqs * cache->n_kv_heads;
+  int64_t groups = (max_len + 64 * kAttnWaves - 1) / (64 * kAttnWaves);
+  if (groups < 1) groups = 1;
+  if (pairs * groups > 0x7FFFFFFFll || rows->n_rows * rows->n_heads > 0x7FFFFF00ll)
+    return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
+  Mass8Args p{};
+  p.a = kv4_rows(rows);
+  p.data = cache->data;
+  p.exps = reinterpret_cast<const uint32_t*>(cache->exponents);
+  p.n_pages = cache->n_pages;
+  p.kv_heads = (int)cache->n_kv_heads;
+  p.kv_heads_by = Divisor(cache->n_kv_heads);
+  p.group_by = Divisor(rows->n_heads / cache->n_kv_heads);
+  p.pairs_by = Divisor(pairs);
+  p.window = window > 0x40000000 ? 0 : (int)window;
+  p.scale = scale;
+  p.lse = lse;
+  p.held = held;
+  p.mass = mass;
+  p.mass_tokens = mass_tokens;
+  kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
+    mass8_kernel<decltype(dt)::value, decltype(d)::value>
+        <<<dim3((unsigned)(pairs * groups)), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(p);
+  });
+  return check_launch(who);
+}

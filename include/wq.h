@@ -499,6 +499,118 @@ int wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_rows* rows, int64_t
                      int64_t n_sel, uint16_t* out, float* lse, void* workspace,
                      int64_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- 8-bit key/value cache
+ * The cache in 8 bits, an exponent for each block of tokens and head, for where 4 bits
+ * are too few.  Pages of 64 tokens, block tables, rows, slots and runs are those of
+ * the 4-bit cache, and wq_kv4_plan and wq_kv4_max_runs serve both.
+ *
+ * Format: a page is four blocks of 16 tokens.  A block's keys of one head share an
+ * exponent, and so do its values: a value stands for q 2^e, q in -127..127, where e
+ * is the smallest number from -24 on with max |w| 2^-e < 127.5 over the block's tokens
+ * and channels, and q = rint(w 2^-e), in float32 with round-half-to-even from inputs
+ * clamped to +-65504 (NaN as 0; so e <= 10).  Powers of two keep the quantization
+ * exact but for the one rounding, and a block whose later tokens are larger raises
+ * its exponent by shifts: the codes it has become rint(q 2^(e - e')).
+ *
+ * Layout: data [n_pages][n_kv_heads][128 D] bytes q + 128, keys then values, D =
+ * head_dim = 64, 128 or 256.  With token t = 16 u + l = 16 u + 4 r + i of a page (l < 16,
+ * r < 4, i < 4):
+ *   key byte    [u][d / 64][d % 32 / 8][l][d / 32 % 2][d % 8]
+ *   value byte  [d / 16][r][d % 16][u][i]
+ * 16 bytes are then operands of the matrix cores (8 channels of a token, 8 tokens of
+ * a channel), and a wave's load is contiguous.
+ * exponents: [n_pages][n_kv_heads][8], those of the four blocks' keys, then values
+ * (8-byte aligned; what no token was written to may hold anything). */
+
+typedef struct wq_kv8_cache {
+  uint8_t* data;
+  int8_t* exponents;
+  int64_t n_pages, n_kv_heads, head_dim;
+} wq_kv8_cache;
+
+/* Quantizes new keys and values into their slots, as wq_kv4_append does.  Only
+ * these tokens' bytes are written, and those of the tokens before them in a block whose
+ * exponent rises. */
+int wq_kv8_append(const wq_kv8_cache* cache, int dtype, const uint16_t* k, int64_t k_row_stride,
+                  int64_t k_head_stride, const uint16_t* v, int64_t v_row_stride,
+                  int64_t v_head_stride, int64_t n_rows, const int32_t* slots,
+                  const int32_t* runs, int64_t n_runs, void* stream);
+
+/* Attention of the rows over the cache: wq_kv4_attention without a choice of pages. */
+int64_t wq_kv8_attention_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
+                                   int64_t max_rows, int64_t max_len);
+int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_t max_rows,
+                     int64_t max_len, float scale, int64_t window, uint16_t* out, float* lse,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* What the rows looked at: the softmax weights of every cached token, summed over the
+ * rows of its sequence and the heads of its group, on top of the mass it has:
+ *   mass[b][g][t] = (t < held[b] ? mass[b][g][t] : 0)
+ *                   + sum over rows and heads h of group g of exp(logit - lse[row][h])
+ * for the tokens t < lens[b] (mass float32 [n_seqs][n_kv_heads][mass_tokens]; tokens past
+ * mass_tokens or the table have none, and what lies behind a sequence's tokens stays).  lse
+ * is what wq_kv8_attention gives for the same rows, scale and window; a row and head
+ * whose lse is not finite takes no part.  held int32 [n_seqs]: how many tokens have a
+ * mass already (0 for a new sequence; the length before the new tokens, where every
+ * step is counted).  Logits and sums are float32, in a fixed order.
+ * workspace: wq_kv8_accumulate_workspace bytes for the same arguments, 16-byte
+ * aligned (NULL where that is 0). */
+int64_t wq_kv8_accumulate_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
+                                    int64_t max_rows, int64_t max_len);
+int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_t max_rows,
+                      int64_t max_len, const float* lse, float scale, int64_t window,
+                      const int32_t* held, float* mass, int64_t mass_tokens, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
+/* Eviction: a sequence of more than `keep` tokens keeps, for each key/value head, its last
+ * `recent` ones and of the others the keep - recent of most mass (ties: the earlier
+ * token; NaN counts as least), in their order.  Each head keeps its own; the keys have
+ * been rotated, so places in the cache may change.  They move to fresh pages, since
+ * others may share the old ones, which stay as they are:
+ *   kept [n_seqs][n_kv_heads][keep]   the tokens kept, rising, -1 past the end (all, where
+ *                a sequence has at most `keep`)
+ *   new_lens[b]  min(lens[b], keep)
+ *   new_table    [n_seqs][table_width]: the old row where nothing is evicted, else the next
+ *                ceil(keep / 64) entries of free_pages, sequences in order, then -1
+ *   taken[0]     pages taken; more than n_free means that some were missing: their entries
+ *                are -1 and their tokens not written.  The old table still holds all.
+ *   new_mass     [n_seqs][n_kv_heads][new_tokens]: the kept tokens' masses; what lies
+ *                behind them stays.  new_tokens >= keep
+ * A block's exponent becomes the highest of those its tokens had.  Tokens past mass_tokens
+ * or the table are not there; a kept token in a page outside the cache becomes zeros.
+ * 1 <= keep <= 64 table_width, 0 <= recent <= keep, n_seqs <= WQ_KV4_MAX_SEQS.
+ * Outputs must not overlap inputs, nor free_pages name a page that is in use. */
+int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_t mass_tokens,
+                 const int32_t* block_table, int64_t table_width, const int32_t* lens,
+                 int64_t n_seqs, int64_t keep, int64_t recent, const int32_t* free_pages,
+                 int64_t n_free, int32_t* new_table, int32_t* new_lens, float* new_mass,
+                 int64_t new_tokens, int32_t* taken, int32_t* kept, void* stream);
+
+/* -------------------------------- norm and rotation of queries and keys
+ * What stands between a projection and the cache, for both caches: every head of
+ * queries and keys is divided by its root mean square and weighted, and its channels
+ * are rotated in pairs by the row's position,
+ *   y_d = x_d / sqrt(mean x^2 + eps) weight_d
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position inv_freq[j]
+ * for the n_freq pairs j: channels (j, n_freq + j), or with `neighbours` (2 j, 2 j + 1);
+ * channels from 2 n_freq on are not rotated.  float32, rounded once; angles are held to
+ * 2^-32 of a turn at any position.
+ * x and out are n_rows x n_heads x D with strides in elements, multiples of 8 (channels
+ * are consecutive, pointers 16-byte aligned); out may be x with x's strides, and must not
+ * overlap it otherwise.  weight [D] has the type of x; NULL: all 1.  eps < 0: no norm, and no
+ * weight.  n_heads = 0 leaves queries or keys out.  positions int32 [n_rows], inv_freq
+ * float64 [n_freq], a multiple of 4 up to D / 2 (0: no rotation, both may be NULL). */
+typedef struct wq_heads {
+  const uint16_t* x;
+  uint16_t* out;
+  const uint16_t* weight;
+  int64_t n_heads, row_stride, head_stride, out_row_stride, out_head_stride;
+} wq_heads;
+
+int wq_qk_norm_rope(int dtype, const wq_heads* q, const wq_heads* k, int64_t n_rows,
+                    int64_t head_dim, float eps, const int32_t* positions, const double* inv_freq,
+                    int64_t n_freq, int neighbours, void* stream);
+
 /* ------------------------------------------------ kernel-variant selection
  * Not part of the method: for tests and measurements that run a call on each
  * of the kernels the library could choose for it.  Each *_v entry point is
