@@ -215,6 +215,7 @@ append8_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 
 constexpr int kPick8Threads = 1024, kPick8Waves = kPick8Threads / kWave;
 constexpr int kPick8Bins = 2048;
+constexpr int kPick8Held = 16;         // masses a thread holds; those of longer sequences are read again
 
 struct Evict8Args {
   const int32_t *table, *lens, *free_pages;
@@ -223,7 +224,7 @@ struct Evict8Args {
   int32_t *new_table, *new_lens, *taken, *kept;
   float* new_mass;
   int seqs, heads, keep, recent, n_free, pages;   // pages: those of `keep` tokens
-  Divisor heads_by, pages_by;
+  Divisor heads_by;
 };
 
 // Tokens of a sequence: those with a mass and a place in the table.
@@ -252,36 +253,47 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t* s_wave) {
   return all;
 }
 
-// One workgroup a (sequence, head): the room-th highest key 11 bits at a time from
-// histograms in LDS, then every wave a stretch of the tokens with its place from the
-// counts of the waves before it.
+// A sequence's new table row and length, and the pages taken.
+__device__ __forceinline__ void evict_tables(const Evict8Args& p, int b, uint32_t* s_wave) {
+  const int tid = threadIdx.x, len = evict_len(p, b);
+  const bool over = len > p.keep;
+  uint32_t before = 0, all = 0;
+  for (int s = tid; s < p.seqs; s += kPick8Threads) {
+    const uint32_t need = evict_len(p, s) > p.keep ? p.pages : 0;
+    all += need;
+    if (s < b) before += need;
+  }
+  before = block_sum(before, s_wave);
+  if (b == 0) {
+    all = block_sum(all, s_wave);
+    if (tid == 0) p.taken[0] = (int)all;
+  }
+  if (tid == 0) p.new_lens[b] = min(len, p.keep);
+  for (int64_t i = tid; i < p.width; i += kPick8Threads) {
+    int page = -1;
+    if (!over) page = p.table[b * p.width + i];
+    else if (i < p.pages && before + i < (uint32_t)p.n_free) page = p.free_pages[before + i];
+    p.new_table[b * p.width + i] = page;
+  }
+}
+
+// One workgroup a sequence for the tables, and one a (sequence, head) for the tokens:
+// the room-th highest key 11 bits at a time from histograms in LDS (four of them for
+// the first bits, which many masses share), then every wave a stretch of the tokens
+// with its place from the counts of the waves before it.  Masses stay in registers.
+// Latency: 10 us for 4500 tokens, 15 for 16000 (22 with a read of the kept masses
+// behind the choice).
 __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
-  __shared__ uint32_t s_hist[kPick8Bins];
+  __shared__ uint32_t s_hist[6 * kPick8Bins];      // four of the first bits, one of the next each
   __shared__ uint32_t s_wave[kPick8Waves], s_count[kPick8Waves][2], s_found[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b = p.heads_by.div(blockIdx.x), head = blockIdx.x - b * p.heads;
+  if ((int)blockIdx.x < p.seqs) {
+    evict_tables(p, blockIdx.x, s_wave);
+    return;
+  }
+  const int item = blockIdx.x - p.seqs, b = p.heads_by.div(item), head = item - b * p.heads;
   const int len = evict_len(p, b);
   const bool over = len > p.keep;
-  if (head == 0) {
-    uint32_t before = 0, all = 0;
-    for (int s = tid; s < p.seqs; s += kPick8Threads) {
-      const uint32_t need = evict_len(p, s) > p.keep ? p.pages : 0;
-      all += need;
-      if (s < b) before += need;
-    }
-    before = block_sum(before, s_wave);
-    if (b == 0) {
-      all = block_sum(all, s_wave);
-      if (tid == 0) p.taken[0] = (int)all;
-    }
-    if (tid == 0) p.new_lens[b] = min(len, p.keep);
-    for (int64_t i = tid; i < p.width; i += kPick8Threads) {
-      int page = -1;
-      if (!over) page = p.table[b * p.width + i];
-      else if (i < p.pages && before + i < (uint32_t)p.n_free) page = p.free_pages[before + i];
-      p.new_table[b * p.width + i] = page;
-    }
-  }
   const int64_t pair = (int64_t)b * p.heads + head;
   const float* const mass = p.mass + pair * p.mass_tokens;
   float* const new_mass = p.new_mass + pair * p.new_tokens;
@@ -294,21 +306,47 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
     if (t < len) new_mass[i] = mass[t];
   }
   if (room == 0) return;
+  // every wave a stretch of the tokens, 64 at a time
+  const int turns = (old + kPick8Threads - 1) / kPick8Threads;
+  const int t0 = wave * turns * kWave + lane;
+  float held[kPick8Held];
+#pragma unroll
+  for (int i = 0; i < kPick8Held; ++i) {
+    const int t = t0 + i * kWave;
+    held[i] = i < turns && t < old ? mass[t] : 0.f;
+  }
+  // f(mass, its key, token) of the stretch's tokens, all lanes together (a token past
+  // the last: old or more)
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kPick8Held; ++i)
+      if (i < turns) f(held[i], mass_key(held[i]), t0 + i * kWave);
+    for (int i = kPick8Held; i < turns; ++i) {
+      const int t = t0 + i * kWave;
+      const float m = t < old ? mass[t] : 0.f;
+      f(m, mass_key(m), t);
+    }
+  };
+  for (int i = tid; i < 6 * kPick8Bins; i += kPick8Threads) s_hist[i] = 0;
+  __syncthreads();
   uint32_t cut = 0, rank = (uint32_t)room;     // 0 < room < old
   int bits = 0;
   for (int pass = 0; pass < 3; ++pass) {
     const int width = pass < 2 ? 11 : 10, shift = 32 - bits - width;
-    for (int i = tid; i < kPick8Bins; i += kPick8Threads) s_hist[i] = 0;
-    __syncthreads();
-    for (int t = tid; t < old; t += kPick8Threads) {
-      const uint32_t key = mass_key(mass[t]);
-      if (pass == 0 || (key >> (shift + width)) == cut)
-        atomicAdd(&s_hist[(key >> shift) & ((1u << width) - 1)], 1u);
-    }
+    const int copies = pass == 0 ? 4 : 1, first_copy = pass == 0 ? 0 : pass + 3;
+    uint32_t* const hist = s_hist + (pass == 0 ? lane & 3 : first_copy) * kPick8Bins;
+    each([&](float, uint32_t key, int t) {
+      if (t < old && (pass == 0 || (key >> (shift + width)) == cut))
+        atomicAdd(&hist[(key >> shift) & ((1u << width) - 1)], 1u);
+    });
     __syncthreads();
     // thread t holds the bins 2047 - 2 t and 2046 - 2 t: where the sum from above
     // reaches the rank
-    const uint32_t c0 = s_hist[kPick8Bins - 1 - 2 * tid], c1 = s_hist[kPick8Bins - 2 - 2 * tid];
+    uint32_t c0 = 0, c1 = 0;
+    for (int i = first_copy; i < first_copy + copies; ++i) {
+      c0 += s_hist[(i + 1) * kPick8Bins - 1 - 2 * tid];
+      c1 += s_hist[(i + 1) * kPick8Bins - 2 - 2 * tid];
+    }
     uint32_t total;
     uint32_t above = wave_excl_sum(c0 + c1, total);
     if (lane == 0) s_wave[wave] = total;
@@ -324,22 +362,13 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
     cut = s_found[0];
     rank = s_found[1];
     bits += width;
-    __syncthreads();
   }
   // keys above the cut, and of those equal to it the first `rank`
-  const int per = ((old + kPick8Threads - 1) / kPick8Threads) * kWave;
-  const int t0 = min(wave * per, old), t1 = min(t0 + per, old);
   uint32_t above = 0, equal = 0;
-  for (int t = t0 + lane; t < t1; t += kWave) {
-    const uint32_t key = mass_key(mass[t]);
-    above += key > cut;
-    equal += key == cut;
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    above += __shfl_xor(above, d);
-    equal += __shfl_xor(equal, d);
-  }
+  each([&](float, uint32_t key, int t) {
+    above += __popcll(__ballot(t < old && key > cut));
+    equal += __popcll(__ballot(t < old && key == cut));
+  });
   if (lane == 0) { s_count[wave][0] = above; s_count[wave][1] = equal; }
   __syncthreads();
   uint32_t at = 0, eq = 0;
@@ -350,105 +379,202 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   }
   at += min(eq, rank);
   const uint64_t below = (1ull << lane) - 1;
-  for (int t = t0; t < t1; t += kWave) {
-    const bool in = t + lane < t1;
-    const float f = in ? mass[t + lane] : 0.f;
-    const uint32_t key = mass_key(f);
-    const uint64_t same = __ballot(in && key == cut);
-    const bool take = in && (key > cut || (key == cut && eq + __popcll(same & below) < rank));
+  each([&](float m, uint32_t key, int t) {
+    const uint64_t same = __ballot(t < old && key == cut);
+    const bool take = t < old && (key > cut || (key == cut && eq + __popcll(same & below) < rank));
     const uint64_t took = __ballot(take);
     if (take) {
       const uint32_t i = at + __popcll(took & below);
-      kept[i] = t + lane;
-      new_mass[i] = f;
+      kept[i] = t;
+      new_mass[i] = m;
     }
     at += __popcll(took);
     eq += __popcll(same);
-  }
+  });
 }
 
 // The kept tokens of a sequence over its budget, in fresh pages: one workgroup per
-// (page, head, keys or values).  Keys move by 16 bytes of a token; a value's bytes
-// stand with those of its 15 neighbours by position, so a lane gathers the 16 bytes
-// of a channel, the lanes of a wave the same tokens.
+// (page, head).  Keys move by 16 bytes of a token.  A value's bytes stand with those
+// of 15 other tokens, so that a token touches every line of its page's values: the
+// source pages go through LDS, 24 KB of them at a time (D = 256: 16), and a lane gathers the 16
+// bytes of a channel from there (the lanes of a wave the same tokens, 16 bytes
+// apart).  Memory bounds it: 12 sequences of 6001 to 16000 tokens, 6000 kept, 8 heads
+// of 128 channels read 175 MB and write 180 (nearly every source line has a kept
+// token), which a plain copy does in 69 us; it takes 102 (114 without the stores past
+// the caches; leaving out the gather in LDS saves 3 us, more workgroups a compute
+// unit none).
 constexpr int kMove8Threads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMove8Threads)
-move8_kernel(Evict8Args p, uint8_t* __restrict__ data, uint8_t* __restrict__ exps, int64_t n_pages) {
+move8_kernel(Evict8Args p, Divisor pairs_by, uint8_t* __restrict__ data,
+             uint8_t* __restrict__ exps, int64_t n_pages) {
+  constexpr int kPages = D == 256 ? 1 : 384 / D, kBytes = 64 * D;     // source pages in LDS, a page's bytes there
+  constexpr int kChunks = 4 * D / kMove8Threads;       // 16-byte chunks of a page that a thread writes
+  __shared__ __attribute__((aligned(16))) uint8_t s_values[kPages * kBytes];
   __shared__ int64_t s_src[64];       // page and head of a token, times 64, + its place; -1: none
-  __shared__ int s_exp[64];
+  __shared__ __attribute__((aligned(16))) int s_at[64];      // byte of a token's first value, pages in a row
+  __shared__ __attribute__((aligned(16))) int s_by[2][64];   // what its exponents rise by
+  __shared__ int64_t s_page[64];
+  __shared__ int s_pages, s_simple, s_rise;
   const int tid = threadIdx.x;
-  const bool values = blockIdx.x & 1;
-  const int rest = p.pages_by.div(blockIdx.x >> 1), pg = (int)(blockIdx.x >> 1) - rest * p.pages;
-  const int b = p.heads_by.div(rest), head = rest - b * p.heads;
-  if (evict_len(p, b) <= p.keep || pg >= p.width) return;
-  const int to = p.new_table[(int64_t)b * p.width + pg];
-  if (to < 0 || to >= n_pages) return;
+  // pages of a pair (sequence, head) share source pages: for 8 pairs and their
+  // multiples they are on one XCD
+  const int pg = pairs_by.div(blockIdx.x), pair = blockIdx.x - pg * (int)pairs_by.d;
+  const int b = p.heads_by.div(pair), head = pair - b * p.heads;
   const int n = min(p.keep - 64 * pg, 64);
+  const int kept = tid < n ? p.kept[(int64_t)pair * p.keep + 64 * pg + tid] : -1;
+  const int to = pg < p.width ? p.new_table[(int64_t)b * p.width + pg] : -1;
+  if (evict_len(p, b) <= p.keep || to < 0 || to >= n_pages) return;
   const int64_t dst = (int64_t)to * p.heads + head;
   if (tid < 64) {
     int64_t src = -1;
-    int e = kLeast8;
+    int place = -1;
+    u2 ex = {0, 0};
     if (tid < n) {
-      const int t = p.kept[((int64_t)b * p.heads + head) * p.keep + 64 * pg + tid];
-      const int page = p.table[(int64_t)b * p.width + t / 64];
+      place = kept / 64;
+      const int page = p.table[(int64_t)b * p.width + place];
       if (page >= 0 && page < n_pages) {
         const int64_t ph = (int64_t)page * p.heads + head;
-        src = ph * 64 + (t & 63);
-        e = min(max((int)(int8_t)exps[ph * 8 + (values ? 4 : 0) + (t & 63) / kBlock8], kLeast8), kMost8);
+        src = ph * 64 + (kept & 63);
+        ex = *reinterpret_cast<const u2*>(exps + ph * 8);
       }
     }
-    s_src[tid] = src;
-    int most = e;                     // of the block's 16 lanes
+    const int s = (int)(src & 63);
+    bool rise = false;
 #pragma unroll
-    for (int d = 1; d < kBlock8; d <<= 1) most = max(most, __shfl_xor(most, d));
-    s_exp[tid] = most - e;
-    if (tid % kBlock8 == 0 && tid < n) exps[dst * 8 + (values ? 4 : 0) + tid / kBlock8] = (uint8_t)most;
+    for (int v = 0; v < 2; ++v) {
+      const int e = src < 0 ? kLeast8 : exponent8(ex[v], s / kBlock8);
+      int most = e;                   // of the block's 16 lanes
+#pragma unroll
+      for (int d = 1; d < kBlock8; d <<= 1) most = max(most, __shfl_xor(most, d));
+      s_by[v][tid] = most - e;
+      if (tid % kBlock8 == 0 && tid < n) exps[dst * 8 + 4 * v + tid / kBlock8] = (uint8_t)most;
+      rise |= v && most > e;
+    }
+    rise = __any(rise);
+    // source pages in the order of their tokens
+    const int prev = __shfl_up(place, 1);
+    const bool first = tid < n && (tid == 0 || place != prev);
+    const uint64_t firsts = __ballot(first);
+    const int nth = __popcll(firsts & ((2ull << tid) - 1)) - 1;
+    s_src[tid] = src;
+    // tokens past the last count as the first byte's, and are not written
+    s_at[tid] = tid >= n ? 0 : src < 0 ? -1 : nth * kBytes + ((s >> 2) & 3) * 256 + (s / 16) * 4 + (s & 3);
+    const bool simple = !__any(tid < n && src < 0) && __popcll(firsts) <= kPages;
+    if (first) s_page[nth] = src < 0 ? -1 : src >> 6;
+    if (tid == 0) {
+      s_pages = __popcll(firsts);
+      s_simple = simple;
+      s_rise = rise;
+    }
   }
   __syncthreads();
   uint8_t* const page = data + dst * (128 * D);
-  if (!values) {
-    for (int c = tid; c < 64 * (D / 16); c += kMove8Threads) {
-      const int t = c & 63, cr = c >> 6;
-      if (t >= n) continue;
-      const int64_t src = s_src[t];
-      u4v w = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};     // no page: zeros
-      if (src >= 0) {
-        const int s = (int)(src & 63);
-        w = *reinterpret_cast<const u4v*>(data + (src >> 6) * (128 * D) + (s / 16) * (16 * D) + cr * 256 + (s & 15) * 16);
-      }
-      const int by = s_exp[t];
-      if (by > 0) {
+  const u4v zeros = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+  u4v key[kChunks], w[kChunks];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) w[x] = raise4(w[x], by);
-      }
-      *reinterpret_cast<u4v*>(page + (t / 16) * (16 * D) + cr * 256 + (t & 15) * 16) = w;
-    }
-    return;
+  for (int k = 0; k < kChunks; ++k) {
+    const int c = tid + k * kMove8Threads, t = c & 63, cr = c >> 6;
+    const int64_t src = s_src[t];
+    const int s = (int)(src & 63);
+    key[k] = w[k] = zeros;
+    if (src >= 0)
+      key[k] = *reinterpret_cast<const u4v*>(data + (src >> 6) * (128 * D) + (s / 16) * (16 * D) +
+                                             cr * 256 + (s & 15) * 16);
   }
-  for (int c = tid; c < 4 * D; c += kMove8Threads) {
-    const int d = c % D, r = c / D;
-    const int at = 64 * D + (d / 16) * 1024 + (d % 16) * 16;
-    u4v* const out = reinterpret_cast<u4v*>(page + at + r * 256);
-    if (4 * r >= n) continue;
-    u4v w = n < 64 ? *out : u4v{0, 0, 0, 0};
+  for (int q = 0; q < s_pages; q += kPages) {
+    if (q > 0) __syncthreads();
+    u4v got[kPages * kChunks];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int x = 0; x < kPages * kChunks; ++x) {
+      const int c = tid + x * kMove8Threads, slot = c / (4 * D);
+      const int64_t from = q + slot < s_pages ? s_page[q + slot] : -1;
+      got[x] = from >= 0 ? *reinterpret_cast<const u4v*>(data + from * (128 * D) + kBytes + (c % (4 * D)) * 16)
+                         : zeros;
+    }
+    if (q == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * u + 4 * r + i;
-        if (t >= n) continue;
-        const int64_t src = s_src[t];
-        uint32_t v = 128;
-        if (src >= 0) {
-          const int s = (int)(src & 63);
-          v = data[(src >> 6) * (128 * D) + at + ((s >> 2) & 3) * 256 + (s / 16) * 4 + (s & 3)];
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = tid + k * kMove8Threads, t = c & 63, cr = c >> 6, by = s_by[0][t];
+        if (by > 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) key[k][x] = raise4(key[k][x], by);
         }
-        if (s_exp[t] > 0)
-          v = __builtin_bit_cast(uint32_t, __builtin_fmaf((float)v - 128.f, pow2(-s_exp[t]), kRound8)) & 255u;
-        w[u] = (w[u] & ~(255u << (8 * i))) | v << (8 * i);
+        if (t < n)
+          __builtin_nontemporal_store(
+              key[k], reinterpret_cast<u4v*>(page + (t / 16) * (16 * D) + cr * 256 + (t & 15) * 16));
       }
-    *out = w;
+    }
+#pragma unroll
+    for (int x = 0; x < kPages * kChunks; ++x)
+      reinterpret_cast<u4v*>(s_values)[tid + x * kMove8Threads] = got[x];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int c = tid + k * kMove8Threads, d = c % D, r = c / D;
+      const int of = (d / 16) * 1024 + (d % 16) * 16;
+      if (s_simple) {                 // one round has them all
+        uint32_t v[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int4 at = *reinterpret_cast<const int4*>(&s_at[16 * u + 4 * r]);
+          v[4 * u] = s_values[at.x + of];
+          v[4 * u + 1] = s_values[at.y + of];
+          v[4 * u + 2] = s_values[at.z + of];
+          v[4 * u + 3] = s_values[at.w + of];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          w[k][u] = v[4 * u] | v[4 * u + 1] << 8 | v[4 * u + 2] << 16 | v[4 * u + 3] << 24;
+        continue;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int4 at = *reinterpret_cast<const int4*>(&s_at[16 * u + 4 * r]);
+        const int a[4] = {at.x, at.y, at.z, at.w};
+        // four tokens in a row: mostly of one round
+        const int lo = q * kBytes, hi = lo + kPages * kBytes;
+        if (max(max(a[0], a[1]), max(a[2], a[3])) < lo) continue;
+        uint32_t v[4];
+        bool in[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          in[i] = a[i] >= lo && a[i] < hi;
+          v[i] = s_values[in[i] ? a[i] - lo + of : of];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in[i]) w[k][u] = (w[k][u] & ~(255u << (8 * i))) | v[i] << (8 * i);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int c = tid + k * kMove8Threads, d = c % D, r = c / D;
+    u4v* const out = reinterpret_cast<u4v*>(page + kBytes + (d / 16) * 1024 + (d % 16) * 16 + r * 256);
+    if (4 * r >= n) continue;
+    if (s_rise) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int4 by = *reinterpret_cast<const int4*>(&s_by[1][16 * u + 4 * r]);
+        const int f[4] = {by.x, by.y, by.z, by.w};
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = __builtin_fmaf((float)((w[k][u] >> (8 * i)) & 255u) - 128.f, pow2(-f[i]), kRound8);
+        w[k][u] = bytes4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    if (n < 64) {                     // the bytes of tokens past the last stay
+      const u4v old = *out;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int have = min(max(n - (16 * u + 4 * r), 0), 4);
+        const uint32_t m = have == 4 ? 0xFFFFFFFFu : (1u << (8 * have)) - 1;
+        w[k][u] = (w[k][u] & m) | (old[u] & ~m);
+      }
+    }
+    __builtin_nontemporal_store(w[k], out);
   }
 }
 
@@ -514,7 +640,7 @@ extern "C" int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_
       new_tokens > (1 << 30))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad sizes", who);
   const int64_t pages = (keep + WQ_KV4_PAGE - 1) / WQ_KV4_PAGE, pairs = n_seqs * cache->n_kv_heads;
-  if (pairs * pages * 2 > 0x7FFFFFFFll || n_seqs * pages > 0x7FFFFFFFll)
+  if (pairs * pages > 0x7FFFFFFFll)
     return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many pages", who);
   if (!taken) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned4(taken)) return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
@@ -547,15 +673,15 @@ extern "C" int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_
   p.n_free = (int)n_free;
   p.pages = (int)pages;
   p.heads_by = Divisor(cache->n_kv_heads);
-  p.pages_by = Divisor(pages);
-  pick8_kernel<<<dim3((unsigned)pairs), kPick8Threads, 0, (hipStream_t)stream>>>(p);
+  pick8_kernel<<<dim3((unsigned)(n_seqs + pairs)), kPick8Threads, 0, (hipStream_t)stream>>>(p);
   uint8_t* const exps = reinterpret_cast<uint8_t*>(cache->exponents);
-  const dim3 grid((unsigned)(pairs * pages * 2));
+  const dim3 grid((unsigned)(pairs * pages));
+  const Divisor pairs_by(pairs);
   if (cache->head_dim == 64)
-    move8_kernel<64><<<grid, kMove8Threads, 0, (hipStream_t)stream>>>(p, cache->data, exps, cache->n_pages);
+    move8_kernel<64><<<grid, kMove8Threads, 0, (hipStream_t)stream>>>(p, pairs_by, cache->data, exps, cache->n_pages);
   else if (cache->head_dim == 128)
-    move8_kernel<128><<<grid, kMove8Threads, 0, (hipStream_t)stream>>>(p, cache->data, exps, cache->n_pages);
+    move8_kernel<128><<<grid, kMove8Threads, 0, (hipStream_t)stream>>>(p, pairs_by, cache->data, exps, cache->n_pages);
   else
-    move8_kernel<256><<<grid, kMove8Threads, 0, (hipStream_t)stream>>>(p, cache->data, exps, cache->n_pages);
+    move8_kernel<256><<<grid, kMove8Threads, 0, (hipStream_t)stream>>>(p, pairs_by, cache->data, exps, cache->n_pages);
   return check_launch(who);
 }
