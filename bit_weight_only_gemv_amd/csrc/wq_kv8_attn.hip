@@ -425,8 +425,9 @@ static Attn8Plan attn8_plan(const wq_kv8_cache* c, const wq_kv4_rows* a, int64_t
 }
 
 // ------------------------------------------------------------- accumulate
-// mass[b][kvh][t] += sum over the rows' heads of the group of exp(logit - lse).  A
-// workgroup owns pages, so no sum crosses workgroups and the order is fixed.
+// mass[b][kvh][t] += sum over the rows' heads of the group of exp(logit - lse).  Every
+// page belongs to one wave (few columns) or workgroup (many), so no sum crosses
+// workgroups and the order is fixed; keys alone are read.
 struct Mass8Args {
   KvRows a;
   const uint8_t* data;
@@ -439,81 +440,275 @@ struct Mass8Args {
   const int32_t* held;
   float* mass;
   int64_t mass_tokens;
+  h8* queries;            // scaled, [row][head][D]
+  float2* columns;        // [row][head]: factor, lse to base 2
 };
 
-// Sums of v[0..15] over the 16 lanes of a row: lane l ends with that of v[l].
+// Sums of v[0..15] over the 16 lanes of a row: lane l ends with that of v[l].  Each
+// step leaves a lane the half of the sums that its bit of l names.
 __device__ __forceinline__ float row16_transposed(const float (&v)[16], int l) {
-  float s = 0.f;
+  float a[8], b[4], c[2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float x = row16_sum(v[i]);
-    s = l == i ? x : s;
-  }
-  return s;
+  for (int i = 0; i < 8; ++i) a[i] = (l & 8 ? v[i + 8] : v[i]) + dpp_mov<0x128>(l & 8 ? v[i] : v[i + 8]);   // row_ror:8
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = (l & 4 ? a[i + 4] : a[i]) + dpp_mov<0x141>(l & 4 ? a[i] : a[i + 4]);   // row_half_mirror
+#pragma unroll
+  for (int i = 0; i < 2; ++i) c[i] = (l & 2 ? b[i + 2] : b[i]) + dpp_mov<0x4E>(l & 2 ? b[i] : b[i + 2]);    // quad_perm [2,3,0,1]
+  return (l & 1 ? c[1] : c[0]) + dpp_mov<0xB1>(l & 1 ? c[0] : c[1]);                                         // quad_perm [1,0,3,2]
 }
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kAttnWaves * kWave, 2) mass8_kernel(Mass8Args p) {
+// A pair's (sequence and key/value head) part of the call.
+struct Mass8Pair {
+  int b, kvh, row0, n, len, held, cols, pages;
+  int skip;               // the first pages of these have left the window, and their masses stay
+  int64_t tokens;
+  const int32_t* table;
+  float* mass;
+  __device__ __forceinline__ Mass8Pair(const Mass8Args& p, int pair) {
+    const KvRows& a = p.a;
+    b = p.kv_heads_by.div(pair);
+    kvh = pair - b * p.kv_heads;
+    row0 = max(a.cu[b], 0);
+    n = max(min(max(a.cu[b + 1], 0), a.rows) - row0, 0);   // rows of the call for any cu_rows
+    len = max(a.lens[b], 0);
+    held = p.held[b];
+    cols = n * (int)p.group_by.d;
+    tokens = min((int64_t)len, p.mass_tokens);
+    pages = (int)min((tokens + 63) / 64, a.width);
+    skip = p.window > 0 ? max(min(len - n - p.window + 1, min(held, len)), 0) / 64 : 0;
+    table = a.table + (int64_t)b * a.width;
+    mass = p.mass + ((int64_t)b * p.kv_heads + kvh) * p.mass_tokens;
+  }
+};
+
+// The weights of a block's four tokens in a lane, added to acc.
+template <bool EDGE>
+__device__ __forceinline__ void add_weights(f4 sc, float c, float lse, int t, int pos, int window, float* acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float y = __builtin_fmaf(sc[i], c, -lse);
+    if (EDGE && (t + i > pos || (window > 0 && t + i <= pos - window))) y = -INFINITY;
+    acc[i] += __builtin_amdgcn_exp2f(y);
+  }
+}
+
+// Few columns (decoding): up to CT column tiles of queries stay in registers, every wave
+// takes pages of its own, the next page's keys under way behind this one's logits.
+template <int DT, int D, int CT>
+__global__ void __launch_bounds__(kAttnWaves * kWave, 2) mass8_few_kernel(Mass8Args p) {
   constexpr int G = D / 32;
   const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane >> 4, l = lane & 15;
   const int R = (int)p.group_by.d;
-  const int rest = p.pairs_by.div(blockIdx.x), pair = blockIdx.x - rest * p.pairs_by.d;
-  const int b = p.kv_heads_by.div(pair), kvh = pair - b * p.kv_heads;
-  const int row0 = max(a.cu[b], 0);
-  const int n = max(min(max(a.cu[b + 1], 0), a.rows) - row0, 0);
-  const int len = max(a.lens[b], 0), held = p.held[b];
-  const int cols = n * R;
-  const int64_t tokens = min((int64_t)len, p.mass_tokens);
-  const int pages = (int)min((tokens + 63) / 64, a.width);
-  const int32_t* const table = a.table + (int64_t)b * a.width;
-  float* const mass = p.mass + ((int64_t)b * p.kv_heads + kvh) * p.mass_tokens;
-  const int step = (gridDim.x / p.pairs_by.d) * kAttnWaves;
+  const int rest = p.pairs_by.div(blockIdx.x);
+  const Mass8Pair o(p, blockIdx.x - rest * p.pairs_by.d);
+  const int step = (gridDim.x / p.pairs_by.d) * kAttnWaves, first = o.skip + rest * kAttnWaves + wave;
+  const int count = first < o.pages ? (o.pages - first + step - 1) / step : 0;
+  if (count == 0) return;
+  const int64_t stride = (int64_t)p.kv_heads * (128 * D);
+  const uint8_t* const base = p.data + (int64_t)o.kvh * (128 * D);
+  const int tok = 16 * (l >> 2) + 4 * r + (l & 3);       // the token whose sum this lane ends with
 
-  for (int at = rest * kAttnWaves + wave; at < pages; at += step) {
-    const int t0 = at * 64;
-    const int id = __builtin_amdgcn_readfirstlane(table[at]);
+  // more columns than the hint promised take more rounds over the pages
+  for (int tile = 0; tile == 0 || tile * 16 < o.cols; tile += CT) {
+    Query<G> Q[CT];
+    float lse[CT];
+    int pos[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int col = (tile + ct) * 16 + l, nth = p.group_by.div(col);
+      const int row = o.row0 + nth, head = o.kvh * R + col - nth * R;
+      const bool in = col < o.cols;
+      const float x = in ? p.lse[(int64_t)row * a.heads + head] : INFINITY;
+      const bool on = in && fabsf(x) < INFINITY;         // else its weights are exp(0 - inf)
+      lse[ct] = on ? x * 1.44269504f : INFINITY;
+      pos[ct] = on ? o.len - o.n + nth : -1;
+      Q[ct].load(a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r, on);
+    }
+    const int c_lo = min(tile * 16, max(o.cols - 1, 0)), c_hi = max(min((tile + CT) * 16, o.cols) - 1, 0);
+    const int pos_lo = o.len - o.n + p.group_by.div(c_lo), pos_hi = o.len - o.n + p.group_by.div(c_hi);
+
+    int k = -1, held_id = -1, id = -1, at = -1;
+    uint32_t held_exp = 0, exp_k = 0;
+    float old = 0.f;
+    Keys8<D> kt;
+    auto next = [&]() {      // the wave's next page (at: past the last, -1), its keys' loads
+      if (++k >= count) {
+        at = -1;
+        return;
+      }
+      if ((k & 63) == 0) {
+        const int j = first + step * (k + lane);
+        held_id = k + lane < count ? o.table[j] : -1;
+        if (held_id < 0 || held_id >= p.n_pages) held_id = -1;
+        if (held_id >= 0) held_exp = p.exps[2 * ((int64_t)held_id * p.kv_heads + o.kvh)];
+      }
+      at = first + step * k;
+      id = __builtin_amdgcn_readlane(held_id, k & 63);
+      if (p.window > 0 && at * 64 + 63 <= pos_lo - p.window) id = -1;     // none of these rows sees it
+      exp_k = __builtin_amdgcn_readlane(held_exp, k & 63);
+      if (id >= 0) kt.load(base + id * stride, lane);
+      const int t = at * 64 + tok;
+      old = t < o.tokens && (t < o.held || tile > 0) ? o.mass[t] : 0.f;
+    };
+    next();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) Q[ct].template scale<DT>(p.scale);
+    while (at >= 0) {
+      const int t0 = at * 64, id_now = id;
+      const uint32_t exp_now = exp_k;
+      const float old_now = old;
+      f4 sc[CT][4];
+      unroll<4>([&](auto u) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) sc[ct][u] = f4{0, 0, 0, 0};
+        unroll<G>([&](auto g) {
+          const u4v w = kt.codes[u][g / 2];
+          const h8 ka = codes8(w[2 * (g % 2)], w[2 * (g % 2) + 1]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) sc[ct][u] = mfma(ka, Q[ct].q[g], sc[ct][u]);
+        });
+      });
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) asm volatile("" : "+v"(sc[ct][u]));   // done here, not after the loads
+      __builtin_amdgcn_sched_barrier(0);
+      next();
+      __builtin_amdgcn_sched_barrier(0);
+      float acc[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+      if (id_now >= 0) {
+        const bool edge = t0 + 63 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float c = ldexpf(Q[ct].factor, exponent8(exp_now, u));
+            const int t = t0 + 16 * u + 4 * r;
+            if (edge) add_weights<true>(sc[ct][u], c, lse[ct], t, pos[ct], p.window, acc + 4 * u);
+            else add_weights<false>(sc[ct][u], c, lse[ct], t, pos[ct], p.window, acc + 4 * u);
+          }
+      }
+      const float s = row16_transposed(acc, l);
+      if (t0 + tok < o.tokens) o.mass[t0 + tok] = old_now + s;
+    }
+  }
+}
+
+// Many columns (prompts): the queries scaled once, [row][head][D], with their factor
+// and lse to base 2.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) scale8_kernel(Mass8Args p, Divisor heads_by, int64_t items) {
+  constexpr int G = D / 32;
+  const int lane = threadIdx.x & 63, r = lane >> 4, l = lane & 15;
+  const int64_t item = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 16 + l;
+  const bool in = item < items;
+  const int row = in ? heads_by.div((int)item) : 0, head = in ? (int)item - row * p.a.heads : 0;
+  const float x = in ? p.lse[item] : INFINITY;
+  const bool on = in && fabsf(x) < INFINITY;             // else its weights are exp(0 - inf)
+  Query<G> q;
+  q.load(p.a.q + (on ? row * p.a.q_row + head * p.a.q_head : 0) + 8 * r, on);
+  q.template scale<DT>(p.scale);
+  if (!in) return;
+#pragma unroll
+  for (int g = 0; g < G; ++g) p.queries[item * (D / 8) + 4 * g + r] = q.q[g];
+  if (r == 0) p.columns[item] = float2{q.factor, on ? x * 1.44269504f : INFINITY};
+}
+
+// Two pages a workgroup, four waves each: a page's keys stay in a wave's registers as
+// FP16 numbers while it goes through every fourth column tile.
+constexpr int kMass8Pages = 2, kMass8Turns = 4;
+template <int D>
+__global__ void __launch_bounds__(kMass8Pages* kMass8Turns* kWave, 2) mass8_many_kernel(Mass8Args p) {
+  constexpr int G = D / 32;
+  __shared__ float s_sum[kMass8Pages][kMass8Turns][kWave];
+  const KvRows& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane >> 4, l = lane & 15;
+  const int R = (int)p.group_by.d;
+  const int rest = p.pairs_by.div(blockIdx.x);
+  const Mass8Pair o(p, blockIdx.x - rest * p.pairs_by.d);
+  const int step = (gridDim.x / p.pairs_by.d) * kMass8Pages;
+  const int pg = wave / kMass8Turns, turn = wave % kMass8Turns;
+  const int tok = 16 * (l >> 2) + 4 * r + (l & 3);
+
+  for (int at0 = o.skip + rest * kMass8Pages; at0 < o.pages; at0 += step) {
+    const int at = at0 + pg, t0 = at * 64;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    const int id = at < o.pages ? __builtin_amdgcn_readfirstlane(o.table[at]) : -1;
     if (id >= 0 && id < p.n_pages) {
-      const int64_t ph = (int64_t)id * p.kv_heads + kvh;
+      const int64_t ph = (int64_t)id * p.kv_heads + o.kvh;
       Keys8<D> kt;
       kt.load(p.data + ph * (128 * D), lane);
       const uint32_t exp_k = p.exps[2 * ph];
-      for (int tile = 0; tile * 16 < cols; ++tile) {
-        const int col = tile * 16 + l;
-        const int nth = p.group_by.div(col), row = row0 + nth, head = kvh * R + col - nth * R;
-        const bool in = col < cols;
-        float lse = in ? p.lse[(int64_t)row * a.heads + head] : INFINITY;
-        const bool on = in && fabsf(lse) < INFINITY;
-        lse = on ? lse * 1.44269504f : INFINITY;
-        const int pos = on ? len - n + nth : -1;
-        Query<G> Q;
-        Q.load(a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r, on);
-        Q.template scale<DT>(p.scale);
+      // the rows that see some of the page: their positions from t0 on, and before the
+      // window has passed it
+      const int64_t from = (int64_t)t0 - (o.len - o.n);
+      const int64_t to = p.window > 0 ? from + 63 + p.window : (int64_t)o.n;
+      const int tile0 = (int)(max(from, (int64_t)0) * R / 16);
+      const int cols = (int)(min(max(to, (int64_t)0), (int64_t)o.n) * R), tiles = (cols + 15) / 16;
+      h8 q[G], q_next[G];
+      float2 col, col_next;
+      auto load = [&](int tile) {
+        const int c = tile * 16 + l, nth = p.group_by.div(c);
+        const bool in = c < o.cols;
+        const int64_t item = in ? (int64_t)(o.row0 + nth) * a.heads + o.kvh * R + c - nth * R : 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) q_next[g] = p.queries[item * (D / 8) + 4 * g + r];
+        col_next = p.columns[item];
+        if (!in) col_next.y = INFINITY;
+      };
+      int tile = tile0 + turn;
+      if (tile < tiles) load(tile);
+      h8 ka[4][G];
+      unroll<4>([&](auto u) {
+        unroll<G>([&](auto g) {
+          const u4v w = kt.codes[u][g / 2];
+          ka[u][g] = codes8(w[2 * (g % 2)], w[2 * (g % 2) + 1]);
+        });
+      });
+      for (; tile < tiles; tile += kMass8Turns) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) q[g] = q_next[g];
+        col = col_next;
+        if (tile + kMass8Turns < tiles) load(tile + kMass8Turns);
+        const int pos_lo = o.len - o.n + p.group_by.div(tile * 16);
+        const int pos_hi = o.len - o.n + p.group_by.div(min(tile * 16 + 15, o.cols - 1));
+        const int pos = o.len - o.n + p.group_by.div(tile * 16 + l);
+        const bool edge = t0 + 63 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
         unroll<4>([&](auto u) {
           f4 sc = {0, 0, 0, 0};
-          unroll<G>([&](auto g) {
-            const u4v w = kt.codes[u][g / 2];
-            sc = mfma(codes8(w[2 * (g % 2)], w[2 * (g % 2) + 1]), Q.q[g], sc);
-          });
-          const float c = ldexpf(Q.factor, exponent8(exp_k, u));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 16 * u + 4 * r + i;
-            float y = __builtin_fmaf(sc[i], c, -lse);
-            if (t > pos || (p.window > 0 && t <= pos - p.window)) y = -INFINITY;
-            acc[4 * u + i] += __builtin_amdgcn_exp2f(y);
-          }
+          unroll<G>([&](auto g) { sc = mfma(ka[u][g], q[g], sc); });
+          const float c = ldexpf(col.x, exponent8(exp_k, u));
+          const int t = t0 + 16 * u + 4 * r;
+          if (edge) add_weights<true>(sc, c, col.y, t, pos, p.window, acc + 4 * u);
+          else add_weights<false>(sc, c, col.y, t, pos, p.window, acc + 4 * u);
         });
       }
     }
-    const int t = t0 + 16 * (l >> 2) + 4 * r + (l & 3);
-    const float s = row16_transposed(acc, l);
-    if (t < tokens) mass[t] = t < held ? mass[t] + s : s;
+    s_sum[pg][turn][lane] = row16_transposed(acc, l);
+    __syncthreads();
+    if (turn == 0 && at < o.pages) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMass8Turns; ++i) s += s_sum[pg][i][lane];
+      const int t = t0 + tok;
+      if (t < o.tokens) o.mass[t] = t < o.held ? o.mass[t] + s : s;
+    }
+    __syncthreads();
   }
+}
+
+// Up to two column tiles stay in registers; more are many.
+static int mass8_tiles(const wq_kv8_cache* c, const wq_kv4_rows* a, int64_t max_rows) {
+  if (max_rows > a->n_rows) max_rows = a->n_rows;
+  const int64_t cols = (max_rows < 1 ? 1 : max_rows) * (a->n_heads / c->n_kv_heads);
+  return cols <= 16 ? 1 : cols <= 32 ? 2 : 3;
 }
 
 }  // namespace wqd
@@ -602,11 +797,16 @@ extern "C" int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* ro
   return status == WQ_OK ? check_launch(who) : status;
 }
 
+static int64_t mass8_queries_bytes(const wq_kv8_cache* c, const wq_kv4_rows* a) {
+  return a->n_rows * a->n_heads * c->head_dim * 2;
+}
+
 extern "C" int64_t wq_kv8_accumulate_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
                                                int64_t max_rows, int64_t max_len) {
   if (int e = check_attention8(cache, rows, max_rows, max_len, "wq_kv8_accumulate_workspace")) return e;
   wq::ok();
-  return 0;
+  if (rows->n_rows == 0 || rows->n_seqs == 0 || mass8_tiles(cache, rows, max_rows) < 3) return 0;
+  return (mass8_queries_bytes(cache, rows) + rows->n_rows * rows->n_heads * 8 + 15) / 16 * 16;
 }
 
 extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
@@ -619,14 +819,24 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
   if (window < 0 || mass_tokens < 1)
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: bad window or mass size", who);
   if (rows->n_rows == 0 || rows->n_seqs == 0) return wq::ok();
-  if (!lse || !held || !mass) return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
-  if (!aligned4(lse) || !aligned4(held) || !aligned4(mass))
+  const int64_t need = wq_kv8_accumulate_workspace(cache, rows, max_rows, max_len);
+  if (!lse || !held || !mass || (need && !workspace))
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (workspace_bytes < need)
+    return wq::fail(WQ_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                    (long long)workspace_bytes, (long long)need);
+  if (!aligned4(lse) || !aligned4(held) || !aligned4(mass) || !aligned16(workspace))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
   if (max_len > 64 * rows->table_width) max_len = 64 * rows->table_width;
-  const int64_t pairs = rows->n_seqs * cache->n_kv_heads;
-  int64_t groups = (max_len + 64 * kAttnWaves - 1) / (64 * kAttnWaves);
-  if (groups < 1) groups = 1;
-  if (pairs * groups > 0x7FFFFFFFll || rows->n_rows * rows->n_heads > 0x7FFFFF00ll)
+  const int tiles = mass8_tiles(cache, rows, max_rows);
+  const int64_t pairs = rows->n_seqs * cache->n_kv_heads, items = rows->n_rows * rows->n_heads;
+  const int64_t pages = max_len < 1 ? 1 : (max_len + 63) / 64;
+  // Few columns: three workgroups for every compute unit run at once; each wave has
+  // several pages where there are enough, so that its queries are made once.
+  const int64_t at_once = 768, each = tiles < 3 ? kAttnWaves : kMass8Pages;
+  int64_t groups = (pages + each - 1) / each;
+  if (tiles < 3 && pairs * groups > 2 * at_once) groups = (2 * at_once + pairs - 1) / pairs;
+  if (pairs * groups > 0x7FFFFFFFll || items > 0x7FFFFF00ll)
     return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
   Mass8Args p{};
   p.a = kv4_rows(rows);
@@ -643,9 +853,20 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
   p.held = held;
   p.mass = mass;
   p.mass_tokens = mass_tokens;
+  p.queries = static_cast<h8*>(workspace);
+  p.columns = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + mass8_queries_bytes(cache, rows));
+  const dim3 grid((unsigned)(pairs * groups));
+  hipStream_t st = (hipStream_t)stream;
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
-    mass8_kernel<decltype(dt)::value, decltype(d)::value>
-        <<<dim3((unsigned)(pairs * groups)), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(p);
+    constexpr int DT = decltype(dt)::value, D = decltype(d)::value;
+    if (tiles == 1) {
+      mass8_few_kernel<DT, D, 1><<<grid, kAttnWaves * kWave, 0, st>>>(p);
+    } else if (tiles == 2) {
+      mass8_few_kernel<DT, D, 2><<<grid, kAttnWaves * kWave, 0, st>>>(p);
+    } else {
+      scale8_kernel<DT, D><<<dim3((unsigned)((items + 63) / 64)), 256, 0, st>>>(p, Divisor(rows->n_heads), items);
+      mass8_many_kernel<D><<<grid, kMass8Pages * kMass8Turns * kWave, 0, st>>>(p);
+    }
   });
   return check_launch(who);
 }
