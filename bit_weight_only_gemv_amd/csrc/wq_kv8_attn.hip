@@ -440,9 +440,19 @@ struct Mass8Args {
   const int32_t* held;
   float* mass;
   int64_t mass_tokens;
-  h8* queries;            // scaled, [row][head][D]
-  float2* columns;        // [row][head]: factor, lse to base 2
+  // scaled queries in the order of the matrix cores' operands, and a column's factor, lse to
+  // base 2 and position: per key/value head `col_tiles` column tiles, of which those of
+  // sequence b begin at mass8_first_tile
+  h8* queries;            // [kvh][tile][D / 32][64 lanes]
+  f4* columns;            // [kvh][tile][16]
+  int64_t col_tiles;
 };
+
+// The column tiles of the rows before a sequence's, each sequence's last one partly used:
+// no more than this.
+__device__ __forceinline__ int64_t mass8_first_tile(int row0, int R, int b) {
+  return (int64_t)row0 * R / 16 + b;
+}
 
 // Sums of v[0..15] over the 16 lanes of a row: lane l ends with that of v[l].  Each
 // step leaves a lane the half of the sums that its bit of l names.
@@ -598,34 +608,41 @@ __global__ void __launch_bounds__(kAttnWaves * kWave, 2) mass8_few_kernel(Mass8A
   }
 }
 
-// Many columns (prompts): the queries scaled once, [row][head][D], with their factor
-// and lse to base 2.
+// Many columns (prompts): the queries scaled and laid out once.
 template <int DT, int D>
-__global__ void __launch_bounds__(256) scale8_kernel(Mass8Args p, Divisor heads_by, int64_t items) {
+__global__ void __launch_bounds__(kAttnWaves * kWave) scale8_kernel(Mass8Args p) {
   constexpr int G = D / 32;
+  const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, r = lane >> 4, l = lane & 15;
-  const int64_t item = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 16 + l;
-  const bool in = item < items;
-  const int row = in ? heads_by.div((int)item) : 0, head = in ? (int)item - row * p.a.heads : 0;
-  const float x = in ? p.lse[item] : INFINITY;
-  const bool on = in && fabsf(x) < INFINITY;             // else its weights are exp(0 - inf)
-  Query<G> q;
-  q.load(p.a.q + (on ? row * p.a.q_row + head * p.a.q_head : 0) + 8 * r, on);
-  q.template scale<DT>(p.scale);
-  if (!in) return;
+  const int R = (int)p.group_by.d;
+  const int rest = p.pairs_by.div(blockIdx.x);
+  const Mass8Pair o(p, blockIdx.x - rest * p.pairs_by.d);
+  const int64_t at = (int64_t)o.kvh * p.col_tiles + mass8_first_tile(o.row0, R, o.b);
+  const int step = (gridDim.x / p.pairs_by.d) * kAttnWaves;
+  for (int tile = rest * kAttnWaves + (threadIdx.x >> 6); tile * 16 < o.cols; tile += step) {
+    const int col = tile * 16 + l, nth = p.group_by.div(col);
+    const int row = o.row0 + nth, head = o.kvh * R + col - nth * R;
+    const float x = col < o.cols ? p.lse[(int64_t)row * a.heads + head] : INFINITY;
+    const bool on = fabsf(x) < INFINITY;               // else its weights are exp(0 - inf)
+    Query<G> q;
+    q.load(a.q + (on ? row * a.q_row + head * a.q_head : 0) + 8 * r, on);
+    q.template scale<DT>(p.scale);
 #pragma unroll
-  for (int g = 0; g < G; ++g) p.queries[item * (D / 8) + 4 * g + r] = q.q[g];
-  if (r == 0) p.columns[item] = float2{q.factor, on ? x * 1.44269504f : INFINITY};
+    for (int g = 0; g < G; ++g) p.queries[((at + tile) * G + g) * kWave + lane] = q.q[g];
+    if (r == 0)
+      p.columns[(at + tile) * 16 + l] = f4{q.factor, on ? x * 1.44269504f : INFINITY,
+                                           __builtin_bit_cast(float, on ? o.len - o.n + nth : -1), 0.f};
+  }
 }
 
-// Two pages a workgroup, four waves each: a page's keys stay in a wave's registers as
-// FP16 numbers while it goes through every fourth column tile.
-constexpr int kMass8Pages = 2, kMass8Turns = 4;
+// Two pages a workgroup, two waves each: a page's keys stay in a wave's registers as
+// FP16 numbers while it goes through every second column tile, the next one's loads
+// ahead.
+constexpr int kMass8Pages = 2, kMass8Turns = 2;
 template <int D>
 __global__ void __launch_bounds__(kMass8Pages* kMass8Turns* kWave, 2) mass8_many_kernel(Mass8Args p) {
   constexpr int G = D / 32;
   __shared__ float s_sum[kMass8Pages][kMass8Turns][kWave];
-  const KvRows& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane >> 4, l = lane & 15;
   const int R = (int)p.group_by.d;
@@ -634,6 +651,9 @@ __global__ void __launch_bounds__(kMass8Pages* kMass8Turns* kWave, 2) mass8_many
   const int step = (gridDim.x / p.pairs_by.d) * kMass8Pages;
   const int pg = wave / kMass8Turns, turn = wave % kMass8Turns;
   const int tok = 16 * (l >> 2) + 4 * r + (l & 3);
+  const int64_t first = (int64_t)o.kvh * p.col_tiles + mass8_first_tile(o.row0, R, o.b);
+  const h8* const queries = p.queries + first * (G * kWave) + lane;
+  const f4* const columns = p.columns + first * 16 + l;
 
   for (int at0 = o.skip + rest * kMass8Pages; at0 < o.pages; at0 += step) {
     const int at = at0 + pg, t0 = at * 64;
@@ -646,48 +666,48 @@ __global__ void __launch_bounds__(kMass8Pages* kMass8Turns* kWave, 2) mass8_many
       Keys8<D> kt;
       kt.load(p.data + ph * (128 * D), lane);
       const uint32_t exp_k = p.exps[2 * ph];
-      // the rows that see some of the page: their positions from t0 on, and before the
-      // window has passed it
-      const int64_t from = (int64_t)t0 - (o.len - o.n);
-      const int64_t to = p.window > 0 ? from + 63 + p.window : (int64_t)o.n;
-      const int tile0 = (int)(max(from, (int64_t)0) * R / 16);
-      const int cols = (int)(min(max(to, (int64_t)0), (int64_t)o.n) * R), tiles = (cols + 15) / 16;
-      h8 q[G], q_next[G];
-      float2 col, col_next;
+      // the rows that see some of the page, from the first one on to where the window
+      // has passed it; of those [whole0, whole1) see all of it
+      const int64_t from = (int64_t)t0 - (o.len - o.n), n = o.n;
+      auto row_in = [&](int64_t row) { return min(max(row, (int64_t)0), n); };
+      const int64_t to = p.window > 0 ? row_in(from + 63 + p.window) : n;
+      const int tile0 = (int)(row_in(from) * R / 16), tiles = (int)((to * R + 15) / 16);
+      const int whole0 = (int)((row_in(from + 63) * R + 15) / 16);
+      const int whole1 = p.window > 0 ? (int)(row_in(from + p.window) * R / 16) : tiles;
+      h8 q_next[G];
+      f4 col_next;
       auto load = [&](int tile) {
-        const int c = tile * 16 + l, nth = p.group_by.div(c);
-        const bool in = c < o.cols;
-        const int64_t item = in ? (int64_t)(o.row0 + nth) * a.heads + o.kvh * R + c - nth * R : 0;
 #pragma unroll
-        for (int g = 0; g < G; ++g) q_next[g] = p.queries[item * (D / 8) + 4 * g + r];
-        col_next = p.columns[item];
-        if (!in) col_next.y = INFINITY;
+        for (int g = 0; g < G; ++g) q_next[g] = queries[((int64_t)tile * G + g) * kWave];
+        col_next = columns[(int64_t)tile * 16];
       };
       int tile = tile0 + turn;
       if (tile < tiles) load(tile);
       h8 ka[4][G];
+      float by[4];
       unroll<4>([&](auto u) {
+        by[u] = pow2(exponent8(exp_k, u));
         unroll<G>([&](auto g) {
           const u4v w = kt.codes[u][g / 2];
           ka[u][g] = codes8(w[2 * (g % 2)], w[2 * (g % 2) + 1]);
         });
       });
       for (; tile < tiles; tile += kMass8Turns) {
+        h8 q[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) q[g] = q_next[g];
-        col = col_next;
+        const f4 col = col_next;
         if (tile + kMass8Turns < tiles) load(tile + kMass8Turns);
-        const int pos_lo = o.len - o.n + p.group_by.div(tile * 16);
-        const int pos_hi = o.len - o.n + p.group_by.div(min(tile * 16 + 15, o.cols - 1));
-        const int pos = o.len - o.n + p.group_by.div(tile * 16 + l);
-        const bool edge = t0 + 63 > pos_lo || (p.window > 0 && t0 <= pos_hi - p.window);
+        const float pos_bits = col[2];       // a bit cast of the element itself takes the first one
+        const int pos = __builtin_bit_cast(int, pos_bits);
+        const bool edge = tile < whole0 || tile >= whole1;
         unroll<4>([&](auto u) {
           f4 sc = {0, 0, 0, 0};
           unroll<G>([&](auto g) { sc = mfma(ka[u][g], q[g], sc); });
-          const float c = ldexpf(col.x, exponent8(exp_k, u));
+          const float c = col[0] * by[u];
           const int t = t0 + 16 * u + 4 * r;
-          if (edge) add_weights<true>(sc, c, col.y, t, pos, p.window, acc + 4 * u);
-          else add_weights<false>(sc, c, col.y, t, pos, p.window, acc + 4 * u);
+          if (edge) add_weights<true>(sc, c, col[1], t, pos, p.window, acc + 4 * u);
+          else add_weights<false>(sc, c, col[1], t, pos, p.window, acc + 4 * u);
         });
       }
     }
@@ -797,8 +817,12 @@ extern "C" int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* ro
   return status == WQ_OK ? check_launch(who) : status;
 }
 
+// Column tiles of a key/value head that hold any division of the rows into sequences.
+static int64_t mass8_col_tiles(const wq_kv8_cache* c, const wq_kv4_rows* a) {
+  return a->n_rows * (a->n_heads / c->n_kv_heads) / 16 + a->n_seqs + 1;
+}
 static int64_t mass8_queries_bytes(const wq_kv8_cache* c, const wq_kv4_rows* a) {
-  return a->n_rows * a->n_heads * c->head_dim * 2;
+  return c->n_kv_heads * mass8_col_tiles(c, a) * 32 * c->head_dim;
 }
 
 extern "C" int64_t wq_kv8_accumulate_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
@@ -806,7 +830,7 @@ extern "C" int64_t wq_kv8_accumulate_workspace(const wq_kv8_cache* cache, const 
   if (int e = check_attention8(cache, rows, max_rows, max_len, "wq_kv8_accumulate_workspace")) return e;
   wq::ok();
   if (rows->n_rows == 0 || rows->n_seqs == 0 || mass8_tiles(cache, rows, max_rows) < 3) return 0;
-  return (mass8_queries_bytes(cache, rows) + rows->n_rows * rows->n_heads * 8 + 15) / 16 * 16;
+  return mass8_queries_bytes(cache, rows) + cache->n_kv_heads * mass8_col_tiles(cache, rows) * 256;
 }
 
 extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
@@ -836,7 +860,9 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
   const int64_t at_once = 768, each = tiles < 3 ? kAttnWaves : kMass8Pages;
   int64_t groups = (pages + each - 1) / each;
   if (tiles < 3 && pairs * groups > 2 * at_once) groups = (2 * at_once + pairs - 1) / pairs;
-  if (pairs * groups > 0x7FFFFFFFll || items > 0x7FFFFF00ll)
+  const int64_t most_rows = max_rows > rows->n_rows ? rows->n_rows : max_rows;
+  const int64_t scalers = (most_rows * (rows->n_heads / cache->n_kv_heads) + 16 * kAttnWaves - 1) / (16 * kAttnWaves) + 1;
+  if (pairs * groups > 0x7FFFFFFFll || pairs * scalers > 0x7FFFFFFFll || items > 0x7FFFFF00ll)
     return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);
   Mass8Args p{};
   p.a = kv4_rows(rows);
@@ -854,7 +880,8 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
   p.mass = mass;
   p.mass_tokens = mass_tokens;
   p.queries = static_cast<h8*>(workspace);
-  p.columns = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + mass8_queries_bytes(cache, rows));
+  p.col_tiles = mass8_col_tiles(cache, rows);
+  p.columns = reinterpret_cast<f4*>(static_cast<uint8_t*>(workspace) + mass8_queries_bytes(cache, rows));
   const dim3 grid((unsigned)(pairs * groups));
   hipStream_t st = (hipStream_t)stream;
   kv4_dispatch(rows->dtype, cache->head_dim, [&](auto dt, auto d) {
@@ -864,7 +891,7 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
     } else if (tiles == 2) {
       mass8_few_kernel<DT, D, 2><<<grid, kAttnWaves * kWave, 0, st>>>(p);
     } else {
-      scale8_kernel<DT, D><<<dim3((unsigned)((items + 63) / 64)), 256, 0, st>>>(p, Divisor(rows->n_heads), items);
+      scale8_kernel<DT, D><<<dim3((unsigned)(pairs * scalers)), kAttnWaves * kWave, 0, st>>>(p);
       mass8_many_kernel<D><<<grid, kMass8Pages * kMass8Turns * kWave, 0, st>>>(p);
     }
   });
