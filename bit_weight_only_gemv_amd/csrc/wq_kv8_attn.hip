@@ -89,12 +89,25 @@ struct Keys8 {
   }
 };
 
+// The sequence of place n when they are ordered by length, longest first (of more than
+// 64 sequences: the n-th as they come).
+__device__ __forceinline__ int nth_longest(const KvRows& a, int n, int lane) {
+  if (a.seqs < 2 || a.seqs > kWave) return n;
+  const int len = lane < a.seqs ? a.lens[lane] : INT32_MIN;
+  int before = 0;
+  for (int i = 0; i < a.seqs; ++i) {
+    const int x = __builtin_amdgcn_readlane(len, i);
+    before += x > len || (x == len && i < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < a.seqs && before == n));
+}
+
 struct Attn8Args {
   KvRows a;
   const uint8_t* data;
   const uint32_t* exps;   // [page][head][2]
   int64_t n_pages;
-  Divisor kv_heads_by, group_by, pairs_by, splits_by;
+  Divisor kv_heads_by, group_by, parts_by, splits_by;
   int kv_heads, window, tiles, splits, split_pages;
   float scale;
   uint16_t* out;
@@ -112,13 +125,15 @@ __global__ void __launch_bounds__(NW * kWave, D == 256 ? 1 : 2) attn8_kernel(Att
   const int r = lane >> 4, l = lane & 15;
   const int R = (int)p.group_by.d;
 
-  // pairs (sequence, key/value head) vary fastest: workgroups that read the same
-  // pages are a multiple of the pairs apart and so, for 8 pairs and their multiples,
-  // on the same XCD; the last column tiles, which see the most tokens, come first
-  const int rest = p.pairs_by.div(blockIdx.x), pair = blockIdx.x - rest * p.pairs_by.d;
-  const int b = p.kv_heads_by.div(pair), kvh = pair - b * p.kv_heads;
-  const int turn = p.splits_by.div(rest), split = rest - turn * p.splits;
+  // Heads vary fastest: workgroups that read the same pages are a multiple of the heads
+  // apart and so, for 8 heads and their multiples, on the same XCD.  Long sequences
+  // come first, and of their column tiles the last, which see the most tokens: what
+  // starts late is short.
+  const int rest = p.kv_heads_by.div(blockIdx.x), kvh = blockIdx.x - rest * p.kv_heads;
+  const int place = p.parts_by.div(rest), part = rest - place * p.parts_by.d;
+  const int turn = p.splits_by.div(part), split = part - turn * p.splits;
   const int tile0 = p.tiles - 1 - turn;
+  const int b = nth_longest(a, place, lane);
   const int32_t* const table = a.table + (int64_t)b * a.width;
   // the wave's first page numbers, read at the same time as the lengths: where the
   // hints hold, a split starts here
@@ -240,10 +255,13 @@ __global__ void __launch_bounds__(NW * kWave, D == 256 ? 1 : 2) attn8_kernel(Att
 #pragma unroll
         for (int u = 0; u < 4; ++u) asm volatile("" : "+v"(sc[ct][u]));   // done here, not after the loads
       __builtin_amdgcn_sched_barrier(0);
-      next();
-      kt.load(src, lane);          // past the last page: that page's again, not used
-      load_exponents();
-      __builtin_amdgcn_sched_barrier(0);
+      auto next_keys = [&]() {
+        next();
+        kt.load(src, lane);        // past the last page: that page's again, not used
+        load_exponents();
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      if constexpr (CT == 1) next_keys();
 
       // base-2 logits and the values' exponent above the reference, plus kWeightExp
       float y[CT][16], top[CT];
@@ -309,15 +327,20 @@ __global__ void __launch_bounds__(NW * kWave, D == 256 ? 1 : 2) attn8_kernel(Att
           u4v wv, rv;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
+            // both parts cut, not rounded: the remainder takes what the first leaves, and
+            // the second's error is below 2^-21
             const float y0 = y[ct][8 * h + 2 * x], y1 = y[ct][8 * h + 2 * x + 1];
-            const h2 w = {(_Float16)y0, (_Float16)y1};
-            const h2 rest = {(_Float16)(y0 - (float)w[0]), (_Float16)(y1 - (float)w[1])};
+            const h2 w = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(y0, y1));
             wv[x] = as_u32(w);
-            rv[x] = as_u32(rest);
+            rv[x] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(y0 - (float)w[0], y1 - (float)w[1]));
           }
           wh[ct][h] = __builtin_bit_cast(h8, wv);
           wl[ct][h] = __builtin_bit_cast(h8, rv);
         }
+      }
+      if constexpr (CT > 1) {      // here, where the logits have left their registers
+        __builtin_amdgcn_sched_barrier(0);
+        next_keys();
       }
       unroll<J>([&](auto j) {
 #pragma unroll
@@ -782,7 +805,7 @@ extern "C" int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* ro
   p.kv_heads = (int)cache->n_kv_heads;
   p.kv_heads_by = Divisor(cache->n_kv_heads);
   p.group_by = Divisor(rows->n_heads / cache->n_kv_heads);
-  p.pairs_by = Divisor(plan.pairs);
+  p.parts_by = Divisor(plan.tiles * plan.splits);
   p.splits_by = Divisor(plan.splits);
   p.window = window > 0x40000000 ? 0 : (int)window;
   p.tiles = (int)plan.tiles;

@@ -29,13 +29,12 @@ def _f32(t, shape, what):
     raise ValueError(f"{what} must be a contiguous GPU tensor, float32 {list(shape)}: got {t.dtype} {list(t.shape)}")
 
 
-def _same_device(device, *tensors):
-    """All on `device`, which has to be the current one: the launches go there."""
+def _same_device(*tensors):
+    """All on the current device: the launches go there."""
+    now = L._current_device()
     for t in tensors:
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    if device.index is not None and device.index != L._current_device():
-        raise ValueError(f"tensors on {device}, which is not the current device")
+        if t.get_device() != now:
+            raise ValueError(f"a tensor on {t.device}, the current device is {now}")
 
 
 class KV8Cache:
@@ -47,13 +46,13 @@ class KV8Cache:
         if data.dtype != torch.uint8 or data.dim() != 3 or data.shape[2] % 128:
             raise ValueError("data must be uint8 [n_pages, n_kv_heads, 128 D]")
         self.data, self.exponents = data, exponents
-        self.n_pages, self.n_kv_heads, self.head_dim = data.shape[0], data.shape[1], data.shape[2] // 128
-        if exponents.dtype != torch.int8 or tuple(exponents.shape) != (self.n_pages, self.n_kv_heads, 8):
-            raise ValueError("exponents must be int8 [n_pages, n_kv_heads, 8]")
+        n, h, size = data.shape
+        self.n_pages, self.n_kv_heads, self.head_dim = n, h, size // 128
+        if exponents.dtype != torch.int8 or exponents.shape != (n, h, 8) or exponents.device != data.device:
+            raise ValueError("exponents must be int8 [n_pages, n_kv_heads, 8] beside the data")
         self._c = L.Kv8Cache(L._dptr(data), L._dptr(exponents), self.n_pages, self.n_kv_heads,
                              self.head_dim)
         self._ref = ctypes.addressof(self._c)
-        self._device = data.device
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> "KV8Cache":
@@ -71,7 +70,7 @@ class KV8Cache:
             raise ValueError(f"k and v must be {list(want)} of one type")
         kp, kr, kh = _strided(k, "k")
         vp, vr, vh = _strided(v, "v")
-        _same_device(self._device, k, v, slots, runs)
+        _same_device(self.data, k, v, slots, runs)
         L._check(fn(self._ref, _dtype(k), kp, kr, kh, vp, vr, vh, T, L._i32(slots, (T,), "slots"),
                     L._i32(runs, (runs.shape[0], 2), "runs"), runs.shape[0], L._stream(stream)))
 
@@ -85,12 +84,15 @@ class KV8Cache:
         softmax sums."""
         lib = L.load()
         a = self._rows(q, block_table, lens, cu_rows)
-        _same_device(self._device, q, block_table, lens, cu_rows)
+        _same_device(self.data, q, block_table, lens, cu_rows)
         if out is None:
             out = _new(q.shape, q.dtype, q.device, stream)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
+        elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != q.get_device():
             raise ValueError("out must have q's shape, type and device")
-        lp = None if lse is None else _f32(lse, q.shape[:2], "lse")
+        lp = None
+        if lse is not None:
+            lp = _f32(lse, q.shape[:2], "lse")
+            _same_device(lse)
         ar = ctypes.addressof(a)
         need = lib.wq_kv8_attention_workspace(self._ref, ar, max_rows, max_len)
         if need < 0:
@@ -111,7 +113,7 @@ class KV8Cache:
         others start from 0).  Returns mass."""
         lib = L.load()
         a = self._rows(q, block_table, lens, cu_rows)
-        _same_device(self._device, q, lse, block_table, lens, cu_rows, held, mass)
+        _same_device(self.data, q, lse, block_table, lens, cu_rows, held, mass)
         if mass.dim() != 3:
             raise ValueError("mass must be float32 [sequences, n_kv_heads, tokens]")
         mp = _f32(mass, (a.n_seqs, self.n_kv_heads, mass.shape[2]), "mass")
@@ -142,10 +144,10 @@ class KV8Cache:
         H, F = self.n_kv_heads, free_pages.numel()
         if mass.dim() != 3 or new_mass.dim() != 3:
             raise ValueError("masses must be float32 [sequences, n_kv_heads, tokens]")
-        _same_device(self._device, mass, block_table, lens, free_pages, new_table, new_lens, new_mass, taken)
+        _same_device(self.data, mass, block_table, lens, free_pages, new_table, new_lens, new_mass, taken)
         if kept is None:
             kept = _new((B, H, keep), torch.int32, mass.device, stream)
-        _same_device(self._device, kept)
+        _same_device(kept)
         L._check(lib.wq_kv8_evict(
             self._ref, _f32(mass, (B, H, mass.shape[2]), "mass"), mass.shape[2],
             L._i32(block_table, (B, width), "block_table"), width, L._i32(lens, (B,), "lens"), B, keep, recent,

@@ -13,25 +13,29 @@ from .kv4 import _dtype, _new, _strided
 from .kv8 import _same_device
 
 
+_NONE = L.Heads(None, None, None, 0, 0, 0, 0, 0)
+
+
 def _side(x, weight, out, stream, what):
     """wq_heads of one of the two, and its result."""
     if x is None:
         if weight is not None or out is not None:
             raise ValueError(f"{what} is missing, but not its weight or output")
-        return L.Heads(None, None, None, 0, 0, 0, 0, 0), None
+        return _NONE, None
     p, r, h = _strided(x, what)
     if out is None:
         out = _new(x.shape, x.dtype, x.device, stream)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{what}'s output must have its shape and type")
-    op, orow, ohead = _strided(out, what + "'s output")
+    op, orow, ohead = _strided(out, what)
     wp = None
     if weight is not None:
         if weight.shape != x.shape[2:] or weight.dtype != x.dtype:
             raise ValueError(f"{what}'s weight must be [{x.shape[2]}] of its type")
         wp = L._dptr(weight)
-        _same_device(x.device, weight)
-    _same_device(x.device, out)
+        _same_device(x, out, weight)
+    else:
+        _same_device(x, out)
     return L.Heads(p, op, wp, x.shape[1], r, h, orow, ohead), out
 
 
@@ -47,9 +51,9 @@ def wq_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
-    if q is not None and k is not None and (q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:] or
-                                            q.dtype != k.dtype or q.device != k.device):
-        raise ValueError("q and k must have the same rows, channels, type and device")
+    rows, _, channels = x.shape
+    if q is not None and k is not None and (rows != k.shape[0] or channels != k.shape[2] or q.dtype != k.dtype):
+        raise ValueError("q and k must have the same rows, channels and type")
     if eps is None:
         if q_weight is not None or k_weight is not None:
             raise ValueError("weights belong to the norm: eps is None")
@@ -63,8 +67,8 @@ def wq_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps
         n = inv_freq.numel()
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be float64 [n]")
-        pp, fp = L._i32(positions, (x.shape[0],), "positions"), L._dptr(inv_freq)
-        _same_device(x.device, positions, inv_freq)
-    L._check(fn(_dtype(x), ctypes.addressof(a), ctypes.addressof(b), x.shape[0], x.shape[2], eps, pp, fp, n,
+        pp, fp = L._i32(positions, (rows,), "positions"), L._dptr(inv_freq)
+        _same_device(positions, inv_freq)
+    L._check(fn(_dtype(x), ctypes.addressof(a), ctypes.addressof(b), rows, channels, eps, pp, fp, n,
                 bool(neighbours), L._stream(stream)))
     return q_out, k_out

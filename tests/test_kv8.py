@@ -210,7 +210,7 @@ def test_wrapper_checks():
         with pytest.raises(ValueError):                 # the last is not on the GPU
             B.KV8Cache(torch.zeros(*data, **u8), torch.zeros(*exps, **i8))
     c = object.__new__(B.KV8Cache)
-    c.n_kv_heads, c.head_dim, c._device = 2, 64, torch.device("cpu")
+    c.n_kv_heads, c.head_dim = 2, 64
     none, cu, table = torch.zeros(0, **i32), torch.zeros(1, **i32), torch.zeros(0, 4, **i32)
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
     with pytest.raises(ValueError, match="no sequences"):
