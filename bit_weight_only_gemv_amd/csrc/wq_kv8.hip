@@ -36,7 +36,12 @@ __device__ __forceinline__ uint32_t raise4(uint32_t w, int by) {
 // ----------------------------------------------------------------- append
 // One workgroup per (run, head, keys or values).  A thread takes 8 channels of a
 // token at a time; all of a page's loads are in flight before the first is used.
-constexpr int kAppend8Threads = 256;
+// Keys leave as 8 bytes a thread; values go through LDS, where a thread then gathers
+// 16 tokens of a channel.  Memory bounds prompts: 23145 tokens of 8 heads of 128
+// channels (142 MB) take 31 us, 28 as a plain copy of as many bytes.  Single tokens:
+// latency of run, slot, token and bytes in turn, with 256 of them 9.9 us in workgroups
+// of one wave and 11.4 in four.
+constexpr int kAppend8Threads = 256, kAppend8Few = 64;
 
 // 16-bit values past +-65504 (BF16: 65536, whose code is the same) and infinities
 // as that, NaN as 0.
@@ -77,11 +82,11 @@ __device__ __forceinline__ int exponent_of(float most) {
 }
 
 // FULL: the run is a whole page, so nothing is masked.
-template <int DT, int D, bool VALUES, bool FULL>
+template <int DT, int D, int NT, bool VALUES, bool FULL>
 __device__ __forceinline__ void append8_run(const uint16_t* __restrict__ src, int64_t row, int o,
                                             int count, uint8_t* __restrict__ page,
                                             uint8_t* __restrict__ exps, uint32_t* s_mem) {
-  constexpr int O = D / 8, TS = kAppend8Threads / O, IT = 64 / TS;
+  constexpr int O = D / 8, TS = NT / O, IT = 64 / TS;
   __shared__ uint32_t s_most[4];
   const int tid = threadIdx.x, oc = tid % O;
   u4v raw[IT];
@@ -96,8 +101,11 @@ __device__ __forceinline__ void append8_run(const uint16_t* __restrict__ src, in
   const int was = older ? min(max((int)(int8_t)exps[u0], kLeast8), kMost8) : kLeast8;
   if (tid < 4) s_most[tid] = 0;
   lds_barrier();
+  // turns without a token of the run are passed over
+  auto idle = [&](int it) { return !FULL && (it * TS + TS <= o || it * TS >= o + count); };
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
+    if (idle(it)) continue;
     uint32_t m = max_halves(max_halves(raw[it][0] & 0x7FFF7FFFu, raw[it][1] & 0x7FFF7FFFu),
                             max_halves(raw[it][2] & 0x7FFF7FFFu, raw[it][3] & 0x7FFF7FFFu));
     m = max(m & 0xFFFFu, m >> 16);
@@ -122,6 +130,7 @@ __device__ __forceinline__ void append8_run(const uint16_t* __restrict__ src, in
   };
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
+    if (idle(it)) continue;
     const int t = tid / O + it * TS;
     if (!FULL && (t < o || t >= o + count)) continue;
     const float by = pow2(-exponent(t / kBlock8));
@@ -142,7 +151,7 @@ __device__ __forceinline__ void append8_run(const uint16_t* __restrict__ src, in
     if (by > 0) {
       const int nt = o % kBlock8;
       uint32_t* const block = reinterpret_cast<uint32_t*>(page + u0 * (16 * D));
-      for (int c = tid; c < nt * (D / 4); c += kAppend8Threads) {
+      for (int c = tid; c < nt * (D / 4); c += NT) {
         const int x = c >> 2, l = x % nt, cr = x / nt;
         uint32_t* const at = block + cr * 64 + l * 4 + (c & 3);
         *at = raise4(*at, by);
@@ -153,7 +162,7 @@ __device__ __forceinline__ void append8_run(const uint16_t* __restrict__ src, in
   __syncthreads();
   // a thread: row r of the page's blocks, one channel: 4 bytes of each block, from LDS
   const uint8_t* const bytes = reinterpret_cast<const uint8_t*>(s_mem);
-  for (int c = tid; c < 4 * D; c += kAppend8Threads) {
+  for (int c = tid; c < 4 * D; c += NT) {
     const int d = c % D, r = c / D;
     uint32_t* const at = reinterpret_cast<uint32_t*>(page + 64 * D + ((d / 16 * 4 + r) * 16 + d % 16) * 16);
     u4v w;
@@ -182,8 +191,8 @@ __device__ __forceinline__ void append8_run(const uint16_t* __restrict__ src, in
   }
 }
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kAppend8Threads)
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(NT)
 append8_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
                const uint16_t* __restrict__ v, int64_t v_row, int64_t v_head, int T,
                const int32_t* __restrict__ slots, const int2* __restrict__ runs,
@@ -201,12 +210,12 @@ append8_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
   uint8_t* const ex = exps + ph * 8;
   if (values) {
     const uint16_t* const src = v + rc.x * v_row + head * v_head;
-    if (rc.y == 64) append8_run<DT, D, true, true>(src, v_row, 0, 64, page, ex + 4, s_mem);
-    else append8_run<DT, D, true, false>(src, v_row, o, rc.y, page, ex + 4, s_mem);
+    if (rc.y == 64) append8_run<DT, D, NT, true, true>(src, v_row, 0, 64, page, ex + 4, s_mem);
+    else append8_run<DT, D, NT, true, false>(src, v_row, o, rc.y, page, ex + 4, s_mem);
   } else {
     const uint16_t* const src = k + rc.x * k_row + head * k_head;
-    if (rc.y == 64) append8_run<DT, D, false, true>(src, k_row, 0, 64, page, ex, s_mem);
-    else append8_run<DT, D, false, false>(src, k_row, o, rc.y, page, ex, s_mem);
+    if (rc.y == 64) append8_run<DT, D, NT, false, true>(src, k_row, 0, 64, page, ex, s_mem);
+    else append8_run<DT, D, NT, false, false>(src, k_row, o, rc.y, page, ex, s_mem);
   }
 }
 
@@ -614,12 +623,18 @@ extern "C" int wq_kv8_append(const wq_kv8_cache* cache, int dtype, const uint16_
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements", who);
   const dim3 grid((unsigned)(n_runs * cache->n_kv_heads * 2));
   kv4_dispatch(dtype, cache->head_dim, [&](auto dt, auto d) {
-    append8_kernel<decltype(dt)::value, decltype(d)::value>
-        <<<grid, kAppend8Threads, 0, (hipStream_t)stream>>>(
-            k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, (int)n_rows, slots,
-            reinterpret_cast<const int2*>(runs), cache->data,
-            reinterpret_cast<uint8_t*>(cache->exponents), cache->n_pages, (int)cache->n_kv_heads,
-            Divisor(cache->n_kv_heads));
+    auto launch = [&](auto kernel, int threads) {
+      kernel<<<grid, threads, 0, (hipStream_t)stream>>>(
+          k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, (int)n_rows, slots,
+          reinterpret_cast<const int2*>(runs), cache->data,
+          reinterpret_cast<uint8_t*>(cache->exponents), cache->n_pages, (int)cache->n_kv_heads,
+          Divisor(cache->n_kv_heads));
+    };
+    // runs of less than four tokens on average: a wave each
+    if (n_rows < 4 * n_runs)
+      launch(append8_kernel<decltype(dt)::value, decltype(d)::value, kAppend8Few>, kAppend8Few);
+    else
+      launch(append8_kernel<decltype(dt)::value, decltype(d)::value, kAppend8Threads>, kAppend8Threads);
   });
   return check_launch(who);
 }

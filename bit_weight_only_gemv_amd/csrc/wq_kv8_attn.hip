@@ -878,11 +878,12 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
   const int tiles = mass8_tiles(cache, rows, max_rows);
   const int64_t pairs = rows->n_seqs * cache->n_kv_heads, items = rows->n_rows * rows->n_heads;
   const int64_t pages = max_len < 1 ? 1 : (max_len + 63) / 64;
-  // Few columns: three workgroups for every compute unit run at once; each wave has
-  // several pages where there are enough, so that its queries are made once.
-  const int64_t at_once = 768, each = tiles < 3 ? kAttnWaves : kMass8Pages;
+  // Few columns: a wave has several pages where there are enough, so that its queries are
+  // made once, but not so many that uneven lengths leave compute units idle (32 sequences of
+  // up to 8191 tokens, 8 heads: 42 us in up to 3072 workgroups, 46 in 768 to 1536 or 8192).
+  const int64_t each = tiles < 3 ? kAttnWaves : kMass8Pages, most = 3072;
   int64_t groups = (pages + each - 1) / each;
-  if (tiles < 3 && pairs * groups > 2 * at_once) groups = (2 * at_once + pairs - 1) / pairs;
+  if (tiles < 3 && pairs * groups > most) groups = (most + pairs - 1) / pairs;
   const int64_t most_rows = max_rows > rows->n_rows ? rows->n_rows : max_rows;
   const int64_t scalers = (most_rows * (rows->n_heads / cache->n_kv_heads) + 16 * kAttnWaves - 1) / (16 * kAttnWaves) + 1;
   if (pairs * groups > 0x7FFFFFFFll || pairs * scalers > 0x7FFFFFFFll || items > 0x7FFFFF00ll)

@@ -132,7 +132,8 @@ def attend(made, cache, rows, heads, dtype, seed=1, scale=None, window=0, label=
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("lens,new", [([0], [1]), ([63], [1]), ([64], [64]), ([5, 0, 31], [1, 130, 40]), ([47], [3]),
-                                      ([100, 7, 0], [0, 57, 64]), ([33], [31]), ([15, 17, 30], [1, 2, 20])])
+                                      ([100, 7, 0], [0, 57, 64]), ([33], [31]), ([15, 17, 30], [1, 2, 20]),
+                                      ([0, 60] + [7, 15, 16, 63] * 10, [64, 70] + [1, 2, 1, 3] * 10)])
 def test_append(D, dtype, lens, new):
     say("append", D, dtype, lens, new)
     H, t = 3, TYPES[dtype]
