@@ -236,10 +236,9 @@ struct Evict8Args {
   Divisor heads_by;
 };
 
-// Tokens of a sequence: those with a mass and a place in the table.
+// Tokens of a sequence: those with a place in the table.
 __device__ __forceinline__ int evict_len(const Evict8Args& p, int b) {
-  const int64_t most = min(p.mass_tokens, 64 * p.width);
-  return (int)min((int64_t)max(p.lens[b], 0), most);
+  return (int)min((int64_t)max(p.lens[b], 0), 64 * p.width);
 }
 
 // Order of a mass as an unsigned key: NaN lowest, -0 as 0.
@@ -304,7 +303,8 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   const int len = evict_len(p, b);
   const bool over = len > p.keep;
   const int64_t pair = (int64_t)b * p.heads + head;
-  const float* const mass = p.mass + pair * p.mass_tokens;
+  const float* const masses = p.mass + pair * p.mass_tokens;
+  auto mass_of = [&](int t) { return t < p.mass_tokens ? masses[t] : 0.f; };
   float* const new_mass = p.new_mass + pair * p.new_tokens;
   int32_t* const kept = p.kept + pair * p.keep;
   const int room = over ? p.keep - p.recent : 0, old = over ? len - p.recent : 0;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   for (int i = room + tid; i < p.keep; i += kPick8Threads) {
     const int t = old + (i - room);
     kept[i] = t < len ? t : -1;
-    if (t < len) new_mass[i] = mass[t];
+    if (t < len) new_mass[i] = mass_of(t);
   }
   if (room == 0) return;
   // every wave a stretch of the tokens, 64 at a time
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
 #pragma unroll
   for (int i = 0; i < kPick8Held; ++i) {
     const int t = t0 + i * kWave;
-    held[i] = i < turns && t < old ? mass[t] : 0.f;
+    held[i] = i < turns && t < old ? mass_of(t) : 0.f;
   }
   // f(mass, its key, token) of the stretch's tokens, all lanes together (a token past
   // the last: old or more)
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
       if (i < turns) f(held[i], mass_key(held[i]), t0 + i * kWave);
     for (int i = kPick8Held; i < turns; ++i) {
       const int t = t0 + i * kWave;
-      const float m = t < old ? mass[t] : 0.f;
+      const float m = t < old ? mass_of(t) : 0.f;
       f(m, mass_key(m), t);
     }
   };

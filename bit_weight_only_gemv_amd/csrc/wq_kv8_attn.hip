@@ -279,11 +279,14 @@ __global__ void __launch_bounds__(NW * kWave, D == 256 ? 1 : 2) attn8_kernel(Att
           for (int i = 0; i < 4; ++i) y[ct][4 * u + i] = __builtin_fmaf(sc[ct][u][i], c, d);
         }
         if (edge) {
-          asm volatile("");      // stays a branch: few pages have an edge
+          // stays a branch: few pages have an edge.  The distance of the column's position
+          // from the lane's first token
+          int rel = pos[ct] - t0 - 4 * r;
+          asm volatile("" : "+v"(rel));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int t = t0 + 16 * (i >> 2) + 4 * r + (i & 3);
-            if (t > pos[ct] || (p.window > 0 && t <= pos[ct] - p.window)) y[ct][i] = -INFINITY;
+            const int t = 16 * (i >> 2) + (i & 3);
+            if (t > rel || (p.window > 0 && t <= rel - p.window)) y[ct][i] = -INFINITY;
           }
         }
         top[ct] = -INFINITY;
@@ -332,7 +335,8 @@ __global__ void __launch_bounds__(NW * kWave, D == 256 ? 1 : 2) attn8_kernel(Att
             const float y0 = y[ct][8 * h + 2 * x], y1 = y[ct][8 * h + 2 * x + 1];
             const h2 w = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(y0, y1));
             wv[x] = as_u32(w);
-            rv[x] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(y0 - (float)w[0], y1 - (float)w[1]));
+            rv[x] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(
+                __builtin_fmaf((float)w[0], -1.f, y0), __builtin_fmaf((float)w[1], -1.f, y1)));
           }
           wh[ct][h] = __builtin_bit_cast(h8, wv);
           wl[ct][h] = __builtin_bit_cast(h8, rv);

@@ -207,6 +207,10 @@ extern "C" int wq_qk_norm_rope(int dtype, const wq_heads* q, const wq_heads* k, 
         ((n_rows > 1 && s->out_row_stride != s->row_stride) ||
          (s->n_heads > 1 && s->out_head_stride != s->head_stride)))
       return wq::fail(WQ_ERR_INVALID_ARG, "%s: in place, the output's strides must be the input's", who);
+  for (const wq_heads* s : {q, k})
+    if (s->n_heads && ((n_rows > 1 && s->out_row_stride < head_dim) ||
+                       (s->n_heads > 1 && s->out_head_stride < head_dim)))
+      return wq::fail(WQ_ERR_INVALID_ARG, "%s: the output's rows or heads overlap", who);
   const int64_t per = kRopeTurns * (512 / head_dim), chunks = (heads + per - 1) / per;
   const int64_t units = n_rows * chunks;
   if (units > 0x7FFFFFFFll) return wq::fail(WQ_ERR_UNSUPPORTED, "%s: too many rows", who);

@@ -67,6 +67,8 @@ def wq_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps
         n = inv_freq.numel()
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be float64 [n]")
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
         pp, fp = L._i32(positions, (rows,), "positions"), L._dptr(inv_freq)
         _same_device(positions, inv_freq)
     L._check(fn(_dtype(x), ctypes.addressof(a), ctypes.addressof(b), rows, channels, eps, pp, fp, n,

@@ -577,7 +577,8 @@ int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_
  *   new_mass     [n_seqs][n_kv_heads][new_tokens]: the kept tokens' masses; what lies
  *                behind them stays.  new_tokens >= keep
  * A block's exponent becomes the highest of those its tokens had.  Tokens past mass_tokens
- * or the table are not there; a kept token in a page outside the cache becomes zeros.
+ * have no mass (0), those past the table are not there; a kept token in a page outside the
+ * cache becomes zeros.
  * 1 <= keep <= 64 table_width, 0 <= recent <= keep, n_seqs <= WQ_KV4_MAX_SEQS.
  * Outputs must not overlap inputs, nor free_pages name a page that is in use. */
 int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_t mass_tokens,
@@ -593,13 +594,14 @@ int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_t mass_toke
  *   y_d = x_d / sqrt(mean x^2 + eps) weight_d
  *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position inv_freq[j]
  * for the n_freq pairs j: channels (j, n_freq + j), or with `neighbours` (2 j, 2 j + 1);
- * channels from 2 n_freq on are not rotated.  float32, rounded once; angles are held to
- * 2^-32 of a turn at any position.
+ * channels from 2 n_freq on are not rotated.  float32, rounded once; angles are good to
+ * 2^-31 of a turn for positions up to 2^20 either way and inv_freq up to 1 (to 2^-23
+ * for any position).
  * x and out are n_rows x n_heads x D with strides in elements, multiples of 8 (channels
  * are consecutive, pointers 16-byte aligned); out may be x with x's strides, and must not
- * overlap it otherwise.  weight [D] has the type of x; NULL: all 1.  eps < 0: no norm, and no
+ * overlap it otherwise (nor its own rows or heads each other).  weight [D] has the type of x; NULL: all 1.  eps < 0: no norm, and no
  * weight.  n_heads = 0 leaves queries or keys out.  positions int32 [n_rows], inv_freq
- * float64 [n_freq], a multiple of 4 up to D / 2 (0: no rotation, both may be NULL). */
+ * float64 [n_freq] (finite), a multiple of 4 up to D / 2 (0: no rotation, both may be NULL). */
 typedef struct wq_heads {
   const uint16_t* x;
   uint16_t* out;

@@ -147,13 +147,15 @@ def accumulate(data, exps, q, lse, table, lens, cu, held, mass, scale, window=0)
 
 def evict(data, exps, mass, table, lens, keep, recent, free, new_mass):
     """data and exps changed in place -> kept, new_table, new_lens, new_mass, taken."""
-    B, H, S = mass.shape
+    B, H, _ = mass.shape
     width, D = table.shape[1], data.shape[2] // 128
     kept, new_table, new_mass = np.full((B, H, keep), -1, np.int64), table.copy(), new_mass.copy()
     new_lens, taken, need = np.zeros(B, np.int64), 0, -(-keep // PAGE)
     source, source_exps = data.copy(), exps.copy()
+    # tokens past the masses have none
+    mass = np.concatenate([mass, np.zeros((B, H, max(0, PAGE * width - mass.shape[2])), mass.dtype)], -1)
     for b in range(B):
-        n = min(max(int(lens[b]), 0), S, PAGE * width)
+        n = min(max(int(lens[b]), 0), PAGE * width)
         new_lens[b] = min(n, keep)
         if n > keep:
             new_table[b] = -1

@@ -278,6 +278,21 @@ def test_attention_hints_do_not_change_what_is_seen():
                label=f"hints {max_rows} {max_len}")
 
 
+@pytest.mark.parametrize("n", [64, 65, 130])
+def test_many_sequences(n):
+    """Up to 64 sequences are taken by length, more as they come."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 300, n)
+    lens[3] = lens[5]
+    made = Made(lens, 2, 64, seed=n)
+    cache = made.gpu()
+    attend(made, cache, [1] * n, 4, torch.float16, label=f"{n} sequences")
+    rows = [int(rng.integers(0, 30)) for _ in range(n)]
+    attend(made, cache, rows, 4, torch.float16, label=f"{n} sequences of several rows")
+    weigh(made, cache, rows, 4, torch.float16, label=f"{n} sequences of several rows")
+    weigh(made, cache, [1] * n, 4, torch.float16, label=f"{n} sequences")
+
+
 def test_attention_extreme_logits_and_values():
     for q_scale, v_scale, spread in ((30.0, 1.0, 3.0), (1e-4, 1e-3, 1.0), (1.0, 8000.0, 1.0), (1000.0, 0.01, 30.0),
                                      (1.0, 1e-6, 1.0)):

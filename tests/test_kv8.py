@@ -171,6 +171,7 @@ def test_refuses_bad_rows(bad, status):
     (rope, dict(eps=float("nan"))), (rope, dict(q=heads(x=None))), (rope, dict(k=heads(out=None))),
     (rope, dict(q=heads(x=P + 2))), (rope, dict(q=heads(out=P + 8))), (rope, dict(k=heads(weight=P + 4))),
     (rope, dict(q=heads(row_stride=1020))), (rope, dict(q=heads(out_head_stride=4))), (rope, dict(k=heads(head_stride=-128))),
+    (rope, dict(q=heads(out_row_stride=0))), (rope, dict(k=heads(out_head_stride=0))), (rope, dict(k=heads(out_head_stride=64))),
     (rope, dict(q=heads(n_heads=-1))), (rope, dict(q=heads(n_heads=1 << 20))), (rope, dict(q=heads(out=P))),
 ])
 def test_refuses_bad_arguments(call, bad):
@@ -230,6 +231,6 @@ def test_rope_wrapper_checks():
     pos, f = torch.zeros(3, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
     for bad in (dict(q=None, k=None), dict(k=q[:2]), dict(k=q.bfloat16()), dict(k=q[..., :32]), dict(eps=-1.0),
                 dict(eps=float("nan")), dict(eps=None, q_weight=w), dict(k=None, k_weight=w), dict(q_weight=w[:32]),
-                dict(inv_freq=f.float())):
+                dict(inv_freq=f.float()), dict(positions=None)):
         with pytest.raises(ValueError):
             B.wq_qk_norm_rope(**{**dict(q=q, k=q, positions=pos, inv_freq=f), **bad})
