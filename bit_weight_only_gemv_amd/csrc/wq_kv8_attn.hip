@@ -22,6 +22,17 @@
 // pages are spared the cross-lane maximum and the rescale of the sums.  The
 // reference stays within 2^64 of the highest and f within [-24, 10], so that FP32
 // holds the sums.
+//
+// What bounds it (traced times).  One token a sequence over a long cache: the cache's
+// bytes.  Four sequences of 131072 tokens, 8 heads of 128 channels, 1074 MB: 185 us,
+// 5.8 TB/s, where a plain read reaches 5.6; a page costs a wave 483 vector and 48
+// matrix instructions, at two waves a SIMD.  32 sequences of up to 8191 tokens, 361 MB:
+// 74 us, the last of it with few workgroups at work (the longest sequences' splits).
+// Many rows: instructions of both kinds (617 vector and 96 matrix ones a page and wave
+// with two column tiles; without the remainders' products 91 us instead of 115, without
+// the conversions of codes 107, without the exponentials 104), and uneven sequences: 512
+// and fewer rows of two prompts over 6000 tokens take 107 us for 54 GFLOP.  Short caches:
+// latency, 7.6 us for 500 tokens.
 
 #include "wq_attn.cuh"
 #include "wq_common.cuh"
@@ -90,7 +101,8 @@ struct Keys8 {
 };
 
 // The sequence of place n when they are ordered by length, longest first (of more than
-// 64 sequences: the n-th as they come).
+// 64 sequences: the n-th as they come).  Two prompts of 267 and 458 rows over 6000 and
+// 3967 tokens take 112 us so, and 133 with both side by side.
 __device__ __forceinline__ int nth_longest(const KvRows& a, int n, int lane) {
   if (a.seqs < 2 || a.seqs > kWave) return n;
   const int len = lane < a.seqs ? a.lens[lane] : INT32_MIN;
@@ -431,16 +443,24 @@ static Attn8Plan attn8_plan(const wq_kv8_cache* c, const wq_kv4_rows* a, int64_t
   if (max_rows > a->n_rows) max_rows = a->n_rows;
   if (max_len > 64 * a->table_width) max_len = 64 * a->table_width;
   const int64_t cols = (max_rows < 1 ? 1 : max_rows) * R;
+  // Two column tiles share the codes' conversion where there are enough of them: a
+  // 512-token piece of two prompts over 6000 tokens takes 117 us with two, 174 with one,
+  // and 246 with four, whose registers spill.  Heads of 256 channels would not fit either.
   p.ct = c->head_dim <= 128 && cols >= 64 ? 2 : 1;
   p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
   p.pairs = a->n_seqs * c->n_kv_heads;
   int64_t pages = (max_len + 63) / 64;
   if (pages < 1) pages = 1;
+  // Two workgroups of 4 waves for every compute unit, as many as run at once (one with
+  // heads of 256 channels): finer splits cost more in parts to be joined than they even
+  // out (32 sequences of up to 8191 tokens: 77 us, in one and a half to three rounds 80 to
+  // 86).  A split has at least two pages a wave, one while that leaves compute units idle.
   const int64_t items = p.pairs * p.tiles, at_once = c->head_dim == 256 ? 256 : 512;
   int64_t splits = (at_once + items - 1) / items;
   const int64_t waves = items * ((pages + kAttnWaves - 1) / kAttnWaves) <= 256 ? kAttnWaves : 2 * kAttnWaves;
   const int64_t most = (pages + waves - 1) / waves;
   if (splits > most) splits = most;
+  // few pages for few workgroups: one workgroup of up to 8 waves, and no second launch
   p.waves = kAttnWaves;
   if (items <= 256 && pages <= 2 * kAttnMoreWaves) {
     splits = 1;
@@ -531,6 +551,8 @@ __device__ __forceinline__ void add_weights(f4 sc, float c, float lse, int t, in
 
 // Few columns (decoding): up to CT column tiles of queries stay in registers, every wave
 // takes pages of its own, the next page's keys under way behind this one's logits.
+// Bytes and latency: 32 sequences of up to 8191 tokens, 8 heads of 128 channels, 191 MB
+// in 42 us (4.5 TB/s; 55 with the queries made anew for every page).
 template <int DT, int D, int CT>
 __global__ void __launch_bounds__(kAttnWaves * kWave, 2) mass8_few_kernel(Mass8Args p) {
   constexpr int G = D / 32;
@@ -664,7 +686,10 @@ __global__ void __launch_bounds__(kAttnWaves * kWave) scale8_kernel(Mass8Args p)
 
 // Two pages a workgroup, two waves each: a page's keys stay in a wave's registers as
 // FP16 numbers while it goes through every second column tile, the next one's loads
-// ahead.
+// ahead.  Vector instructions bound it, 73 a tile and page, 16 of them exponentials,
+// beside 16 matrix ones: 267 and 458 rows over 6000 and 3967 tokens, 27 GFLOP, take 42 us
+// with the scaling (one page a workgroup 50, four waves a page 52, one wave a page 58 to
+// 68; with the columns' places found in the loop 76).
 constexpr int kMass8Pages = 2, kMass8Turns = 2;
 template <int D>
 __global__ void __launch_bounds__(kMass8Pages* kMass8Turns* kWave, 2) mass8_many_kernel(Mass8Args p) {

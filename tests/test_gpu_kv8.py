@@ -897,3 +897,60 @@ def test_tensors_of_another_device_are_refused():
         cache.attention(q, ints(made.table), ints([70]).cpu(), ints([0, 1]), 1, 70)
     with pytest.raises(ValueError):
         B.wq_qk_norm_rope(q, None, ints([0]).cpu(), inverse_frequencies(32))
+
+
+@pytest.mark.parametrize("keep", [0, 100])
+def test_example_block_in_8_bits(keep):
+    """The example's rotated decode steps, small, against the oracle, with evictions."""
+    import os
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import kv4_decode
+    D, H = 64, 2
+    block = kv4_decode.Block(3, 400, hidden=512, heads=8, kv_heads=H, dim=D, bits=8, rotate=True)
+    prompt = np.array([62, 200, 1])
+    kv = block.fill(prompt.tolist())
+    made = object.__new__(Made)
+    made.H, made.D, made.d, made.e = H, D, block.cache.data, block.cache.exponents
+    made.data, made.exps = np.zeros(made.d.shape, np.uint8), np.zeros(made.e.shape, np.int8)
+    free = torch.randperm(len(made.data), generator=torch.Generator().manual_seed(0)).numpy()
+    made.table, made.lens, slots, runs, taken = K4.plan(np.zeros(3, np.int64), sums(prompt), np.full(block.table.shape, -1), free)
+    free = np.roll(free, -taken)
+    K8.append(made.data, made.exps, f32(kv[0]), f32(kv[1]), slots, runs)
+    step, x, proj, att, y = block.stepper(0, keep > 0)
+    cu, at = np.arange(4), prompt.copy()
+    g = torch.Generator().manual_seed(1)
+    for i in range(5):
+        if keep and i in (1, 4):
+            mass = f32(block.mass)
+            block.evict(keep)
+            _, made.table, made.lens, want, _ = K8.evict(made.data, made.exps, mass, made.table, made.lens, keep, keep // 4, free,
+                                                         np.zeros_like(mass))
+            used = np.isin(free, made.table)
+            free = np.concatenate([free[~used], free[used]])
+            assert np.array_equal(f32(block.mass), want) and np.array_equal(host(block.free), free)
+        x.copy_(torch.randn(x.shape, generator=g).half().view(torch.int16))
+        step()
+        torch.cuda.synchronize()
+        q, k, v = block.split(proj)                    # rotated in place
+        held = made.lens
+        made.table, made.lens, slots, runs, taken = K4.plan(made.lens, cu, made.table, free)
+        free = np.roll(free, -taken)
+        at += 1
+        K8.append(made.data, made.exps, f32(k), f32(v), slots, runs)
+        assert made.same() and np.array_equal(host(block.lens), made.lens) and np.array_equal(host(block.table), made.table)
+        assert np.array_equal(host(block.at), at)
+        rms = f32(q).astype(np.float64).reshape(-1, D)
+        assert np.allclose((rms ** 2).mean(-1), 1, atol=2e-3)                # normed, and turned by no length
+        check_attention(att, block.lse, made, q, cu, D ** -0.5, label=f"example step {i}")
+        assert torch.isfinite(y.view(torch.float16).float()).all() and (y != 0).any()
+    if keep:
+        assert (made.lens <= keep + 1).all() and block.mass.isfinite().all() and (block.mass > 0).any()
+
+
+def test_example_runs(capsys):
+    import os
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import kv4_decode
+    kv4_decode.main(["--bits", "8", "--rotate", "--keep", "150", "--seqs", "3", "--prompt", "200", "--steps", "40"])
+    kv4_decode.main(["--rotate", "--seqs", "2", "--prompt", "100", "--steps", "4"])
+    assert capsys.readouterr().out.count("us a step") == 2
