@@ -25,7 +25,7 @@
 //
 // What bounds it (traced times).  One token a sequence over a long cache: the cache's
 // bytes.  Four sequences of 131072 tokens, 8 heads of 128 channels, 1074 MB: 185 us,
-// 5.8 TB/s, where a plain read reaches 5.6; a page costs a wave 483 vector and 48
+// 5.8 TB/s, where a plain read reaches 5.6; a page costs a wave 435 vector and 48
 // matrix instructions, at two waves a SIMD.  32 sequences of up to 8191 tokens, 361 MB:
 // 74 us, the last of it with few workgroups at work (the longest sequences' splits).
 // Many rows: instructions of both kinds (617 vector and 96 matrix ones a page and wave

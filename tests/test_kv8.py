@@ -195,6 +195,19 @@ def test_empty_calls_do_nothing():
     assert rope(q=heads(n_heads=0, x=None, out=None, weight=None), k=heads(n_heads=0, x=None, out=None, weight=None)) == 0
 
 
+def test_workspaces_are_needed_where_they_are_asked_for():
+    """Many rows: scaled queries; long sequences: parts of splits.  Sizes grow with both."""
+    many, few = rows(n_rows=50, n_heads=32, table_width=900), rows()
+    need = L.load().wq_kv8_accumulate_workspace(ref(cache()), ref(many), 50, 64)
+    assert need >= 50 * 32 * 128 * 2 and L.load().wq_kv8_accumulate_workspace(ref(cache()), ref(few), 1, 64) == 0
+    parts = L.load().wq_kv8_attention_workspace(ref(cache()), ref(many), 1, 64 * 900)
+    assert parts >= 50 * 32 * 128 * 4
+    for bad in (dict(ws=None), dict(ws_bytes=need - 1), dict(ws=P + 8)):
+        assert accumulate(a=many, max_rows=50, **bad) == L.WQ_ERR_INVALID_ARG
+    for bad in (dict(ws=None), dict(ws_bytes=parts - 1), dict(ws=P + 8)):
+        assert attend(a=many, max_len=64 * 900, **bad) == L.WQ_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("big", [1 << 31, 1 << 58, (1 << 63) - 1])
 def test_hints_beyond_the_call_count_as_its_size(big):
     a = rows(n_rows=50, n_heads=32, table_width=900)
