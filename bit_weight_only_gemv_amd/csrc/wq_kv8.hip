@@ -424,7 +424,7 @@ move8_kernel(Evict8Args p, Divisor pairs_by, uint8_t* __restrict__ data,
   __shared__ __attribute__((aligned(16))) int s_at[64];      // byte of a token's first value, pages in a row
   __shared__ __attribute__((aligned(16))) int s_by[2][64];   // what its exponents rise by
   __shared__ int64_t s_page[64];
-  __shared__ int s_pages, s_simple, s_rise;
+  __shared__ int s_pages, s_rise;
   const int tid = threadIdx.x;
   // pages of a pair (sequence, head) share source pages: for 8 pairs and their
   // multiples they are on one XCD
@@ -467,13 +467,10 @@ move8_kernel(Evict8Args p, Divisor pairs_by, uint8_t* __restrict__ data,
     const uint64_t firsts = __ballot(first);
     const int nth = __popcll(firsts & ((2ull << tid) - 1)) - 1;
     s_src[tid] = src;
-    // tokens past the last count as the first byte's, and are not written
-    s_at[tid] = tid >= n ? 0 : src < 0 ? -1 : nth * kBytes + ((s >> 2) & 3) * 256 + (s / 16) * 4 + (s & 3);
-    const bool simple = !__any(tid < n && src < 0) && __popcll(firsts) <= kPages;
+    s_at[tid] = src < 0 ? -1 : nth * kBytes + ((s >> 2) & 3) * 256 + (s / 16) * 4 + (s & 3);
     if (first) s_page[nth] = src < 0 ? -1 : src >> 6;
     if (tid == 0) {
       s_pages = __popcll(firsts);
-      s_simple = simple;
       s_rise = rise;
     }
   }
@@ -522,21 +519,6 @@ move8_kernel(Evict8Args p, Divisor pairs_by, uint8_t* __restrict__ data,
     for (int k = 0; k < kChunks; ++k) {
       const int c = tid + k * kMove8Threads, d = c % D, r = c / D;
       const int of = (d / 16) * 1024 + (d % 16) * 16;
-      if (s_simple) {                 // one round has them all
-        uint32_t v[16];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int4 at = *reinterpret_cast<const int4*>(&s_at[16 * u + 4 * r]);
-          v[4 * u] = s_values[at.x + of];
-          v[4 * u + 1] = s_values[at.y + of];
-          v[4 * u + 2] = s_values[at.z + of];
-          v[4 * u + 3] = s_values[at.w + of];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          w[k][u] = v[4 * u] | v[4 * u + 1] << 8 | v[4 * u + 2] << 16 | v[4 * u + 3] << 24;
-        continue;
-      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int4 at = *reinterpret_cast<const int4*>(&s_at[16 * u + 4 * r]);

@@ -839,6 +839,53 @@ def test_a_captured_step_serves_growing_sequences():
     assert int(lens.min()) == 75
 
 
+def test_a_captured_piece_of_a_prompt_and_an_eviction():
+    """Many rows (scaled queries, splits to be joined) and an eviction in one graph, with
+    workspaces of its own; every replay equals the eager calls on the same data."""
+    made = Made([900, 300], 2, 128, seed=5, extra=30)
+    cache, other = made.gpu(), made.gpu()
+    n, heads, keep = 60, 8, 200
+    q = torch.zeros(2 * n, heads, 128, dtype=torch.bfloat16, device="cuda")
+    table, lens, cu, held = ints(made.table), ints(made.lens), ints([0, n, 2 * n]), ints([0, 0])
+    free = ints(made.free)
+
+    def outputs():
+        return dict(out=torch.zeros_like(q), lse=torch.zeros(2 * n, heads, device="cuda"), mass=torch.zeros(2, 2, 960, device="cuda"),
+                    table=torch.zeros_like(table), lens=torch.zeros_like(lens), new=torch.zeros(2, 2, keep, device="cuda"),
+                    taken=ints([0]), kept=ints(np.zeros((2, 2, keep))))
+
+    def calls(c, o):
+        for max_rows in (1, n):                        # in splits, and all rows' columns together
+            c.attention(q, table, lens, cu, max_rows, 900, out=o["out"], lse=o["lse"])
+        c.accumulate(q, o["lse"], table, lens, cu, held, o["mass"], n, 900)
+        c.evict(o["mass"], table, lens, keep, 20, free, o["table"], o["lens"], o["new"], o["taken"], kept=o["kept"])
+
+    a, b = outputs(), outputs()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        calls(cache, a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(cache, a)
+    for i in range(4):
+        q.copy_(queries(2 * n, heads, 128, torch.bfloat16, seed=i))
+        graph.replay()
+        torch.cuda.synchronize()
+        calls(other, b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[k], b[k]) for k in a), i
+        assert torch.equal(cache.data, other.data) and torch.equal(cache.exponents, other.exponents), i
+        lens.sub_(1)
+        torch.rand(1 << 20, device="cuda").sum()
+
+
+def test_evict_of_many_sequences():
+    rng = np.random.default_rng(8)
+    made = Made(rng.integers(0, 200, 90), 1, 64, seed=2, extra=170)
+    check_evict(made, made.gpu(), masses((90, 1, 64 * made.table.shape[1]), 3), 70, 9, label="90 sequences")
+
+
 def test_calls_on_another_stream():
     """What such a call returns and uses is memory of its own stream."""
     made = Made([3000, 500], 2, 128, seed=1, extra=60)
