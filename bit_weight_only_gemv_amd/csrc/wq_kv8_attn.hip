@@ -909,8 +909,8 @@ extern "C" int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* r
   const int64_t pages = max_len < 1 ? 1 : (max_len + 63) / 64;
   // Few columns: a wave has several pages where there are enough, so that its queries are
   // made once, but not so many that uneven lengths leave compute units idle (32 sequences of
-  // up to 8191 tokens, 8 heads: 42 us in up to 3072 workgroups, 46 in 768 to 1536 or 8192).
-  const int64_t each = tiles < 3 ? kAttnWaves : kMass8Pages, most = 3072;
+  // up to 8191 tokens, 8 heads: 42 us in up to 12 workgroups a compute unit, 46 in 3, 6 or 32).
+  const int64_t each = tiles < 3 ? kAttnWaves : kMass8Pages, most = 12 * 256;
   int64_t groups = (pages + each - 1) / each;
   if (tiles < 3 && pairs * groups > most) groups = (most + pairs - 1) / pairs;
   const int64_t most_rows = max_rows > rows->n_rows ? rows->n_rows : max_rows;
