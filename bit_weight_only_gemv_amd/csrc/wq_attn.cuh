@@ -40,15 +40,18 @@ __device__ __forceinline__ float log_sum(float sum, float mx) {
 
 // Joins the splits of one (row, head): split s's weight is 2^(m_s - max m).  16
 // bytes a lane and D / 4 lanes a split, so that 1024 / D splits are read at a
-// time; their sums are added in order.
+// time; their sums are added in order.  With `cu` (then seqs + 1 entries, and the heads of a
+// row), rows outside the sequences' have no parts and stay as they are.
 template <int DT, int D>
 static __global__ void __launch_bounds__(kAttnWaves * kWave)
 join_kernel(const float* __restrict__ part, int64_t items, int splits, uint16_t* __restrict__ out,
-            float* __restrict__ lse) {
+            float* __restrict__ lse, const int32_t* __restrict__ cu = nullptr, int seqs = 0,
+            int heads = 0) {
   constexpr int L = D / 4, S = kAttnWaves * kWave / L;
   __shared__ f4 s_acc[S][L];
   __shared__ float s_sum[S][3];
   const int64_t at = blockIdx.x;
+  if (cu != nullptr && (at < (int64_t)cu[0] * heads || at >= (int64_t)cu[seqs] * heads)) return;
   const int x = threadIdx.x % L, y = threadIdx.x / L;
   const f4* ml = reinterpret_cast<const f4*>(part + items * splits * D) + at * splits;
   const f4* o = reinterpret_cast<const f4*>(part + at * splits * D) + x;

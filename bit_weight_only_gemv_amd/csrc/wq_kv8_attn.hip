@@ -864,7 +864,7 @@ extern "C" int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* ro
     }
     if (status == WQ_OK && plan.splits > 1)
       join_kernel<DT, D><<<dim3((unsigned)items), kAttnWaves * kWave, 0, (hipStream_t)stream>>>(
-          p.part, items, p.splits, out, lse);
+          p.part, items, p.splits, out, lse, rows->cu_rows, (int)rows->n_seqs, (int)rows->n_heads);
   });
   return status == WQ_OK ? check_launch(who) : status;
 }

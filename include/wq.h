@@ -536,7 +536,9 @@ int wq_kv8_append(const wq_kv8_cache* cache, int dtype, const uint16_t* k, int64
                   int64_t v_head_stride, int64_t n_rows, const int32_t* slots,
                   const int32_t* runs, int64_t n_runs, void* stream);
 
-/* Attention of the rows over the cache: wq_kv4_attention without a choice of pages. */
+/* Attention of the rows over the cache: wq_kv4_attention without a choice of pages.
+ * cu_rows may end before n_rows here and below (a padded batch): the rows behind the
+ * last sequence's take no part, and their out and lse stay as they are. */
 int64_t wq_kv8_attention_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
                                    int64_t max_rows, int64_t max_len);
 int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_t max_rows,
@@ -580,7 +582,7 @@ int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_
  * have no mass (0), those past the table are not there; a kept token in a page outside the
  * cache becomes zeros.
  * 1 <= keep <= 64 table_width, 0 <= recent <= keep, n_seqs <= WQ_KV4_MAX_SEQS.
- * Outputs must not overlap inputs, nor free_pages name a page that is in use. */
+ * Outputs must not overlap inputs, nor free_pages name a page that is in use or one twice. */
 int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_t mass_tokens,
                  const int32_t* block_table, int64_t table_width, const int32_t* lens,
                  int64_t n_seqs, int64_t keep, int64_t recent, const int32_t* free_pages,

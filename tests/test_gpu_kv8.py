@@ -388,6 +388,28 @@ def test_attention_batches_without_rows():
     cache.attention(q, torch.zeros(0, 4, dtype=torch.int32, device="cuda"), none, ints([0]), 0, 0)
 
 
+@pytest.mark.parametrize("lens,rows,pad", [([3000, 700], [1, 1], 3), ([2500, 90], [40, 90], 7), ([90], [1], 2), ([5000], [0], 4)])
+def test_padded_batches_leave_the_rows_behind_as_they_were(lens, rows, pad):
+    """cu_rows ends before the rows do, in one launch and in splits that are joined."""
+    made = Made(lens, 2, 64, seed=4)
+    cache = made.gpu()
+    n, cu = sum(rows), sums(rows)
+    q = queries(n + pad, 8, 64, torch.float16)
+    q[n:] = float("nan")
+    args = (ints(made.table), ints(made.lens), ints(cu))
+    for max_rows, max_len in ((max(max(rows), 1), max(lens)), (n + pad, 1 << 20), (1, 64)):
+        out, lse = torch.full_like(q, 3.0), torch.full((n + pad, 8), 5.0, device="cuda")
+        cache.attention(q, *args, max_rows, max_len, out=out, lse=lse)
+        torch.cuda.synchronize()
+        check_attention(out[:n], lse[:n], made, q[:n], cu, 0.125, label=f"padded {lens} {max_rows} {max_len}")
+        assert (out[n:] == 3).all() and (lse[n:] == 5).all()
+        lse[n:] = 1.0
+        before = torch.rand(len(lens), 2, 5056, generator=torch.Generator().manual_seed(1)).cuda()
+        mass, held = before.clone(), np.maximum(made.lens - np.asarray(rows), 0)
+        cache.accumulate(q, lse, *args, ints(held), mass, max_rows, max_len)
+        check_mass(made, q[:n], lse[:n], cu, held, host(before), mass, 0.125, label="padded masses")
+
+
 def test_any_cu_rows_and_lengths_stay_in_bounds():
     """Outputs are whatever they are; rows of no sequence stay as they were."""
     made = Made([100, 130], 2, 64, seed=3)
