@@ -224,7 +224,8 @@ append8_kernel(const uint16_t* __restrict__ k, int64_t k_row, int64_t k_head,
 
 constexpr int kPick8Threads = 1024, kPick8Waves = kPick8Threads / kWave;
 constexpr int kPick8Bins = 2048;
-constexpr int kPick8Held = 16;         // masses a thread holds; those of longer sequences are read again
+constexpr int kPick8Held = 16;         // masses a thread holds; those of longer sequences are read again,
+constexpr int kPick8Again = 8;         // so many at a time
 
 struct Evict8Args {
   const int32_t *table, *lens, *free_pages;
@@ -288,9 +289,11 @@ __device__ __forceinline__ void evict_tables(const Evict8Args& p, int b, uint32_
 // One workgroup a sequence for the tables, and one a (sequence, head) for the tokens:
 // the room-th highest key 11 bits at a time from histograms in LDS (four of them for
 // the first bits, which many masses share), then every wave a stretch of the tokens
-// with its place from the counts of the waves before it.  Masses stay in registers.
+// with its place from the counts of the waves before it.  Masses stay in registers, in
+// tables of up to 16384 tokens all of them; LONG: of any length.
 // Latency: 10 us for 4500 tokens, 15 for 16000 (22 with a read of the kept masses
 // behind the choice).
+template <bool LONG>
 __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   __shared__ uint32_t s_hist[6 * kPick8Bins];      // four of the first bits, one of the next each
   __shared__ uint32_t s_wave[kPick8Waves], s_count[kPick8Waves][2], s_found[2];
@@ -318,22 +321,26 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   // every wave a stretch of the tokens, 64 at a time
   const int turns = (old + kPick8Threads - 1) / kPick8Threads;
   const int t0 = wave * turns * kWave + lane;
+  auto load = [&](int i) {
+    const int t = t0 + i * kWave;
+    return i < turns && t < old ? mass_of(t) : 0.f;
+  };
   float held[kPick8Held];
 #pragma unroll
-  for (int i = 0; i < kPick8Held; ++i) {
-    const int t = t0 + i * kWave;
-    held[i] = i < turns && t < old ? mass_of(t) : 0.f;
-  }
+  for (int i = 0; i < kPick8Held; ++i) held[i] = load(i);
   // f(mass, its key, token) of the stretch's tokens, all lanes together (a token past
-  // the last: old or more)
+  // the last: old or more); those that are not held are read again, several at a time
   auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < kPick8Held; ++i)
       if (i < turns) f(held[i], mass_key(held[i]), t0 + i * kWave);
-    for (int i = kPick8Held; i < turns; ++i) {
-      const int t = t0 + i * kWave;
-      const float m = t < old ? mass_of(t) : 0.f;
-      f(m, mass_key(m), t);
+    for (int i0 = kPick8Held; LONG && i0 < turns; i0 += kPick8Again) {
+      float m[kPick8Again];
+#pragma unroll
+      for (int i = 0; i < kPick8Again; ++i) m[i] = load(i0 + i);
+#pragma unroll
+      for (int i = 0; i < kPick8Again; ++i)
+        if (i0 + i < turns) f(m[i], mass_key(m[i]), t0 + (i0 + i) * kWave);
     }
   };
   for (int i = tid; i < 6 * kPick8Bins; i += kPick8Threads) s_hist[i] = 0;
@@ -670,7 +677,11 @@ extern "C" int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_
   p.n_free = (int)n_free;
   p.pages = (int)pages;
   p.heads_by = Divisor(cache->n_kv_heads);
-  pick8_kernel<<<dim3((unsigned)(n_seqs + pairs)), kPick8Threads, 0, (hipStream_t)stream>>>(p);
+  const dim3 picks((unsigned)(n_seqs + pairs));
+  if (64 * table_width <= kPick8Held * kPick8Threads)
+    pick8_kernel<false><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
+  else
+    pick8_kernel<true><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
   uint8_t* const exps = reinterpret_cast<uint8_t*>(cache->exponents);
   const dim3 grid((unsigned)(pairs * pages));
   const Divisor pairs_by(pairs);

@@ -591,6 +591,11 @@ def test_evict_of_long_sequences():
     made = Made([9000, 4000], 1, 64, seed=3, extra=100)
     mass = masses((2, 1, 9000), 1)
     check_evict(made, made.gpu(), mass, 3001, 17, label="long")
+    # past what the threads hold (16384), by one turn and by several of eight
+    for n, keep in ((16500, 16420), (27000, 1500)):
+        made = Made([n, 300], 1, 64, seed=3, extra=300)
+        mass = masses((2, 1, 64 * made.table.shape[1]), 2, ties=n == 27000)
+        check_evict(made, made.gpu(), mass, keep, 17, label="longer")
 
 
 def test_evict_moves_blocks_of_different_exponents():
