@@ -291,8 +291,9 @@ __device__ __forceinline__ void evict_tables(const Evict8Args& p, int b, uint32_
 // the first bits, which many masses share), then every wave a stretch of the tokens
 // with its place from the counts of the waves before it.  Masses stay in registers, in
 // tables of up to 16384 tokens all of them; LONG: of any length.
-// Latency: 10 us for 4500 tokens, 15 for 16000 (22 with a read of the kept masses
-// behind the choice).
+// Latency: 11 us for 4500 tokens, 18 for 16000 (22 and more with a read of the kept
+// masses behind the choice); of 131072 tokens 16384 are chosen and moved in 195 us, 237
+// with the masses that are not held read one at a time.
 template <bool LONG>
 __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   __shared__ uint32_t s_hist[6 * kPick8Bins];      // four of the first bits, one of the next each
@@ -321,9 +322,12 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   // every wave a stretch of the tokens, 64 at a time
   const int turns = (old + kPick8Threads - 1) / kPick8Threads;
   const int t0 = wave * turns * kWave + lane;
+  // without a branch, so that no load waits for another
+  const int have = (int)min((int64_t)old, p.mass_tokens);
   auto load = [&](int i) {
     const int t = t0 + i * kWave;
-    return i < turns && t < old ? mass_of(t) : 0.f;
+    const float m = masses[min(t, have - 1)];
+    return t < have ? m : 0.f;
   };
   float held[kPick8Held];
 #pragma unroll
