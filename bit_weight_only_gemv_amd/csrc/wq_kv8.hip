@@ -286,6 +286,9 @@ __device__ __forceinline__ void evict_tables(const Evict8Args& p, int b, uint32_
   }
 }
 
+// A batch without sequences takes no pages.
+__global__ void none_taken_kernel(int32_t* taken) { taken[0] = 0; }
+
 // One workgroup a sequence for the tables, and one a (sequence, head) for the tokens:
 // the room-th highest key 11 bits at a time from histograms in LDS (four of them for
 // the first bits, which many masses share), then every wave a stretch of the tokens
@@ -658,7 +661,10 @@ extern "C" int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_
   if (!aligned4(mass) || !aligned4(block_table) || !aligned4(lens) || !aligned4(free_pages) ||
       !aligned4(new_table) || !aligned4(new_lens) || !aligned4(new_mass) || !aligned4(kept))
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: misaligned device pointer", who);
-  if (n_seqs == 0) return wq::ok();
+  if (n_seqs == 0) {
+    none_taken_kernel<<<dim3(1), 1, 0, (hipStream_t)stream>>>(taken);
+    return check_launch(who);
+  }
   if (new_table == block_table || new_mass == mass || new_lens == lens)
     return wq::fail(WQ_ERR_INVALID_ARG, "%s: the new table, lengths and masses need memory of their own", who);
   Evict8Args p{};

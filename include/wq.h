@@ -576,6 +576,7 @@ int wq_kv8_accumulate(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_
  *                ceil(keep / 64) entries of free_pages, sequences in order, then -1
  *   taken[0]     pages taken; more than n_free means that some were missing: their entries
  *                are -1 and their tokens not written.  The old table still holds all.
+                0 without sequences, which write nothing else
  *   new_mass     [n_seqs][n_kv_heads][new_tokens]: the kept tokens' masses; what lies
  *                behind them stays.  new_tokens >= keep
  * A block's exponent becomes the highest of those its tokens had.  Tokens past mass_tokens

@@ -639,6 +639,32 @@ def test_evict_of_nothing():
     assert kept.shape == (0, 1, 5)
 
 
+def test_evict_of_no_sequences_takes_no_pages():
+    """Fixed buffers of a step that has no sequences left: the last step's pages are not
+    taken again, eagerly or in a graph, by calls with and without free pages."""
+    cache = Made([70], 1, 64).gpu()
+    before = cache.data.clone(), cache.exponents.clone()
+    none, taken = torch.zeros(0, dtype=torch.int32, device="cuda"), ints([77])
+    masses_ = torch.zeros(0, 1, 64, device="cuda"), torch.zeros(0, 1, 5, device="cuda")
+    table, new_table, new_lens = none.view(0, 2), none.view(0, 2).clone(), none.clone()
+    frees = [none, ints([1, 2])]
+
+    def call(free):
+        return cache.evict(masses_[0], table, none, 5, 1, free, new_table, new_lens, masses_[1], taken)
+
+    for free in frees:
+        taken.fill_(77)
+        assert call(free).shape == (0, 1, 5) and int(taken) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(frees[1])
+    for i in range(3):
+        taken.fill_(5 + i)
+        graph.replay()
+        assert int(taken) == 0
+    assert torch.equal(cache.data, before[0]) and torch.equal(cache.exponents, before[1])
+
+
 # ------------------------------------------------------------------ rope
 
 

@@ -195,6 +195,11 @@ def test_empty_calls_do_nothing():
     assert rope(q=heads(n_heads=0, x=None, out=None, weight=None), k=heads(n_heads=0, x=None, out=None, weight=None)) == 0
 
 
+def test_evict_of_no_sequences_needs_no_tables_but_taken():
+    none = dict(B_=0, mass=None, table=None, lens=None, free=None, n_free=0, new_table=None, new_lens=None, new_mass=None, kept=None)
+    assert evict(**none, taken=None) == evict(**none, taken=P + 2) == L.WQ_ERR_INVALID_ARG
+
+
 def test_workspaces_are_needed_where_they_are_asked_for():
     """Many rows: scaled queries; long sequences: parts of splits.  Sizes grow with both."""
     many, few = rows(n_rows=50, n_heads=32, table_width=900), rows()
