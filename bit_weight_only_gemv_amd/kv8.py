@@ -37,6 +37,17 @@ def _same_device(*tensors):
             raise ValueError(f"a tensor on {t.device}, the current device is {now}")
 
 
+def _zeros(n, device, stream):
+    """n int32 zeros that only a call on `stream` uses."""
+    import torch
+    if stream is None:
+        return torch.zeros(n, dtype=torch.int32, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(n, dtype=torch.int32, device=device)
+
+
 class KV8Cache:
     """data uint8 [n_pages, n_kv_heads, 128 D] and exponents int8 [n_pages,
     n_kv_heads, 8], as plain device buffers."""
@@ -110,13 +121,20 @@ class KV8Cache:
         """Adds to mass float32 [sequences, n_kv_heads, tokens] the softmax weights that
         the rows and heads give each cached token; lse is attention's for the same
         arguments, held int32 [sequences] how many tokens have a mass already (the
-        others start from 0).  Returns mass."""
+        others start from 0, also where there are no rows).  Returns mass."""
         lib = L.load()
         a = self._rows(q, block_table, lens, cu_rows)
         _same_device(self.data, q, lse, block_table, lens, cu_rows, held, mass)
         if mass.dim() != 3:
             raise ValueError("mass must be float32 [sequences, n_kv_heads, tokens]")
         mp = _f32(mass, (a.n_seqs, self.n_kv_heads, mass.shape[2]), "mass")
+        lp = _f32(lse, (a.n_rows, a.n_heads), "lse")
+        if not a.n_rows and a.n_seqs:
+            # no rows: the call does nothing, and a padded batch of one row behind the last
+            # sequence, which is never read, starts the new tokens' masses
+            none = _zeros(max(a.n_seqs + 1, 4), q.device, stream)
+            lp = a.q = a.cu_rows = none.data_ptr()
+            a.n_rows, a.q_row_stride, a.q_head_stride, workspace = 1, 0, 0, None
         ar = ctypes.addressof(a)
         need = lib.wq_kv8_accumulate_workspace(self._ref, ar, max_rows, max_len)
         if need < 0:
@@ -124,10 +142,9 @@ class KV8Cache:
         if workspace is None and need:
             workspace = _workspace(need, q.device, stream)
         L._check(lib.wq_kv8_accumulate(
-            self._ref, ar, max_rows, max_len, _f32(lse, (a.n_rows, a.n_heads), "lse"),
-            self.head_dim ** -0.5 if scale is None else scale, window, L._i32(held, (a.n_seqs,), "held"),
-            mp, mass.shape[2], L._dptr(workspace), 0 if workspace is None else workspace.numel(),
-            L._stream(stream)))
+            self._ref, ar, max_rows, max_len, lp, self.head_dim ** -0.5 if scale is None else scale, window,
+            L._i32(held, (a.n_seqs,), "held"), mp, mass.shape[2], L._dptr(workspace),
+            0 if workspace is None else workspace.numel(), L._stream(stream)))
         return mass
 
     def evict(self, mass, block_table, lens, keep, recent, free_pages, new_table, new_lens, new_mass,

@@ -555,6 +555,9 @@ int wq_kv8_attention(const wq_kv8_cache* cache, const wq_kv4_rows* rows, int64_t
  * whose lse is not finite takes no part.  held int32 [n_seqs]: how many tokens have a
  * mass already (0 for a new sequence; the length before the new tokens, where every
  * step is counted).  Logits and sums are float32, in a fixed order.
+ * A call with n_rows = 0 does nothing, so what lies from held on is not started either; a
+ * step whose sequences have no rows starts it as a padded batch, n_rows at least 1 and cu_rows
+ * all 0, of which no q or lse is read.
  * workspace: wq_kv8_accumulate_workspace bytes for the same arguments, 16-byte
  * aligned (NULL where that is 0). */
 int64_t wq_kv8_accumulate_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,

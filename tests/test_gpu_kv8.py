@@ -536,6 +536,45 @@ def test_accumulate_sums_to_the_rows_and_repeats():
         assert torch.equal(a, weigh(made, cache, rows, 8, torch.float16, held=[0, 0])[2])
 
 
+@pytest.mark.parametrize("heads", [4, 80])
+@pytest.mark.parametrize("window", [0, 100])
+def test_accumulate_without_rows_starts_the_new_tokens(heads, window):
+    """Sums over no rows are 0: tokens from `held` on start at that, whatever the buffer held, and
+    the others keep their masses; with any hints, a workspace of any size, on another stream and in a graph."""
+    made = Made([333, 64, 0, 130], 2, 64, seed=3)
+    cache, held = made.gpu(), np.array([100, 64, 0, -3])
+    args = (ints(made.table), ints(made.lens), ints(np.zeros(5)), ints(held))
+    q = torch.zeros(0, heads, 64, dtype=torch.float16, device="cuda")
+    lse = torch.zeros(0, heads, device="cuda")
+    before = torch.rand(4, 2, 400, generator=torch.Generator().manual_seed(1)).cuda()
+    before[0, 0, 150:170], before[3, 1, 5] = float("nan"), float("inf")
+    want, t = before.clone(), np.arange(400)
+    for b, n in enumerate(made.lens):
+        want[b][:, torch.from_numpy((t >= held[b]) & (t < n)).cuda()] = 0
+
+    def call(mass, hints=(0, 333), **kw):
+        return cache.accumulate(q, lse, *args, mass, *hints, window=window, **kw)
+
+    side = torch.cuda.Stream()
+    for hints in ((0, 0), (0, 333), (1, 1 << 20), (50, 64)):
+        for kw in (dict(), dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), dict(stream=side),
+                   dict(stream=side.cuda_stream)):
+            mass = before.clone()
+            torch.cuda.synchronize()
+            assert call(mass, hints, **kw) is mass
+            torch.cuda.synchronize()
+            assert torch.equal(mass.nan_to_num(7.0), want.nan_to_num(7.0)), (hints, kw)
+    graph, mass = torch.cuda.CUDAGraph(), before.clone()
+    with torch.cuda.graph(graph):
+        call(mass)
+    for _ in range(3):
+        mass.copy_(before)
+        graph.replay()
+        torch.rand(1 << 18, device="cuda").sum()
+        torch.cuda.synchronize()
+        assert torch.equal(mass.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
 # ----------------------------------------------------------------- evict
 
 
