@@ -108,7 +108,9 @@ class KV8Cache:
         need = lib.wq_kv8_attention_workspace(self._ref, ar, max_rows, max_len)
         if need < 0:
             L._check(need)
-        if workspace is None and need:
+        if workspace is not None:
+            _same_device(workspace)
+        elif need:
             workspace = _workspace(need, q.device, stream)
         L._check(lib.wq_kv8_attention(
             self._ref, ar, max_rows, max_len, self.head_dim ** -0.5 if scale is None else scale, window,
@@ -139,7 +141,9 @@ class KV8Cache:
         need = lib.wq_kv8_accumulate_workspace(self._ref, ar, max_rows, max_len)
         if need < 0:
             L._check(need)
-        if workspace is None and need:
+        if workspace is not None:
+            _same_device(workspace)
+        elif need:
             workspace = _workspace(need, q.device, stream)
         L._check(lib.wq_kv8_accumulate(
             self._ref, ar, max_rows, max_len, lp, self.head_dim ** -0.5 if scale is None else scale, window,

@@ -243,6 +243,44 @@ def test_wrapper_checks():
                 torch.zeros(2, 2, 5), cu)
 
 
+def test_workspaces_of_another_device_are_refused(monkeypatch):
+    """Before the library sees them: a launch would write there."""
+    torch = pytest.importorskip("torch")
+
+    class OnGpu:
+        """What the wrappers ask of a contiguous tensor on GPU `at`."""
+        is_cuda, device = True, "cuda"
+
+        def __init__(self, shape, dtype, at=0):
+            self.shape, self.dtype, self.at = torch.Size(shape), dtype, at
+
+        def __getattr__(self, name):
+            if name.startswith("__"):
+                raise AttributeError(name)
+            t = torch.empty(self.shape, dtype=self.dtype, device="meta")
+            return dict(get_device=lambda: self.at, data_ptr=lambda: P).get(name, getattr(t, name))
+
+    L.load()
+    monkeypatch.setattr(L, "_current_device", lambda: 0)
+    monkeypatch.setattr(L, "_raw_stream", lambda device: 0)
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    c = object.__new__(B.KV8Cache)
+    c.n_kv_heads, c.head_dim, c.data = 2, 128, OnGpu((10, 2, 128 * 128), u8)
+    c._c = cache()
+    c._ref = ctypes.addressof(c._c)
+    q, table, lens, cu = OnGpu((50, 32, 128), torch.float16), OnGpu((1, 900), i32), OnGpu((1,), i32), OnGpu((2,), i32)
+    far, size = OnGpu((1 << 40,), u8, at=1), 64 * 900
+    with pytest.raises(ValueError, match="device"):
+        c.attention(q, table, lens, cu, 1, size, out=OnGpu(q.shape, torch.float16), workspace=far)
+    with pytest.raises(ValueError, match="device"):
+        c.accumulate(q, OnGpu((50, 32), f32), table, lens, cu, lens, OnGpu((1, 2, size), f32), 50, size, workspace=far)
+    near = OnGpu((16,), u8)                         # of this one: it gets to the library, and is too small
+    with pytest.raises(B.WQError, match="workspace of 16 bytes"):
+        c.attention(q, table, lens, cu, 1, size, out=OnGpu(q.shape, torch.float16), workspace=near)
+    with pytest.raises(B.WQError, match="workspace of 16 bytes"):
+        c.accumulate(q, OnGpu((50, 32), f32), table, lens, cu, lens, OnGpu((1, 2, size), f32), 50, size, workspace=near)
+
+
 def test_rope_wrapper_checks():
     torch = pytest.importorskip("torch")
     q, w = torch.zeros(3, 4, 64, dtype=torch.float16), torch.zeros(64, dtype=torch.float16)
