@@ -789,6 +789,29 @@ def test_norm_rope_in_place_and_strided():
         B.wq_qk_norm_rope(y[:, :8], None, pos, f, q_out=y.view(-1)[:5 * 8 * 128].view(5, 8, 128))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 2.0 ** -100, 1e-6, 2.0 ** 100])
+def test_norm_rope_of_bf16_heads_of_any_size(D, eps):
+    """Squares past float32's range, both ways: heads of 2^-133 to 2^127 beside ordinary ones,
+    single large channels among small ones.  Scaling by powers of two adds no rounding."""
+    g = torch.Generator().manual_seed(D)
+    size = torch.tensor([-126, -100, -75, -64, -45, -30, 0, 30, 59, 63, 64, 100, 124], dtype=torch.float64)
+    x = torch.randn(5, len(size), D, generator=g).double().clamp(-7, 7) * torch.exp2(size)[:, None]
+    x[1, :, 3] *= 2.0 ** 20
+    x[2, :, 5:] *= 2.0 ** -40
+    x = x.clamp(-3e38, 3e38).bfloat16().cuda()
+    x[3, :, :] = x[3, :, :1]
+    x[4, :, 1:] = 0
+    w = (1 + 0.3 * torch.randn(D, generator=g)).bfloat16().cuda()
+    pos, f = torch.arange(5, dtype=torch.int32) * 77, inverse_frequencies(D // 2)
+    for neighbours in (False, True):
+        a, _ = B.wq_qk_norm_rope(x, None, pos.cuda(), f, w, eps=eps, neighbours=neighbours)
+        check_rope(x, a, w, pos.numpy(), f, eps, neighbours, f"{D} {eps} {neighbours}")
+        for h in range(len(size)):                  # and each beside no other
+            b, _ = B.wq_qk_norm_rope(x[:, h:h + 1], None, pos.cuda(), f, w, eps=eps, neighbours=neighbours)
+            assert torch.equal(b[:, 0], a[:, h])
+
+
 def test_norm_rope_nan_stays_in_its_head():
     x = torch.randn(3, 9, 64, generator=torch.Generator().manual_seed(1)).half().cuda()
     pos, f = ints([1, 2, 3]), inverse_frequencies(32)
