@@ -12,7 +12,8 @@
 // of a turn and multiplied with the position in whole numbers modulo 2^64: no bit
 // is lost however far the position (a float32 product is off by 0.004 at position
 // 131072).  Sine and cosine are then their Taylor sums over an eighth of a turn
-// each way (to x^9 and x^10: off by less than 2 10^-9 and 2 10^-10).
+// each way (to x^9 and x^10: off by less than 2 10^-9 and 2 10^-10), in float32: the
+// angle there is good to 2^-26 of a turn, the sums to 2^-23.
 //
 // Memory bounds prompts: 8190 rows of 40 heads of 128 channels (168 MB) take 38 us, a
 // plain copy of them 33.  One row: 4.5 us, latency.

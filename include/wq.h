@@ -600,14 +600,15 @@ int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_t mass_toke
  *   y_d = x_d / sqrt(mean x^2 + eps) weight_d
  *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position inv_freq[j]
  * for the n_freq pairs j: channels (j, n_freq + j), or with `neighbours` (2 j, 2 j + 1);
- * channels from 2 n_freq on are not rotated.  float32, rounded once; angles are good to
- * 2^-31 of a turn for positions up to 2^20 either way and inv_freq up to 1 (to 2^-23
- * for any position).
+ * channels from 2 n_freq on are not rotated.  float32, rounded once; for positions up to
+ * 2^20 either way and inv_freq up to 1, angles are good to 2^-26 of a turn and their sines and
+ * cosines to 2^-23, as float32 holds them (angles of any position to 2^-23 of a turn).
  * x and out are n_rows x n_heads x D with strides in elements, multiples of 8 (channels
  * are consecutive, pointers 16-byte aligned); out may be x with x's strides, and must not
- * overlap it otherwise (nor its own rows or heads each other).  weight [D] has the type of x; NULL: all 1.  eps < 0: no norm, and no
- * weight.  n_heads = 0 leaves queries or keys out.  positions int32 [n_rows], inv_freq
- * float64 [n_freq] (finite), a multiple of 4 up to D / 2 (0: no rotation, both may be NULL). */
+ * overlap it otherwise (nor its own rows or heads each other).  weight [D] has the type
+ * of x; NULL: all 1.  eps < 0: no norm, and no weight.  n_heads = 0 leaves queries or keys
+ * out.  positions int32 [n_rows], inv_freq float64 [n_freq] (finite), a multiple of 4 up to
+ * D / 2 (0: no rotation, both may be NULL). */
 typedef struct wq_heads {
   const uint16_t* x;
   uint16_t* out;

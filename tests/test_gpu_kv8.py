@@ -771,6 +771,27 @@ def test_norm_rope_of_far_positions():
     assert torch.equal(a[:7], x[:7, :, :64]) and torch.equal(a[7, :, :8], -x[7, :, :8])
 
 
+@pytest.mark.parametrize("neighbours", [False, True])
+def test_norm_rope_sines_and_cosines_are_good_to_their_bound(neighbours):
+    """At an eighth of a turn the cosine and sine of a pair of ones cancel, and what is left shows their
+    errors: 2^-23 each for positions up to 2^20 and inv_freq up to 1, and the rounding to FP16
+    (subnormal here: 2^-25)."""
+    rng = np.random.default_rng(7)
+    x = torch.ones(1, 1, 64, dtype=torch.float16, device="cuda")
+    worst = 0.0
+    for pos in (1 << 20, -(1 << 20), 999983, -524287, 131071, 65537, -4099, 1021, 33):
+        whole = rng.integers(0, int(abs(pos) / (2 * np.pi)), 32)
+        f = 2 * np.pi * (whole + 0.125 + rng.uniform(-1, 1, 32) * 2.0 ** -18) / abs(pos)
+        assert f.max() <= 1
+        a, _ = B.wq_qk_norm_rope(x, None, ints([pos]), torch.from_numpy(f).cuda(), eps=None, neighbours=neighbours)
+        ref = K8.norm_rope(np.ones((1, 1, 64)), None, [pos], f, None, neighbours)[0]
+        off = np.abs(host(a) - ref)
+        tol = 2.0 ** -22 + np.maximum(2.0 ** -25, 2.0 ** -11 * np.abs(ref))
+        worst = max(worst, float((off / tol).max()))
+    say(f"  sines and cosines: worst |err|/bound = {worst:.4f}")
+    assert worst <= 1
+
+
 def test_norm_rope_in_place_and_strided():
     x = torch.randn(5, 12, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
     w, f = torch.rand(128, generator=torch.Generator().manual_seed(2)).bfloat16().cuda(), inverse_frequencies(64)
