@@ -301,6 +301,62 @@ def test_attention_extreme_logits_and_values():
             attend(made, made.gpu(), [1, 2], 4, dtype, q_scale=q_scale, label=f"q {q_scale} v {v_scale} k {spread}")
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [[1, 1], [3, 50]])
+def test_attention_of_logits_that_are_large_and_exact(D, dtype, rows):
+    """Logits of up to 2^16 that float32 sums hold exactly: whole queries and keys, a scale that is a
+    power of two.  In every sequence tokens far apart share the highest logit, in pages of lower and of
+    higher ones than before, and all others are 64 or more below; so the result is nearly the mean of the
+    shared ones' values, whatever the logits' size, and wrong if any step of the running reference is."""
+    H, heads, t = 2, 8, TYPES[dtype]
+    made = Made([1100, 700], H, D, seed=D, v_scale=0.5)
+    rng, scale = np.random.default_rng(D), 2.0 ** -3
+    sign = rng.choice([-1.0, 1.0], (1, 1, D))
+    # q . k = 8 logit for keys `a` of size and sign[:, :, :a] of the query's 32 sign
+    shared = {0: (5, 70, 300, 1040), 1: (0, 63, 64, 512)}
+    for b, n in enumerate(made.lens):
+        size = rng.integers(1, 40, n)                       # pages of many heights
+        size[100:164] = 100                                 # one that passes all before it
+        size[list(shared[b])] = 127
+        k = np.where(np.arange(D) < D // 2, size[:, None, None], 0) * sign
+        v = 0.5 * rng.standard_normal((n, H, D))
+        slots = made.table[b, np.arange(n) // 64] * 64 + np.arange(n) % 64
+        K8.append(made.data, made.exps, np.broadcast_to(k, (n, H, D)).astype(np.float16), v.astype(np.float16), slots,
+                  [[j, min(64 - j % 64, n - j)] for j in range(0, n, 64)])
+        blocks = K8.read_page(made.data[made.table[b, 0], 0], made.exps[made.table[b, 0], 0], D)[0]
+        assert np.array_equal(blocks, k[:64, 0])            # held exactly
+    cu = sums(rows)
+    factor = torch.tensor([1.0, 4.0, 8.0, 32.0] * 2)[:, None]
+    q = (torch.from_numpy(sign).float() * factor).expand(int(cu[-1]), heads, D).to(t).cuda()
+    lse = torch.empty(int(cu[-1]), heads, device="cuda")
+    cache = made.gpu()
+    for max_len in (1100, 1 << 20):
+        out = cache.attention(q, ints(made.table), ints(made.lens), ints(cu), max(rows), max_len, scale=scale, lse=lse)
+        ref, lse_ref, size, _ = K8.attention(made.data, made.exps, f32(q), made.table, made.lens, cu, scale)
+        # base-2 logits are rounded where they are scaled (twice) and taken against a reference that is
+        # rounded itself when it is set, moved and shifted: at most 8 times 2^-24 of them, 2^-21 of a logit in
+        # its weight's exponent.  All weights but the shared tokens' are below exp(-64)
+        logit = 127 * D // 2 * scale * host(factor)[:, 0]
+        assert (logit * 27 / 127 >= 64).all()
+        e = 2.0 ** -21 * logit[None, :, None] + 2.0 ** -18
+        tol = torch.finfo(t).eps / 2 * np.abs(ref) + 2 * e * (size + np.abs(ref)) + 2.0 ** -25
+        assert (np.abs(ref) > 2 * tol).any(-1).all()        # zeros would not pass
+        worst = float((np.abs(host(out) - ref) / tol).max())
+        say(f"  exact logits {D} {dtype} {rows} {max_len}: worst |err|/bound = {worst:.4f}")
+        assert worst <= 1
+        assert (np.abs(host(lse) - lse_ref) <= e[..., 0] + 2.0 ** -17 + 2.0 ** -22 * np.abs(lse_ref)).all()
+        for b in range(2):                                  # what the sequences' last rows see
+            want = np.mean([made_values(made, b, j) for j in shared[b]], 0)
+            assert np.abs(ref[cu[b + 1] - 1] - np.repeat(want, heads // H, 0)).max() < 1e-12
+
+
+def made_values(made, b, t):
+    """The values that a cached token stands for: [H, D]."""
+    p = made.table[b, t // 64]
+    return np.stack([K8.read_page(made.data[p, h], made.exps[p, h], made.D)[1][t % 64] for h in range(made.H)])
+
+
 def test_attention_blocks_of_very_different_sizes():
     """Values of 6e4 in some blocks and 1e-6 in others, zeros, and a strong token in a
     block of zeros: weights carry the blocks' exponents, and nothing overflows."""
