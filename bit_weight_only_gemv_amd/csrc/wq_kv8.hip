@@ -226,6 +226,7 @@ constexpr int kPick8Threads = 1024, kPick8Waves = kPick8Threads / kWave;
 constexpr int kPick8Bins = 2048;
 constexpr int kPick8Held = 16;         // masses a thread holds; those of longer sequences are read again,
 constexpr int kPick8Again = 8;         // so many at a time
+constexpr int kPick8Few = 4;           // masses a thread whose keys are made anew each time
 
 struct Evict8Args {
   const int32_t *table, *lens, *free_pages;
@@ -292,13 +293,16 @@ __global__ void none_taken_kernel(int32_t* taken) { taken[0] = 0; }
 // One workgroup a sequence for the tables, and one a (sequence, head) for the tokens:
 // the room-th highest key 11 bits at a time from histograms in LDS (four of them for
 // the first bits, which many masses share), then every wave a stretch of the tokens
-// with its place from the counts of the waves before it.  Masses stay in registers, in
-// tables of up to 16384 tokens all of them; LONG: of any length.
-// Latency: 11 us for 4500 tokens, 18 for 16000 (22 and more with a read of the kept
-// masses behind the choice); of 131072 tokens 16384 are chosen and moved in 195 us, 237
-// with the masses that are not held read one at a time.
-template <bool LONG>
+// with its place from the counts of the waves before it.  Masses stay in registers: in
+// tables of up to 16384 tokens all of them, and their keys too, unless the table has no more
+// than 4096 (4 x 16384 tokens take 42 us, 45 with keys made anew each time; 1000 take 16, 15).
+// LONG: of any length.
+// Latency, with the move: 4500 tokens 18 us; 16384 of 131072 172 us, 195 where a load waits
+// for the one before and 237 where masses that are not held are read one at a time.
+enum Pick8 { kPick8Short, kPick8Keys, kPick8Long };
+template <Pick8 HOW>
 __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
+  constexpr bool LONG = HOW == kPick8Long, KEYS = HOW == kPick8Keys;
   __shared__ uint32_t s_hist[6 * kPick8Bins];      // four of the first bits, one of the next each
   __shared__ uint32_t s_wave[kPick8Waves], s_count[kPick8Waves][2], s_found[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -335,12 +339,13 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   float held[kPick8Held];
 #pragma unroll
   for (int i = 0; i < kPick8Held; ++i) held[i] = load(i);
+  uint32_t keys[kPick8Held];
   // f(mass, its key, token) of the stretch's tokens, all lanes together (a token past
   // the last: old or more); those that are not held are read again, several at a time
   auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < kPick8Held; ++i)
-      if (i < turns) f(held[i], mass_key(held[i]), t0 + i * kWave);
+      if (i < turns) f(held[i], KEYS ? keys[i] : mass_key(held[i]), t0 + i * kWave);
     for (int i0 = kPick8Held; LONG && i0 < turns; i0 += kPick8Again) {
       float m[kPick8Again];
 #pragma unroll
@@ -352,6 +357,17 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
   };
   for (int i = tid; i < 6 * kPick8Bins; i += kPick8Threads) s_hist[i] = 0;
   __syncthreads();
+  if constexpr (KEYS) {
+#pragma unroll
+    for (int i = 0; i < kPick8Held; i += 4) {
+      if (i >= turns) break;
+#pragma unroll
+      for (int x = i; x < i + 4; ++x) {
+        keys[x] = mass_key(held[x]);
+        asm volatile("" : "+v"(keys[x]));        // kept, not made again
+      }
+    }
+  }
   uint32_t cut = 0, rank = (uint32_t)room;     // 0 < room < old
   int bits = 0;
   for (int pass = 0; pass < 3; ++pass) {
@@ -688,10 +704,13 @@ extern "C" int wq_kv8_evict(const wq_kv8_cache* cache, const float* mass, int64_
   p.pages = (int)pages;
   p.heads_by = Divisor(cache->n_kv_heads);
   const dim3 picks((unsigned)(n_seqs + pairs));
-  if (64 * table_width <= kPick8Held * kPick8Threads)
-    pick8_kernel<false><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
+  const int64_t most = 64 * table_width;
+  if (most <= kPick8Few * kPick8Threads)
+    pick8_kernel<kPick8Short><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
+  else if (most <= kPick8Held * kPick8Threads)
+    pick8_kernel<kPick8Keys><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
   else
-    pick8_kernel<true><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
+    pick8_kernel<kPick8Long><<<picks, kPick8Threads, 0, (hipStream_t)stream>>>(p);
   uint8_t* const exps = reinterpret_cast<uint8_t*>(cache->exponents);
   const dim3 grid((unsigned)(pairs * pages));
   const Divisor pairs_by(pairs);

@@ -693,6 +693,17 @@ def test_evict_of_long_sequences():
         check_evict(made, made.gpu(), mass, keep, 17, label="longer")
 
 
+@pytest.mark.parametrize("pages", [64, 65, 256, 257])
+def test_evict_at_the_borders_of_the_ways_to_choose(pages):
+    """Tables of 4096 and 16384 tokens and one page more, full and nearly empty ones; masses that many
+    tokens share."""
+    n = 64 * pages
+    made = Made([n, 130, n - 1], 1, 64, seed=pages, extra=2 * (n // 64), spread=0.1)
+    cache = made.gpu()
+    for ties in (True, False):
+        check_evict(made, cache, masses((3, 1, n), pages, ties=ties), 100 + n // 3, 50, label=f"{pages} pages, ties {ties}")
+
+
 def test_evict_moves_blocks_of_different_exponents():
     made = Made([256], 2, 64, seed=3, extra=9)
     rng = np.random.default_rng(1)
