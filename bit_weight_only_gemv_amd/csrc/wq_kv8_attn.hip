@@ -19,7 +19,9 @@
 // reference that follows logit + f both ways: a page whose largest weight would
 // pass 2^14 or stay below 2^2 sets it to that, where weights carry 2^10.  So 22
 // bits hold for what counts in a page, however small the page's share is, and most
-// pages are spared the cross-lane maximum and the rescale of the sums.  The
+// pages are spared the cross-lane maximum and the rescale of the sums.  (Both parts end
+// at 2^-24, 2^-26 of 2^2: tokens far below their page's largest weight have fewer bits, which
+// shows only where that one's values are nearly zero.)  The
 // reference stays within 2^64 of the highest and f within [-24, 10], so that FP32
 // holds the sums.
 //

@@ -388,6 +388,36 @@ def test_attention_flat_tail_behind_a_strong_token():
         check_attention(out, lse, tail, q, np.array([0, 1]), 0.1, label="flat tail")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("q", [0.5, 1.0, 1.5, 2.0, 2.5])
+def test_attention_beside_a_strong_token_without_values(dtype, q):
+    """One page, whose strong token has values of zero: what the others give is all there is.  Their
+    weights are off by a step of 2^-24, where the largest weight times 2^e of a row's first page stands at
+    2^10: by 2^-34 of that."""
+    D, n = 64, 64
+    made = Made([n], 1, D, seed=3)
+    rng = np.random.default_rng(1)
+    k, v = 0.05 * rng.standard_normal((n, 1, D)), 300.0 * rng.standard_normal((n, 1, D))
+    k[5], v[5] = 1.0, 0.0
+    K8.append(made.data, made.exps, k.astype(np.float16), v.astype(np.float16), made.table[0, 0] * 64 + np.arange(n), [[0, n]])
+    x = torch.full((1, 2, D), q, dtype=TYPES[dtype], device="cuda")
+    out = host(made.gpu().attention(x, ints(made.table), ints([n]), ints([0, 1]), 1, n, scale=0.125))[0]
+    keys, values = K8.read_page(made.data[made.table[0, 0], 0], made.exps[made.table[0, 0], 0], D)
+    z = 0.125 * q * keys.sum(-1)
+    p = np.exp(z - z.max())
+    p /= p.sum()
+    unit = np.repeat(2.0 ** made.exps[made.table[0, 0], 0, 4:].astype(float), 16)
+    ref, size = p @ values, p @ np.abs(values)
+    e = logit_error(D, 0.125 * q * np.abs(keys).sum(-1).max())
+    step = 2.0 ** -34 * (p * unit).max() * (np.abs(values) / unit[:, None]).sum(0)
+    tol = torch.finfo(TYPES[dtype]).eps / 2 * np.abs(ref) + (2 * e + 2.0 ** -17) * (size + np.abs(ref)) + step + \
+        (2.0 ** -25 if dtype == "f16" else 0)
+    assert (np.abs(ref) > 4 * tol).mean() > 0.3             # zeros would not pass
+    worst = float((np.abs(out - ref) / tol).max())
+    say(f"  beside a strong token, q {q}: p from {p.min():.1e}, worst |err|/bound = {worst:.4f}")
+    assert worst <= 1
+
+
 def test_attention_bf16_queries_of_any_size():
     made = Made([100], 1, 64, seed=2)
     for big in (1e30, 1e-30):
