@@ -39,8 +39,8 @@ __device__ __forceinline__ uint32_t raise4(uint32_t w, int by) {
 // Keys leave as 8 bytes a thread; values go through LDS, where a thread then gathers
 // 16 tokens of a channel.  Memory bounds prompts: 23145 tokens of 8 heads of 128
 // channels (142 MB) take 31 us, 28 as a plain copy of as many bytes.  Single tokens:
-// latency of run, slot, token and bytes in turn, with 256 of them 9.9 us in workgroups
-// of one wave and 11.4 in four.
+// latency of run, slot, token and bytes in turn, with 256 of them 8.9 us a call in
+// workgroups of one wave and 10.4 in four.
 constexpr int kAppend8Threads = 256, kAppend8Few = 64;
 
 // 16-bit values past +-65504 (BF16: 65536, whose code is the same) and infinities
@@ -439,9 +439,8 @@ __global__ void __launch_bounds__(kPick8Threads) pick8_kernel(Evict8Args p) {
 // bytes of a channel from there (the lanes of a wave the same tokens, 16 bytes
 // apart).  Memory bounds it: 12 sequences of 6001 to 16000 tokens, 6000 kept, 8 heads
 // of 128 channels read 350 MB (nearly every source line has a kept token, and a source
-// page at the border of two fresh ones is read twice) and write 180 in 108 us, 4.9 TB/s;
-// a plain copy reaches 5.2.  Stores that stay in the caches took 114 us; the gather in
-// LDS costs 3 us, and more workgroups a compute unit gain nothing.
+// page at the border of two fresh ones is read twice) and write 180 in 109 us, 4.9 TB/s;
+// a plain copy reaches 5.2.  Stores that stay in the caches cost 4 us more.
 constexpr int kMove8Threads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMove8Threads)

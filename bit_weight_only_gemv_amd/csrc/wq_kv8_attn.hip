@@ -29,12 +29,12 @@
 // bytes.  Four sequences of 131072 tokens, 8 heads of 128 channels, 1074 MB: 185 us,
 // 5.8 TB/s, where a plain read reaches 5.6; a page costs a wave 435 vector and 48
 // matrix instructions, at two waves a SIMD.  32 sequences of up to 8191 tokens, 361 MB:
-// 74 us, the last of it with few workgroups at work (the longest sequences' splits).
+// 73 us, the last of it with few workgroups at work (the longest sequences' splits).
 // Many rows: instructions of both kinds (617 vector and 96 matrix ones a page and wave
-// with two column tiles; without the remainders' products 91 us instead of 115, without
-// the conversions of codes 107, without the exponentials 104), and uneven sequences: 512
-// and fewer rows of two prompts over 6000 tokens take 107 us for 54 GFLOP.  Short caches:
-// latency, 7.6 us for 500 tokens.
+// with two column tiles) and uneven sequences: two prompts, 267 and 458 rows over 6000 and
+// 3967 tokens, take 105 us for 54 GFLOP.  Where it takes 110 (runs differ by that much), it
+// takes 96 without the remainders' products, 104 without the exponentials, and 110 without
+// the conversions of codes.  Short caches: latency, 7.7 us for 500 tokens.
 
 #include "wq_attn.cuh"
 #include "wq_common.cuh"
@@ -104,7 +104,7 @@ struct Keys8 {
 
 // The sequence of place n when they are ordered by length, longest first (of more than
 // 64 sequences: the n-th as they come).  Two prompts of 267 and 458 rows over 6000 and
-// 3967 tokens take 112 us so, and 133 with both side by side.
+// 3967 tokens take 110 us so, and 115 with both side by side.
 __device__ __forceinline__ int nth_longest(const KvRows& a, int n, int lane) {
   if (a.seqs < 2 || a.seqs > kWave) return n;
   const int len = lane < a.seqs ? a.lens[lane] : INT32_MIN;
@@ -445,9 +445,9 @@ static Attn8Plan attn8_plan(const wq_kv8_cache* c, const wq_kv4_rows* a, int64_t
   if (max_rows > a->n_rows) max_rows = a->n_rows;
   if (max_len > 64 * a->table_width) max_len = 64 * a->table_width;
   const int64_t cols = (max_rows < 1 ? 1 : max_rows) * R;
-  // Two column tiles share the codes' conversion where there are enough of them: a
-  // 512-token piece of two prompts over 6000 tokens takes 117 us with two, 174 with one,
-  // and 246 with four, whose registers spill.  Heads of 256 channels would not fit either.
+  // Two column tiles share the codes' conversion where there are enough of them: the same
+  // prompts take 110 us with two, 128 with one, and 384 with four, whose registers spill.
+  // Heads of 256 channels would not fit either.
   p.ct = c->head_dim <= 128 && cols >= 64 ? 2 : 1;
   p.tiles = (cols + 16 * p.ct - 1) / (16 * p.ct);
   p.pairs = a->n_seqs * c->n_kv_heads;
@@ -455,8 +455,10 @@ static Attn8Plan attn8_plan(const wq_kv8_cache* c, const wq_kv4_rows* a, int64_t
   if (pages < 1) pages = 1;
   // Two workgroups of 4 waves for every compute unit, as many as run at once (one with
   // heads of 256 channels): finer splits cost more in parts to be joined than they even
-  // out (32 sequences of up to 8191 tokens: 77 us, in one and a half to three rounds 80 to
-  // 86).  A split has at least two pages a wave, one while that leaves compute units idle.
+  // out (32 sequences of up to 8191 tokens: 78 us, in one and a half to three rounds 81 to
+  // 87).  A split has at least two pages a wave, one while that leaves compute units idle.
+  // All sequences have as many tiles and splits as the largest could need: a few rows beside
+  // a prompt's many, or tokens far fewer than max_len, leave compute units idle.
   const int64_t items = p.pairs * p.tiles, at_once = c->head_dim == 256 ? 256 : 512;
   int64_t splits = (at_once + items - 1) / items;
   const int64_t waves = items * ((pages + kAttnWaves - 1) / kAttnWaves) <= 256 ? kAttnWaves : 2 * kAttnWaves;

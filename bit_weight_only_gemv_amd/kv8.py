@@ -92,7 +92,8 @@ class KV8Cache:
         """Attention of q [rows, n_heads, D] over the cached tokens of its
         sequences (lens counts the rows' own), over the last `window` of each row
         if that is not 0.  lse float32 [rows, n_heads] receives the logarithm of the
-        softmax sums.  Rows behind the last of cu_rows are left as they are."""
+        softmax sums.  Rows behind the last of cu_rows are left as they are.  Decodes beside
+        a long piece of a prompt are faster in a call of their own."""
         lib = L.load()
         a = self._rows(q, block_table, lens, cu_rows)
         _same_device(self.data, q, block_table, lens, cu_rows)

@@ -538,7 +538,9 @@ int wq_kv8_append(const wq_kv8_cache* cache, int dtype, const uint16_t* k, int64
 
 /* Attention of the rows over the cache: wq_kv4_attention without a choice of pages.
  * A softmax weight enters its product times its block's 2^e: in 22 bits, or in steps of 2^-26 of
- * the largest such number of its page (2^-90 of the row's) where those are coarser.
+ * the largest such number of its page (2^-90 of the row's) where those are coarser.  What is said
+ * there of max_len and windows holds, and sequences of few rows beside one of many are faster in
+ * a call of their own.
  * cu_rows may end before n_rows here and below (a padded batch): the rows behind the
  * last sequence's take no part, and their out and lse stay as they are. */
 int64_t wq_kv8_attention_workspace(const wq_kv8_cache* cache, const wq_kv4_rows* rows,
